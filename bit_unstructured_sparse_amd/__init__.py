@@ -24,13 +24,15 @@ import numpy as np
 __all__ = ["load_library", "encode", "pack_int4", "Encoded", "DeviceMatrix", "spmm_w4a4", "spmm_f16",
            "select", "describe", "workspace_bytes", "BspError", "ALGO_AUTO", "ALGO_ROWWAVE", "ALGO_MFMA",
            "ALGO_SPLITK",
-           "INT4", "FP16", "PAYLOAD_ALIGN", "MAX_N", "library_path"]
+           "INT4", "FP16", "INT8", "PAYLOAD_ALIGN", "MAX_N", "library_path", "KVCache", "new_kv_cache", "kv_append",
+           "kv_gather", "attention_tree", "attention_workspace_bytes", "new_attention_workspace", "LoraAdapters",
+           "spmm_f16_lora", "spmm_w4a4_dq_lora", "lora_workspace_bytes", "new_lora_workspace"]
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 library_path = os.path.join(HERE, "libbitmap_spmm.so")
 
 OK, E_ARG, E_RANGE, E_CAPACITY, E_OVERFLOW, E_HIP, E_UNSUPPORTED = 0, 1, 2, 3, 4, 5, 6
-INT4, FP16, INT2 = 0, 1, 2
+INT4, FP16, INT2, INT8 = 0, 1, 2, 3      # INT8: a cache type only
 ALGO_AUTO, ALGO_ROWWAVE, ALGO_MFMA, ALGO_SPLITK = 0, 1, 2, 3
 PAYLOAD_ALIGN = 16
 MAX_N = 32
@@ -42,7 +44,9 @@ EXPORTS = ["encode_bitmap_tiles", "pack_int4_activations", "spmm_bitmap_w4a4", "
            "bsp_status_string", "bsp_version", "spmm_bitmap_f16_noalloc", "bsp_noalloc_scratch_bytes",
            "union_tile_count", "union_mask_words", "encode_union_tiles", "spmm_union_w4a4",
            "spmm_bitmap_w4a4_dq", "spmm_bitmap_w4a4_grouped", "spmm_bitmap_w2a4", "spmm_bitmap_w2a4_algo",
-           "cbc_gtile_count", "encode_cbc_f16", "spmspv_cbc_workspace_bytes", "spmspv_cbc_f16"]
+           "cbc_gtile_count", "encode_cbc_f16", "spmspv_cbc_workspace_bytes", "spmspv_cbc_f16",
+           "kv_cache_append", "kv_cache_gather", "attention_tree_workspace_bytes", "attention_tree_f16",
+           "lora_workspace_bytes", "spmm_bitmap_f16_lora", "spmm_bitmap_w4a4_dq_lora"]
 
 
 class BspError(RuntimeError):
@@ -111,6 +115,18 @@ def load_library():
         L.spmspv_cbc_workspace_bytes.argtypes, L.spmspv_cbc_workspace_bytes.restype = [I64, I64, I64, P], I32
         L.spmspv_cbc_f16.argtypes = [P, P, P, P, I64, I64, I64, P, I64, ctypes.c_float, P, P, I64, P]
         L.spmspv_cbc_f16.restype = I32
+        F32 = ctypes.c_float
+        L.kv_cache_append.argtypes, L.kv_cache_append.restype = [P, P, I64, P, I64, P, I64, P], I32
+        L.kv_cache_gather.argtypes, L.kv_cache_gather.restype = [P, P, I64, P, I64, P, I64, P], I32
+        L.attention_tree_workspace_bytes.argtypes = [P, I64, I64, I64, I64, P]
+        L.attention_tree_workspace_bytes.restype = I32
+        L.attention_tree_f16.argtypes = [P, I64, P, P, I64, P, P, I64, I64, I64, I64, P, F32, P, I64, P, I64, P]
+        L.attention_tree_f16.restype = I32
+        L.lora_workspace_bytes.argtypes, L.lora_workspace_bytes.restype = [I32, I64, I64, I64, I64, I64, P], I32
+        L.spmm_bitmap_f16_lora.argtypes = [P, P, P, I64, I64, I64, P, I64, P, P, P, I64, P]
+        L.spmm_bitmap_f16_lora.restype = I32
+        L.spmm_bitmap_w4a4_dq_lora.argtypes = [P, P, P, I64, I64, I64, P, P, I64, P, P, P, P, P, I64, P]
+        L.spmm_bitmap_w4a4_dq_lora.restype = I32
         _lib = L
     return _lib
 
@@ -619,3 +635,328 @@ def new_workspace(dtype: int, M: int, K: int, N: int, nnz: int = -1, device="cud
     if n == 0:
         return None
     return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+# ---- paged key/value cache, quantised as it is written ----
+
+TREE_MAX = 64
+
+
+class _KVCacheDesc(ctypes.Structure):
+    """bsp_kv_cache of include/bitmap_spmm.h."""
+    _fields_ = [("dtype", ctypes.c_int), ("num_pages", ctypes.c_int64), ("kv_heads", ctypes.c_int64),
+                ("page_size", ctypes.c_int64), ("head_dim", ctypes.c_int64), ("k", ctypes.c_void_p),
+                ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p)]
+
+
+@dataclass
+class KVCache:
+    """Paged cache tensors: k, v [pages][kv_heads][page_size][row] (float16
+    [head_dim] for FP16, uint8 [head_dim] for INT8, uint8 [head_dim / 2] for
+    INT4) and, for the quantised kinds, k_scale, v_scale int32
+    [pages][kv_heads][page_size] (step as bfloat16 in the high half, offset as
+    float16 in the low half)."""
+    dtype: int
+    k: "object"
+    v: "object"
+    k_scale: "object" = None
+    v_scale: "object" = None
+
+    def __post_init__(self):
+        import torch
+        if self.dtype not in (FP16, INT8, INT4):
+            raise ValueError("a cache is FP16, INT8 or INT4")
+        if self.k.dim() != 4 or self.v.shape != self.k.shape:
+            raise ValueError("k and v must be [pages][kv_heads][page_size][row] of one shape")
+        for n in ("k", "v"):
+            _check_dev(getattr(self, n), n, torch.float16 if self.dtype == FP16 else torch.uint8)
+        for n in ("k_scale", "v_scale"):
+            w = getattr(self, n)
+            if self.dtype == FP16:
+                if w is not None:
+                    raise ValueError("an FP16 cache has no scale words")
+            else:
+                _check_dev(w, n, torch.int32)
+                if w.shape != self.k.shape[:3]:
+                    raise ValueError(f"{n} must be [pages][kv_heads][page_size]")
+        if len({t.device for t in (self.k, self.v, self.k_scale, self.v_scale) if t is not None}) != 1:
+            raise ValueError("the cache's tensors must lie on one device")
+
+    @property
+    def num_pages(self) -> int:
+        return int(self.k.shape[0])
+
+    @property
+    def kv_heads(self) -> int:
+        return int(self.k.shape[1])
+
+    @property
+    def page_size(self) -> int:
+        return int(self.k.shape[2])
+
+    @property
+    def head_dim(self) -> int:
+        return int(self.k.shape[3]) * (2 if self.dtype == INT4 else 1)
+
+    def _desc(self) -> _KVCacheDesc:
+        return _KVCacheDesc(self.dtype, self.num_pages, self.kv_heads, self.page_size, self.head_dim, _dptr(self.k),
+                            _dptr(self.v), _dptr(self.k_scale), _dptr(self.v_scale))
+
+
+def new_kv_cache(dtype: int, num_pages: int, kv_heads: int, page_size: int, head_dim: int, device="cuda") -> KVCache:
+    """A cache of num_pages empty (zero) pages."""
+    import torch
+    if dtype not in (FP16, INT8, INT4):
+        raise ValueError("a cache is FP16, INT8 or INT4")
+    shape = (num_pages, kv_heads, page_size)
+    row = head_dim // 2 if dtype == INT4 else head_dim
+
+    def codes():
+        return torch.zeros(shape + (row,), dtype=torch.float16 if dtype == FP16 else torch.uint8, device=device)
+
+    def words():
+        return None if dtype == FP16 else torch.zeros(shape, dtype=torch.int32, device=device)
+
+    return KVCache(dtype, codes(), codes(), words(), words())
+
+
+def _check_rows(t, name, heads, dim, device):
+    """A float16 [n][heads][dim] tensor whose rows may be strided by token."""
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA (HIP) tensor")
+    if t.dtype != torch.float16:
+        raise TypeError(f"{name} must be torch.float16, got {t.dtype}")
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
+        raise ValueError(f"{name} must be [tokens][{heads}][{dim}], got {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}")
+    if t.numel() and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim)):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    if t.shape[0] > 1 and t.stride(0) < heads * dim:
+        raise ValueError(f"{name}: tokens overlap")
+
+
+def _row_stride(t) -> int:
+    return int(t.stride(0)) if t.shape[0] > 1 else int(t.shape[1] * t.shape[2])
+
+
+def _check_ints(t, name, dtype, numel, device):
+    _check_dev(t, name, dtype, numel)
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}")
+
+
+def kv_append(cache: KVCache, K, V, slots, stream=None) -> None:
+    """Quantise the rows K, V (float16 [n][kv_heads][head_dim], a token's heads
+    contiguous) into cache slots (int64 [n], page * page_size + offset; a slot
+    outside the cache is skipped)."""
+    import torch
+    dev = cache.k.device
+    for t, name in ((K, "K"), (V, "V")):
+        _check_rows(t, name, cache.kv_heads, cache.head_dim, dev)
+    n = int(K.shape[0])
+    if V.shape[0] != n:
+        raise ValueError("K and V must hold the same tokens")
+    _check_ints(slots, "slots", torch.int64, n, dev)
+    d = cache._desc()
+    rc = load_library().kv_cache_append(ctypes.byref(d), _dptr(K), _row_stride(K), _dptr(V), _row_stride(V),
+                                        _dptr(slots), n, _stream_handle(stream))
+    _check(rc, "kv_cache_append")
+
+
+def kv_gather(cache: KVCache, slots, K=None, V=None, stream=None):
+    """The rows of the slots (int64 [n]) as float16 K, V [n][kv_heads][head_dim]
+    (zeros for a slot outside the cache)."""
+    import torch
+    dev = cache.k.device
+    n = int(slots.numel())
+    _check_ints(slots, "slots", torch.int64, n, dev)
+    shape = (n, cache.kv_heads, cache.head_dim)
+    K = torch.empty(shape, dtype=torch.float16, device=dev) if K is None else K
+    V = torch.empty(shape, dtype=torch.float16, device=dev) if V is None else V
+    for t, name in ((K, "K"), (V, "V")):
+        _check_rows(t, name, cache.kv_heads, cache.head_dim, dev)
+        if t.shape[0] != n:
+            raise ValueError(f"{name} must hold {n} tokens")
+    d = cache._desc()
+    rc = load_library().kv_cache_gather(ctypes.byref(d), _dptr(slots), n, _dptr(K), _row_stride(K), _dptr(V),
+                                        _row_stride(V), _stream_handle(stream))
+    _check(rc, "kv_cache_gather")
+    return K, V
+
+
+# ---- attention of drafted token trees over the cache ----
+
+def attention_workspace_bytes(cache: KVCache, B: int, max_q: int, q_heads: int, table_width: int) -> int:
+    """Bytes of workspace attention_tree uses to split the cached tokens."""
+    out = ctypes.c_int64(0)
+    d = cache._desc()
+    _check(load_library().attention_tree_workspace_bytes(ctypes.byref(d), table_width, B, max_q, q_heads,
+                                                         ctypes.byref(out)), "attention_tree_workspace_bytes")
+    return int(out.value)
+
+
+def new_attention_workspace(cache: KVCache, B: int, max_q: int, q_heads: int, table_width: int, device="cuda"):
+    """A zero-filled workspace for attention_tree (None if none is used)."""
+    import torch
+    n = attention_workspace_bytes(cache, B, max_q, q_heads, table_width)
+    return torch.zeros(n, dtype=torch.uint8, device=device) if n else None
+
+
+def attention_tree(Q, cache: KVCache, block_table, kv_lens, q_start, max_q: int, tree_mask=None, scale=None, O=None,
+                   workspace=None, stream=None):
+    """float16 O [rows][q_heads][head_dim]: attention of each sequence's drafted
+    tokens over its cached tokens. Q: float16 [rows][q_heads][head_dim];
+    block_table: int32 [B][width]; kv_lens: int32 [B], cached tokens, the drafted
+    ones last; q_start: int32 [B + 1], the rows of sequence b are q_start[b] up to
+    q_start[b + 1] (at most max_q <= TREE_MAX of them); tree_mask: int64 [rows],
+    bit j of row i's word: drafted token j is seen (None: a chain); scale: default
+    head_dim ** -0.5. workspace: new_attention_workspace(...), or None for no
+    split over the cached tokens."""
+    import torch
+    dev = cache.k.device
+    if Q.dim() != 3:
+        raise ValueError("Q must be [rows][q_heads][head_dim]")
+    hq = int(Q.shape[1])
+    _check_rows(Q, "Q", hq, cache.head_dim, dev)
+    rows = int(Q.shape[0])
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [B][width]")
+    B, width = int(block_table.shape[0]), int(block_table.shape[1])
+    _check_ints(block_table, "block_table", torch.int32, B * width, dev)
+    _check_ints(kv_lens, "kv_lens", torch.int32, B, dev)
+    _check_ints(q_start, "q_start", torch.int32, B + 1, dev)
+    if tree_mask is not None:
+        _check_ints(tree_mask, "tree_mask", torch.int64, rows, dev)
+    if O is None:
+        O = torch.empty((rows, hq, cache.head_dim), dtype=torch.float16, device=dev)
+    _check_rows(O, "O", hq, cache.head_dim, dev)
+    if O.shape[0] != rows:
+        raise ValueError(f"O must hold {rows} rows")
+    wp, wb = _ws_args(workspace)
+    d = cache._desc()
+    rc = load_library().attention_tree_f16(
+        _dptr(Q), _row_stride(Q), ctypes.byref(d), _dptr(block_table), width, _dptr(kv_lens), _dptr(q_start), B, rows,
+        max_q, hq, _dptr(tree_mask), cache.head_dim ** -0.5 if scale is None else scale, _dptr(O), _row_stride(O),
+        wp, wb, _stream_handle(stream))
+    _check(rc, "attention_tree_f16")
+    return O
+
+
+# ---- low-rank adapters beside a shared projection ----
+
+class _LoraDesc(ctypes.Structure):
+    """bsp_lora of include/bitmap_spmm.h."""
+    _fields_ = [("adapters", ctypes.c_int64), ("rank", ctypes.c_int64), ("A", ctypes.c_void_p),
+                ("B", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("ranks", ctypes.c_void_p),
+                ("index", ctypes.c_void_p)]
+
+
+@dataclass
+class LoraAdapters:
+    """The adapters of one projection: A float16 [adapters][R][K], B float16
+    [adapters][M][R] (R a multiple of 8, at most 256); scale float32 [adapters]
+    (None: 1); rank int32 [adapters], the rows of A in use (None: R)."""
+    A: "object"
+    B: "object"
+    scale: "object" = None
+    rank: "object" = None
+
+    def __post_init__(self):
+        import torch
+        if self.A.dim() != 3 or self.B.dim() != 3 or self.A.shape[0] != self.B.shape[0] or \
+                self.A.shape[1] != self.B.shape[2]:
+            raise ValueError("A must be [adapters][R][K] and B [adapters][M][R]")
+        dev = self.A.device
+        _check_dev(self.A, "A", torch.float16)
+        _check_ints(self.B, "B", torch.float16, self.B.numel(), dev)
+        if self.scale is not None:
+            _check_ints(self.scale, "scale", torch.float32, self.adapters, dev)
+        if self.rank is not None:
+            _check_ints(self.rank, "rank", torch.int32, self.adapters, dev)
+
+    @property
+    def adapters(self) -> int:
+        return int(self.A.shape[0])
+
+    @property
+    def R(self) -> int:
+        return int(self.A.shape[1])
+
+    def _desc(self, M, K, index, N) -> _LoraDesc:
+        import torch
+        if self.A.shape[2] != K or self.B.shape[1] != M:
+            raise ValueError(f"the adapters are for a {self.B.shape[1]} x {self.A.shape[2]} projection, not {M} x {K}")
+        _check_ints(index, "index", torch.int32, N, self.A.device)
+        return _LoraDesc(self.adapters, self.R, _dptr(self.A), _dptr(self.B), _dptr(self.scale), _dptr(self.rank),
+                         _dptr(index))
+
+
+def lora_workspace_bytes(dtype: int, M: int, K: int, N: int, rank: int, nnz: int = -1) -> int:
+    """Bytes of workspace the adapter entry points need."""
+    out = ctypes.c_int64(0)
+    _check(load_library().lora_workspace_bytes(dtype, M, K, N, nnz, rank, ctypes.byref(out)), "lora_workspace_bytes")
+    return int(out.value)
+
+
+def new_lora_workspace(W: DeviceMatrix, N: int, adapters: LoraAdapters, device="cuda"):
+    """A zero-filled workspace for the adapter entry points (None if empty)."""
+    import torch
+    n = lora_workspace_bytes(W.dtype, W.M, W.K, N, adapters.R, W.nnz)
+    return torch.zeros(n, dtype=torch.uint8, device=device) if n else None
+
+
+def spmm_f16_lora(W: DeviceMatrix, X, adapters: LoraAdapters, index, Y=None, workspace=None, stream=None):
+    """fp16 Y [N][M] = W x_n + scale[a] B_a (A_a x_n), a = index[n] (int32 [N];
+    negative: no adapter). X: float16 [N][K]. workspace: new_lora_workspace(...)
+    (one is made for the call when not given)."""
+    import torch
+    if W.dtype != FP16:
+        raise TypeError("spmm_f16_lora needs an fp16 DeviceMatrix")
+    if X.dim() != 2 or X.shape[1] != W.K:
+        raise ValueError("X must be [N][K]")
+    N = int(X.shape[0])
+    _check_dev(X, "X", torch.float16)
+    d = adapters._desc(W.M, W.K, index, N)
+    if Y is None:
+        Y = torch.empty((N, W.M), dtype=torch.float16, device=X.device)
+    _check_dev(Y, "Y", torch.float16, N * W.M)
+    if workspace is None:
+        workspace = new_lora_workspace(W, N, adapters, device=X.device)
+    wp, wb = _ws_args(workspace)
+    rc = load_library().spmm_bitmap_f16_lora(
+        _dptr(W.bitmaps), _dptr(W.offsets), _dptr(W.payload), W.payload.numel(), W.M, W.K, _dptr(X), N,
+        ctypes.byref(d), _dptr(Y), wp, wb, _stream_handle(stream))
+    _check(rc, "spmm_bitmap_f16_lora")
+    return Y
+
+
+def spmm_w4a4_dq_lora(W: DeviceMatrix, X, X16, scale_w, scale_x, adapters: LoraAdapters, index, Yh=None,
+                      workspace=None, stream=None):
+    """fp16 Yh [N][M] = (W x_n) * scale_w[m] * scale_x[n] + scale[a] B_a (A_a
+    x16_n): the dequantised int4 product of spmm_bitmap_w4a4_dq with adapters on
+    the float16 activations. X: uint8 [N][ceil(K/2)] packed int4; X16: float16
+    [N][K]."""
+    import torch
+    if W.dtype != INT4:
+        raise TypeError("spmm_w4a4_dq_lora needs an int4 DeviceMatrix")
+    if X16.dim() != 2 or X16.shape[1] != W.K:
+        raise ValueError("X16 must be [N][K]")
+    N = int(X16.shape[0])
+    _check_dev(X16, "X16", torch.float16)
+    _check_dev(X, "X", torch.uint8, N * ((W.K + 1) // 2))
+    _check_dev(scale_w, "scale_w", torch.float32, W.M)
+    _check_dev(scale_x, "scale_x", torch.float32, N)
+    d = adapters._desc(W.M, W.K, index, N)
+    if Yh is None:
+        Yh = torch.empty((N, W.M), dtype=torch.float16, device=X16.device)
+    _check_dev(Yh, "Yh", torch.float16, N * W.M)
+    if workspace is None:
+        workspace = new_lora_workspace(W, N, adapters, device=X16.device)
+    wp, wb = _ws_args(workspace)
+    rc = load_library().spmm_bitmap_w4a4_dq_lora(
+        _dptr(W.bitmaps), _dptr(W.offsets), _dptr(W.payload), W.payload.numel(), W.M, W.K, _dptr(X), _dptr(X16), N,
+        _dptr(scale_w), _dptr(scale_x), ctypes.byref(d), _dptr(Yh), wp, wb, _stream_handle(stream))
+    _check(rc, "spmm_bitmap_w4a4_dq_lora")
+    return Yh

@@ -5,7 +5,7 @@ in this directory with hipcc for gfx950.
 
 One shared library holds the host encoders (encode.cpp, encode_union.cpp,
 encode_cbc.cpp) and every HIP kernel
-(spmm.hip with its kernels_*.hip includes). The probe (probe_read.hip) is a
+(spmm.hip with its kernels_*.hip includes, kv_cache.hip, attention_tree.hip). The probe (probe_read.hip) is a
 measurement aid the benchmark loads; the SpMM library does not contain it.
 Packed-fp32 VALU forms are switched off for the device pass; hipcc's host
 pass warns that it does not know that feature, which is harmless.
@@ -25,7 +25,8 @@ HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 
 SOURCES = [os.path.join(CSRC, "spmm.hip"), os.path.join(CSRC, "encode.cpp"), os.path.join(CSRC, "encode_union.cpp"),
-           os.path.join(CSRC, "encode_cbc.cpp")]
+           os.path.join(CSRC, "encode_cbc.cpp"), os.path.join(CSRC, "kv_cache.hip"),
+           os.path.join(CSRC, "attention_tree.hip")]
 PROBE_SOURCES = [os.path.join(CSRC, "probe_read.hip")]
 
 

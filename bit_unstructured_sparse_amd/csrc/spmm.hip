@@ -23,6 +23,7 @@
 #include "kernels_splitk.hip"
 #include "kernels_union.hip"
 #include "kernels_cbc.hip"
+#include "kernels_lora.hip"
 
 namespace {
 
@@ -709,5 +710,96 @@ extern "C" int spmspv_cbc_f16(const uint32_t *tile_offsets, const uint32_t *coli
     else
         CBC_LAUNCH(CBC_NMAX);
 #undef CBC_LAUNCH
+    return launch_status();
+}
+
+// ---------------------------------------------------------------------------
+// Low-rank adapters beside a shared projection.
+namespace {
+
+int64_t lora_t_bytes(int64_t N, int64_t R) { return (N * R * 4 + 255) / 256 * 256; }
+
+// Where t_n lies in the workspace: past the arrival counters and the partial
+// sums the projection's plan may use.
+int64_t lora_t_offset(int64_t plan_bytes) { return std::max(plan_bytes, sk_ws_counters_bytes()); }
+
+int lora_check(const bsp_lora *l, int64_t M, int64_t K, int64_t N, const void *X16, const void *workspace,
+               int64_t workspace_bytes) {
+    if (l == nullptr || l->adapters < 0 || l->rank < 8 || l->rank > 256 || l->rank % 8 != 0) return BSP_E_ARG;
+    if (l->adapters > INT32_MAX) return BSP_E_OVERFLOW;
+    if (workspace_bytes < 0 || (workspace == nullptr && workspace_bytes != 0)) return BSP_E_ARG;
+    if (((uintptr_t)workspace & 255u) != 0) return BSP_E_ARG;
+    if (M == 0 || N == 0) return BSP_OK;
+    if (l->index == nullptr) return BSP_E_ARG;
+    if (l->adapters > 0 && (l->B == nullptr || (K > 0 && (l->A == nullptr || X16 == nullptr)))) return BSP_E_ARG;
+    if ((((uintptr_t)l->A | (uintptr_t)l->B) & 15u) != 0) return BSP_E_ARG;
+    return BSP_OK;
+}
+
+LoraArgs lora_args(const bsp_lora *l, void *t) {
+    return LoraArgs{l->A, l->B, l->scale, l->ranks, l->index, (float *)t, (int)l->adapters, (int)l->rank};
+}
+
+void launch_lora_down(const LoraArgs &a, const uint16_t *X, int64_t N, int64_t K, hipStream_t stream) {
+    hipLaunchKernelGGL(k_lora_down, dim3((unsigned)((N * a.R + 3) / 4)), dim3(256), 0, stream, a, X, (int)N, (int)K);
+}
+
+void launch_lora_up(const LoraArgs &a, int64_t M, int64_t N, uint16_t *Y, hipStream_t stream) {
+    hipLaunchKernelGGL(k_lora_up, dim3((unsigned)((M + 255) / 256), (unsigned)N), dim3(256), 0, stream, a, (int)M, Y);
+}
+
+}  // namespace
+
+extern "C" int lora_workspace_bytes(int dtype, int64_t M, int64_t K, int64_t N, int64_t nnz, int64_t rank,
+                                    int64_t *bytes) {
+    if (rank < 8 || rank > 256 || rank % 8 != 0) return BSP_E_ARG;
+    int64_t plan = 0;
+    const int rc = bsp_workspace_bytes(dtype, M, K, N, nnz, &plan);
+    if (rc != BSP_OK) return rc;
+    if (bytes == nullptr) return BSP_E_ARG;
+    *bytes = M == 0 || N == 0 ? 0 : lora_t_offset(dtype == BSP_FP16 ? plan : 0) + lora_t_bytes(N, rank);
+    return BSP_OK;
+}
+
+extern "C" int spmm_bitmap_f16_lora(const uint64_t *bitmaps, const uint32_t *offsets, const uint16_t *payload,
+                                    int64_t payload_bytes, int64_t M, int64_t K, const uint16_t *X, int64_t N,
+                                    const bsp_lora *lora, uint16_t *Y, void *workspace, int64_t workspace_bytes,
+                                    hipStream_t stream) {
+    Shape s;
+    int rc = check_args(bitmaps, offsets, payload, payload_bytes, M, K, X, N, Y, BSP_ALGO_AUTO, &s);
+    if (rc != BSP_OK) return rc;
+    rc = lora_check(lora, M, K, N, X, workspace, workspace_bytes);
+    if (rc != BSP_OK || M == 0 || N == 0) return rc;
+    Plan p;
+    rc = choose_plan(BSP_FP16, s, payload_bytes, BSP_ALGO_AUTO, true, &p);
+    if (rc != BSP_OK) return rc;
+    const int64_t at = lora_t_offset(p.ws_bytes());
+    if (workspace == nullptr || workspace_bytes < at + lora_t_bytes(N, lora->rank)) return BSP_E_CAPACITY;
+    const LoraArgs a = lora_args(lora, (uint8_t *)workspace + at);
+    launch_lora_down(a, X, N, K, stream);
+    rc = spmm_common(BSP_FP16, bitmaps, offsets, payload, payload_bytes, M, K, X, N, Y, workspace, at, BSP_ALGO_AUTO,
+                     stream);
+    if (rc != BSP_OK) return rc;
+    launch_lora_up(a, M, N, Y, stream);
+    return launch_status();
+}
+
+extern "C" int spmm_bitmap_w4a4_dq_lora(const uint64_t *bitmaps, const uint32_t *offsets, const uint8_t *payload,
+                                        int64_t payload_bytes, int64_t M, int64_t K, const uint8_t *X,
+                                        const uint16_t *X16, int64_t N, const float *scale_w, const float *scale_x,
+                                        const bsp_lora *lora, uint16_t *Yh, void *workspace, int64_t workspace_bytes,
+                                        hipStream_t stream) {
+    Shape s;
+    int rc = check_args(bitmaps, offsets, payload, payload_bytes, M, K, X, N, Yh, BSP_ALGO_AUTO, &s);
+    if (rc != BSP_OK) return rc;
+    rc = lora_check(lora, M, K, N, X16, workspace, workspace_bytes);
+    if (rc != BSP_OK || M == 0 || N == 0) return rc;
+    const int64_t at = lora_t_offset(0);
+    if (workspace == nullptr || workspace_bytes < at + lora_t_bytes(N, lora->rank)) return BSP_E_CAPACITY;
+    const LoraArgs a = lora_args(lora, (uint8_t *)workspace + at);
+    rc = spmm_bitmap_w4a4_dq(bitmaps, offsets, payload, payload_bytes, M, K, X, N, scale_w, scale_x, Yh, stream);
+    if (rc != BSP_OK) return rc;
+    launch_lora_down(a, X16, N, K, stream);
+    launch_lora_up(a, M, N, Yh, stream);
     return launch_status();
 }

@@ -67,7 +67,8 @@ typedef enum bsp_status {
     BSP_E_UNSUPPORTED = 6 /* a kernel forced through an *_algo entry point cannot run this shape */
 } bsp_status;
 
-typedef enum bsp_dtype { BSP_INT4 = 0, BSP_FP16 = 1, BSP_INT2 = 2 } bsp_dtype;
+/* BSP_INT8 is a cache type only (bsp_kv_cache); BSP_INT2 a weight type only. */
+typedef enum bsp_dtype { BSP_INT4 = 0, BSP_FP16 = 1, BSP_INT2 = 2, BSP_INT8 = 3 } bsp_dtype;
 
 /* Kernel choice for the *_algo entry points. BSP_ALGO_AUTO applies the
  * library's shape-aware selection (by N, density, M, K). A forced choice
@@ -466,6 +467,160 @@ int spmspv_cbc_f16(const uint32_t *tile_offsets, const uint32_t *colinfo, const 
                    const uint16_t *values, int64_t values_bytes, int64_t M, int64_t K, const uint16_t *X,
                    int64_t N, float threshold, uint16_t *Y, void *workspace, int64_t workspace_bytes,
                    hipStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Paged key/value cache, quantised as it is written.
+ *   A cache holds the K and V rows (one per token and kv head, head_dim
+ *   channels) of many sequences in pages of page_size token slots. Slot
+ *   page * page_size + offset is token `offset` of page `page`; which pages a
+ *   sequence owns is the caller's block table.
+ *   k, v         [num_pages][kv_heads][page_size][row], a row being head_dim fp16
+ *                values (BSP_FP16), head_dim code bytes (BSP_INT8) or head_dim / 2
+ *                bytes (BSP_INT4: two codes per byte, low nibble = even channel).
+ *   k_scale, v_scale   uint32 [num_pages][kv_heads][page_size], one word per
+ *                row: the step s as bfloat16 in the high half, the offset o as
+ *                fp16 in the low half (NULL for BSP_FP16). The row stands for
+ *                s * u + o, u its unsigned codes (0..255 or 0..15).
+ *   Quantising a row x (fp16, as given):
+ *                o = min x;  s = fp32((max x - o) / L) rounded up to bfloat16,
+ *                L = 255 or 15;  u = round-half-even((x - o) / s), at most L
+ *                (u = 0 where s = 0). A row holding an infinity or a NaN gets
+ *                s = o = NaN and codes 0: it reads back as NaN.
+ *   s is rounded up so that L steps reach the maximum; the error of a value is
+ *   at most s / 2, plus its rounding to fp16 where it is read back.
+ * --------------------------------------------------------------------------- */
+typedef struct bsp_kv_cache {
+    int dtype;              /* BSP_FP16, BSP_INT8 or BSP_INT4 */
+    int64_t num_pages;      /* num_pages * page_size < 2^31 */
+    int64_t kv_heads;
+    int64_t page_size;      /* a power of two, 16 .. 4096 */
+    int64_t head_dim;       /* 64, 128 or 256 (BSP_E_UNSUPPORTED otherwise) */
+    void *k, *v;            /* DEVICE, 16-byte aligned */
+    uint32_t *k_scale, *v_scale;   /* DEVICE, 16-byte aligned; NULL for BSP_FP16 */
+} bsp_kv_cache;
+
+/*
+ * kv_cache_append -- quantise n tokens' K and V rows into their slots, on `stream`.
+ *   cache     HOST descriptor (read during the call only).
+ *   K, V      DEVICE fp16 [n][kv_heads][head_dim], token t starting at element
+ *             t * k_stride (v_stride): a slice of a fused QKV projection's
+ *             output will do. Strides >= kv_heads * head_dim.
+ *   slots     DEVICE int64 [n]. A slot outside [0, num_pages * page_size) is
+ *             skipped; two tokens of one call must not share a slot.
+ * n == 0 or kv_heads == 0 launches nothing.
+ */
+int kv_cache_append(const bsp_kv_cache *cache, const uint16_t *K, int64_t k_stride, const uint16_t *V,
+                    int64_t v_stride, const int64_t *slots, int64_t n, hipStream_t stream);
+
+/*
+ * kv_cache_gather -- the K and V rows of n slots as fp16 (the sum s * u + o in
+ * fp32, at most 65504, one round to nearest even), [n][kv_heads][head_dim] with token strides
+ * as above. A slot outside the cache gives zeros. The same slot may repeat.
+ */
+int kv_cache_gather(const bsp_kv_cache *cache, const int64_t *slots, int64_t n, uint16_t *K, int64_t k_stride,
+                    uint16_t *V, int64_t v_stride, hipStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Attention of drafted token trees over the paged cache (decode: one token per
+ * sequence is a tree of one).
+ *   Sequence b has kv_lens[b] tokens in the cache, the last T_b of them this
+ *   step's drafted tokens (appended before the call); their queries are rows
+ *   q_start[b] .. q_start[b+1]-1 of Q, T_b = q_start[b+1] - q_start[b].
+ *   Drafted token i sees every token before the drafted ones, and drafted token
+ *   j iff bit j of tree_mask[q_start[b] + i] is set (its ancestors and itself);
+ *   without a mask, j <= i (a chain).
+ *   O[row][h] = sum_j softmax_j(scale * Q[row][h] . k_j) v_j over the visible
+ *   tokens j, k_j and v_j the rows of kv head h / (q_heads / kv_heads) as the
+ *   cache stands for them. A row that sees no token gives zeros. What lies in
+ *   the cache at tokens a row does not see, NaN included, has no effect on it;
+ *   in an fp16 cache a channel of a seen drafted token's v that is infinite or
+ *   NaN gives NaN in that channel.
+ * Scores, softmax statistics and sums are fp32, the exponentials enter the
+ * second product as fp16 (their scale chosen so that they stay normal numbers
+ * down to 2^-20 of the largest), one rounding to fp16 at the end. Partial sums
+ * are joined in a fixed order: results do not depend on timing.
+ * --------------------------------------------------------------------------- */
+
+/* Most drafted tokens of a sequence in one call (bits of a mask word). */
+#define BSP_TREE_MAX 64
+
+/*
+ * attention_tree_workspace_bytes -- bytes of workspace attention_tree_f16 uses
+ * to split the cached tokens over workgroups; table_width as in the call. Host
+ * only. 0 when B, max_q, q_heads or kv_heads is 0.
+ */
+int attention_tree_workspace_bytes(const bsp_kv_cache *cache, int64_t table_width, int64_t B, int64_t max_q,
+                                   int64_t q_heads, int64_t *bytes);
+
+/*
+ * attention_tree_f16 -- the attention above, asynchronous on `stream`.
+ *   Q            DEVICE fp16, token row r at element r * q_stride, [q_heads][head_dim] there.
+ *   cache        HOST descriptor (read during the call only).
+ *   block_table  DEVICE int32 [B][table_width]: page of tokens p * page_size ...
+ *                of sequence b at [b][p]. Entries outside the cache are read as page 0.
+ *   kv_lens      DEVICE int32 [B], at most table_width * page_size (clamped to it).
+ *   q_start      DEVICE int32 [B+1], non-decreasing, q_start[B] <= total_q. Rows
+ *                of Q no sequence owns leave O as it is.
+ *   max_q        most drafted tokens of a sequence, 0..BSP_TREE_MAX; rows past it are
+ *                not computed.
+ *   tree_mask    DEVICE uint64 [total_q], or NULL for chains.
+ *   scale        finite.
+ *   O            DEVICE fp16, token row r at element r * o_stride. Must not overlap Q.
+ *   workspace    DEVICE, NULL (one workgroup walks all of a sequence) or
+ *                attention_tree_workspace_bytes() bytes, 256-byte aligned, zero-filled
+ *                before its first use (its first 64 KiB hold arrival counters, left zero by
+ *                every call: a workspace of the other entry points will do). Too
+ *                small: BSP_E_CAPACITY. Calls that share one must be ordered.
+ */
+int attention_tree_f16(const uint16_t *Q, int64_t q_stride, const bsp_kv_cache *cache, const int32_t *block_table,
+                       int64_t table_width, const int32_t *kv_lens, const int32_t *q_start, int64_t B,
+                       int64_t total_q, int64_t max_q, int64_t q_heads, const uint64_t *tree_mask, float scale,
+                       uint16_t *O, int64_t o_stride, void *workspace, int64_t workspace_bytes, hipStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Low-rank adapters of many requests beside one shared sparse projection:
+ *   Y[n] = W x_n + scale[a] * B_a (A_a x_n),  a = index[n]   (a < 0: W x_n alone)
+ * with A_a [rank][K] and B_a [M][rank] fp16. A_a x_n is summed and kept in
+ * fp32, W x_n and the adapter's part meet in fp32, one rounding to fp16 at the end.
+ * --------------------------------------------------------------------------- */
+typedef struct bsp_lora {
+    int64_t adapters;       /* adapters held; an index at or past it counts as -1 */
+    int64_t rank;           /* the storage rank R: a multiple of 8, 8..256 */
+    const uint16_t *A;      /* DEVICE fp16 [adapters][R][K], 16-byte aligned */
+    const uint16_t *B;      /* DEVICE fp16 [adapters][M][R], 16-byte aligned */
+    const float *scale;     /* DEVICE [adapters], or NULL for 1 */
+    const int32_t *ranks;   /* DEVICE [adapters], the rows of A_a in use (0..R, clamped), or
+                               NULL for R; what lies past them is not used */
+    const int32_t *index;   /* DEVICE [N], the adapter of each token */
+} bsp_lora;
+
+/*
+ * lora_workspace_bytes -- bytes of workspace the calls below need for an M x K
+ * product of N tokens and storage rank R; dtype BSP_FP16 or BSP_INT4. Host only.
+ */
+int lora_workspace_bytes(int dtype, int64_t M, int64_t K, int64_t N, int64_t nnz, int64_t rank, int64_t *bytes);
+
+/*
+ * spmm_bitmap_f16_lora -- spmm_bitmap_f16_ws with adapters. The workspace is
+ * required (256-byte aligned, zero-filled before its first use, as for the _ws entry
+ * points, and of lora_workspace_bytes); BSP_E_CAPACITY when it is too small.
+ */
+int spmm_bitmap_f16_lora(const uint64_t *bitmaps, const uint32_t *offsets, const uint16_t *payload,
+                         int64_t payload_bytes, int64_t M, int64_t K, const uint16_t *X, int64_t N,
+                         const bsp_lora *lora, uint16_t *Y, void *workspace, int64_t workspace_bytes,
+                         hipStream_t stream);
+
+/*
+ * spmm_bitmap_w4a4_dq_lora -- spmm_bitmap_w4a4_dq with adapters: W x_n is the
+ * dequantised int4 product (packed X, scale_w, scale_x); the adapters take the
+ * fp16 activations X16 [N][K] the packed ones came from. Yh = fp16(fp32(fp32(y)
+ * * scale_w[m]) * scale_x[n] + the adapter's part). K <= 16384, X on a 4-byte
+ * boundary (else BSP_E_UNSUPPORTED).
+ */
+int spmm_bitmap_w4a4_dq_lora(const uint64_t *bitmaps, const uint32_t *offsets, const uint8_t *payload,
+                             int64_t payload_bytes, int64_t M, int64_t K, const uint8_t *X, const uint16_t *X16,
+                             int64_t N, const float *scale_w, const float *scale_x, const bsp_lora *lora,
+                             uint16_t *Yh, void *workspace, int64_t workspace_bytes, hipStream_t stream);
 
 /* Static string for a bsp_status code. */
 const char *bsp_status_string(int status);
