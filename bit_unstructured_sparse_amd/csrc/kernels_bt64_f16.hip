@@ -199,12 +199,12 @@ __device__ __forceinline__ void bf_contract(uint64_t word, uint32_t p, const Win
 // block i's partials written after a barrier that follows the sum of block
 // i - 1), as the plan fits them.
 // Workgroup g owns blocks [g*bq + min(g, br), ...): bq or bq + 1 of them.
-template <int NB>
+template <int NB, class Add>
 __global__ __launch_bounds__(1024) void k_bt64_f16(
         const uint64_t *__restrict__ bitmaps, const uint32_t *__restrict__ offsets,
         const uint16_t *__restrict__ payload, uint32_t payload_bytes, int M, int K,
         const uint16_t *__restrict__ X, int N, uint16_t *__restrict__ Y, uint32_t stage_bytes, uint32_t nbuf,
-        int bq, int br, int psets) {
+        int bq, int br, int psets, const Add add) {
     extern __shared__ __attribute__((aligned(16))) uint8_t bf_smem[];
     const int nwaves = blockDim.x >> 6;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
@@ -340,7 +340,7 @@ __global__ __launch_bounds__(1024) void k_bt64_f16(
             if (n < N && rl < rows) {
                 float s = 0.f;
                 for (int w = 0; w < nwaves; ++w) s += pb[(w * NB + nb) * 256 + k * 64 + ln];
-                Y[(int64_t)n * M + m0 + rl] = __builtin_bit_cast(uint16_t, (_Float16)s);
+                Y[(int64_t)n * M + m0 + rl] = __builtin_bit_cast(uint16_t, (_Float16)add.to(s, n, m0 + rl, M));
             }
         }
     };
@@ -446,11 +446,11 @@ __global__ __launch_bounds__(1024) void k_bt64_f16(
 #define BF8_NSTEP_MAX 8                  // steps per workgroup, at most (NSTEP 2, 4 or 8)
 #define BF8_WAVES 8
 
-template <int NSTEP, bool XR, bool RING = false>
+template <int NSTEP, bool XR, bool RING, class Add>
 __global__ __launch_bounds__(512) void k_bt8_f16(
         const uint32_t *__restrict__ offsets, int M, int K, int sq, int sr, const uint64_t *__restrict__ bitmaps,
         const uint16_t *__restrict__ X, int N, const uint16_t *__restrict__ payload, uint32_t payload_bytes,
-        uint16_t *__restrict__ Y, uint32_t area_kb) {
+        uint16_t *__restrict__ Y, uint32_t area_kb, const Add add) {
     extern __shared__ __attribute__((aligned(16))) uint8_t bf_smem[];
     const int nwaves = blockDim.x >> 6;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
@@ -551,7 +551,7 @@ __global__ __launch_bounds__(512) void k_bt8_f16(
             sum += pw[l1];
             sum += pw[l2];
         }
-        Y[(int64_t)n * M + m] = __builtin_bit_cast(uint16_t, (_Float16)sum);
+        Y[(int64_t)n * M + m] = __builtin_bit_cast(uint16_t, (_Float16)add.to(sum, n, m, M));
     };
     issue(0);
     bf_h8 xb[1][8];   // X of this lane's tile, loaded behind the first DMA (below)
@@ -654,7 +654,7 @@ __global__ __launch_bounds__(512) void k_bt8_f16(
                 sum += pw[l1];
                 sum += pw[l2];
             }
-            Y[(int64_t)n * M + m] = __builtin_bit_cast(uint16_t, (_Float16)sum);
+            Y[(int64_t)n * M + m] = __builtin_bit_cast(uint16_t, (_Float16)add.to(sum, n, m, M));
         }
     }
 }
@@ -720,35 +720,28 @@ static bool bf8_plan(int64_t M, int64_t K, int64_t N, int64_t payload_bytes, Bf8
     return p->lds <= (size_t)BF_LDS_MAX;
 }
 
+template <class Add = NoAdd>
 static void launch_bt8_f16(const Bf8Plan &p, const uint64_t *bitmaps, const uint32_t *offsets,
                            const uint16_t *payload, uint32_t payload_bytes, int M, int K, const uint16_t *X, int N,
-                           uint16_t *Y, hipStream_t stream) {
+                           uint16_t *Y, hipStream_t stream, const Add &add = Add{}) {
     // X in runs of the rows at N > 4 (4096 x 4096 at N = 8: 10.5 -> 9.5 us);
     // per-lane loads below (N = 1 and 4 measured 0.05 us faster that way)
-#define BF8_LAUNCH(S, XR)                                                                                       \
-    do {                                                                                                        \
-        (void)hipFuncSetAttribute((const void *)k_bt8_f16<S, XR>, hipFuncAttributeMaxDynamicSharedMemorySize,  \
-                                  (int)p.lds);                                                                  \
-        hipLaunchKernelGGL((k_bt8_f16<S, XR>), dim3(p.grid), dim3(64 * p.nwaves), p.lds, stream, offsets, M, K, \
-                           p.sq, p.sr, bitmaps, X, N, payload, payload_bytes, Y, p.area_kb);                    \
-    } while (0)
-#define BF8_LAUNCH_R(S, XR)                                                                                         \
-    do {                                                                                                            \
-        (void)hipFuncSetAttribute((const void *)k_bt8_f16<S, XR, true>,                                             \
-                                  hipFuncAttributeMaxDynamicSharedMemorySize, (int)p.lds);                          \
-        hipLaunchKernelGGL((k_bt8_f16<S, XR, true>), dim3(p.grid), dim3(64 * p.nwaves), p.lds, stream, offsets, M, \
-                           K, p.sq, p.sr, bitmaps, X, N, payload, payload_bytes, Y, p.area_kb);                     \
+#define BF8_LAUNCH(S, XR, RING)                                                                                    \
+    do {                                                                                                           \
+        (void)hipFuncSetAttribute((const void *)k_bt8_f16<S, XR, RING, Add>,                                       \
+                                  hipFuncAttributeMaxDynamicSharedMemorySize, (int)p.lds);                         \
+        hipLaunchKernelGGL((k_bt8_f16<S, XR, RING, Add>), dim3(p.grid), dim3(64 * p.nwaves), p.lds, stream,        \
+                           offsets, M, K, p.sq, p.sr, bitmaps, X, N, payload, payload_bytes, Y, p.area_kb, add);   \
     } while (0)
     if (p.nstep == 2) {
-        if (N > 4) BF8_LAUNCH(2, true); else BF8_LAUNCH(2, false);
+        if (N > 4) BF8_LAUNCH(2, true, false); else BF8_LAUNCH(2, false, false);
     } else if (p.nstep == 4) {
-        if (N > 4) BF8_LAUNCH(4, true); else BF8_LAUNCH(4, false);
+        if (N > 4) BF8_LAUNCH(4, true, false); else BF8_LAUNCH(4, false, false);
     } else if (!p.ring) {
-        if (N > 4) BF8_LAUNCH(8, true); else BF8_LAUNCH(8, false);
+        if (N > 4) BF8_LAUNCH(8, true, false); else BF8_LAUNCH(8, false, false);
     } else {
-        if (N > 4) BF8_LAUNCH_R(8, true); else BF8_LAUNCH_R(8, false);
+        if (N > 4) BF8_LAUNCH(8, true, true); else BF8_LAUNCH(8, false, true);
     }
-#undef BF8_LAUNCH_R
 #undef BF8_LAUNCH
 }
 
@@ -808,20 +801,21 @@ static bool bf_plan(int64_t M, int64_t K, int64_t N, int64_t payload_bytes, BfPl
     return p->lds <= (size_t)budget;
 }
 
-template <int NB>
+template <int NB, class Add>
 static void launch_bf_t(const BfPlan &p, const uint64_t *bitmaps, const uint32_t *offsets, const uint16_t *payload,
                         uint32_t payload_bytes, int M, int K, const uint16_t *X, int N, uint16_t *Y,
-                        hipStream_t stream) {
-    (void)hipFuncSetAttribute((const void *)k_bt64_f16<NB>, hipFuncAttributeMaxDynamicSharedMemorySize, (int)p.lds);
-    hipLaunchKernelGGL((k_bt64_f16<NB>), dim3(p.grid), dim3(64 * p.nwaves), p.lds, stream, bitmaps, offsets, payload,
-                       payload_bytes, M, K, X, N, Y, p.stage_bytes, p.nbuf, p.bq, p.br, p.psets);
+                        hipStream_t stream, const Add &add) {
+    (void)hipFuncSetAttribute((const void *)k_bt64_f16<NB, Add>, hipFuncAttributeMaxDynamicSharedMemorySize, (int)p.lds);
+    hipLaunchKernelGGL((k_bt64_f16<NB, Add>), dim3(p.grid), dim3(64 * p.nwaves), p.lds, stream, bitmaps, offsets, payload,
+                       payload_bytes, M, K, X, N, Y, p.stage_bytes, p.nbuf, p.bq, p.br, p.psets, add);
 }
 
+template <class Add = NoAdd>
 static void launch_bt64_f16(const BfPlan &p, const uint64_t *bitmaps, const uint32_t *offsets,
                             const uint16_t *payload, uint32_t payload_bytes, int M, int K, const uint16_t *X, int N,
-                            uint16_t *Y, hipStream_t stream) {
+                            uint16_t *Y, hipStream_t stream, const Add &add = Add{}) {
     if (p.nb == 1)
-        launch_bf_t<1>(p, bitmaps, offsets, payload, payload_bytes, M, K, X, N, Y, stream);
+        launch_bf_t<1>(p, bitmaps, offsets, payload, payload_bytes, M, K, X, N, Y, stream, add);
     else
-        launch_bf_t<2>(p, bitmaps, offsets, payload, payload_bytes, M, K, X, N, Y, stream);
+        launch_bf_t<2>(p, bitmaps, offsets, payload, payload_bytes, M, K, X, N, Y, stream, add);
 }

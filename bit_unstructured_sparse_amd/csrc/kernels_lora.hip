@@ -2,7 +2,8 @@
 // sparse projection: Y[n] = W x_n + scale[a] B_a (A_a x_n), a = index[n].
 //
 // Two small products around the sparse one: t_n = scale[a] A_a x_n (rank
-// values per token, fp32, through the workspace), then B_a t_n added to W x_n.
+// values per token, fp32, through the workspace) ahead of it, and B_a t_n in
+// the final write, where W x_n is still an fp32 (or int32) sum: one rounding.
 
 struct LoraArgs {
     const uint16_t *A, *B;
@@ -10,6 +11,12 @@ struct LoraArgs {
     const int32_t *ranks, *index;
     float *t;          // [N][R]
     int adapters, R;
+};
+
+// What a kernel adds to its sum for output (n, m) before rounding it. The
+// plain entry points add nothing.
+struct NoAdd {
+    __device__ __forceinline__ float to(float s, int, int, int) const { return s; }
 };
 
 // The adapter of token n (-1: none) and its rank.
@@ -22,6 +29,33 @@ __device__ __forceinline__ int lora_of(const LoraArgs &a, int n, int *rank) {
     *rank = a.ranks != nullptr ? min(max(a.ranks[i], 0), a.R) : a.R;
     return i;
 }
+
+typedef _Float16 lora_h8 __attribute__((ext_vector_type(8)));
+typedef float lora_f4 __attribute__((ext_vector_type(4)));
+
+// s + B_a[m] t_n, 8 rank positions at a time; what lies past the rank (any
+// bits) is replaced by zero.
+struct LoraAdd {
+    LoraArgs a;
+    __device__ __forceinline__ float to(float s, int n, int m, int M) const {
+        int rank;
+        const int i = lora_of(a, n, &rank);
+        if (i < 0) return s;
+        const uint16_t *row = a.B + ((int64_t)i * M + m) * a.R;
+        const float *t = a.t + (int64_t)n * a.R;
+        float u = 0.f;
+        for (int r = 0; r < rank; r += 8) {
+            const lora_h8 b = *reinterpret_cast<const lora_h8 *>(row + r);
+            const lora_f4 t0 = *reinterpret_cast<const lora_f4 *>(t + r), t1 = *reinterpret_cast<const lora_f4 *>(t + r + 4);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float bj = r + j < rank ? (float)b[j] : 0.f;
+                u = fmaf(bj, j < 4 ? t0[j & 3] : t1[j & 3], u);
+            }
+        }
+        return s + u;
+    }
+};
 
 // t[n][r]: one wavefront per (n, r); rows past the rank and tokens without an
 // adapter give zero.
@@ -41,16 +75,12 @@ __global__ __launch_bounds__(256) void k_lora_down(const LoraArgs a, const uint1
     if (lane == 0) a.t[(int64_t)n * a.R + r] = s;
 }
 
-// Y[n][m] += B_a[m] t_n, a thread per output.
-__global__ __launch_bounds__(256) void k_lora_up(const LoraArgs a, int M, uint16_t *__restrict__ Y) {
+// The dequantised int32 sums with the adapters' part, rounded once.
+__global__ __launch_bounds__(256) void k_lora_dq(const LoraAdd add, const int32_t *__restrict__ Y32, int M,
+                                                 const float *__restrict__ sw, const float *__restrict__ sx,
+                                                 uint16_t *__restrict__ Yh) {
     const int m = blockIdx.x * 256 + threadIdx.x, n = blockIdx.y;
     if (m >= M) return;
-    int rank;
-    const int i = lora_of(a, n, &rank);
-    if (i < 0) return;
-    const uint16_t *row = a.B + ((int64_t)i * M + m) * a.R;
-    float s = 0.f;
-    for (int r = 0; r < rank; ++r) s += bsp_h2f(row[r]) * a.t[(int64_t)n * a.R + r];
-    uint16_t *y = Y + (int64_t)n * M + m;
-    *y = bsp_f2h(bsp_h2f(*y) + s);
+    const int64_t at = (int64_t)n * M + m;
+    Yh[at] = bsp_f2h(add.to((float)Y32[at] * sw[m] * sx[n], n, m, M));
 }

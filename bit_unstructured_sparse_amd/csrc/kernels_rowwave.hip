@@ -63,12 +63,12 @@ __global__ __launch_bounds__(256) void k_rowwave_w4a4(const uint64_t *__restrict
     }
 }
 
-template <int NB>
+template <int NB, class Add>
 __global__ __launch_bounds__(256) void k_rowwave_f16(const uint64_t *__restrict__ bitmaps,
                                                      const uint32_t *__restrict__ offsets,
                                                      const uint16_t *__restrict__ payload, uint32_t payload_bytes,
                                                      int M, int K, const uint16_t *__restrict__ X, int N,
-                                                     uint16_t *__restrict__ Y) {
+                                                     uint16_t *__restrict__ Y, const Add add) {
     const int m = blockIdx.x * (blockDim.x / BSP_WAVE) + threadIdx.x / BSP_WAVE;
     const int lane = threadIdx.x % BSP_WAVE;
     if (m >= M) return;
@@ -101,7 +101,7 @@ __global__ __launch_bounds__(256) void k_rowwave_f16(const uint64_t *__restrict_
     for (int n = 0; n < NB; ++n) {
         if (n < N) {
             const float s = bsp_wave_sum(acc[n]);
-            if (lane == 0) Y[(int64_t)n * M + m] = bsp_f2h(s);
+            if (lane == 0) Y[(int64_t)n * M + m] = bsp_f2h(add.to(s, n, m, M));
         }
     }
 }
@@ -119,12 +119,15 @@ static void launch_rowwave_w4a4(const uint64_t *bitmaps, const uint32_t *offsets
                            K, X, N, Y);
 }
 
+template <class Add = NoAdd>
 static void launch_rowwave_f16(const uint64_t *bitmaps, const uint32_t *offsets, const uint16_t *payload,
                                uint32_t payload_bytes, int M, int K, const uint16_t *X, int N, uint16_t *Y,
-                               hipStream_t stream) {
+                               hipStream_t stream, const Add &add = Add{}) {
     const dim3 block(256), grid((unsigned)((M + 3) / 4));
     if (N <= 8)
-        hipLaunchKernelGGL(k_rowwave_f16<8>, grid, block, 0, stream, bitmaps, offsets, payload, payload_bytes, M, K, X, N, Y);
+        hipLaunchKernelGGL((k_rowwave_f16<8, Add>), grid, block, 0, stream, bitmaps, offsets, payload, payload_bytes, M, K,
+                           X, N, Y, add);
     else
-        hipLaunchKernelGGL(k_rowwave_f16<32>, grid, block, 0, stream, bitmaps, offsets, payload, payload_bytes, M, K, X, N, Y);
+        hipLaunchKernelGGL((k_rowwave_f16<32, Add>), grid, block, 0, stream, bitmaps, offsets, payload, payload_bytes, M, K,
+                           X, N, Y, add);
 }

@@ -563,8 +563,8 @@ __global__ __launch_bounds__(512) void k_bsks_w4a4(SkArgs a) {
 // Same skeleton with one tile per lane (CT = 4 x wavefronts), u16 payload
 // (8 elements per 16-byte granule), the fp16 decode and MFMA of the 16-row
 // kernel, fp32 partials, and one round-to-nearest-even to fp16 at the end.
-template <int NB>
-__global__ __launch_bounds__(1024) void k_bsk_f16(SkArgs a) {
+template <int NB, class Add>
+__global__ __launch_bounds__(1024) void k_bsk_f16(SkArgs a, const Add add) {
     extern __shared__ __attribute__((aligned(16))) uint8_t sk_smem[];
     const int nwaves = blockDim.x >> 6;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
@@ -722,7 +722,7 @@ __global__ __launch_bounds__(1024) void k_bsk_f16(SkArgs a) {
         for (int w = 0; w < nwaves; ++w) s += part[((i * nwaves + w) * NB + nb) * 256 + k * 64 + ln];
         const int b = pl.b0 + i, m = b * 16 + rl;
         if (a.S == 1) {
-            if (m < M) Y[(int64_t)n * M + m] = __builtin_bit_cast(uint16_t, (_Float16)s);
+            if (m < M) Y[(int64_t)n * M + m] = __builtin_bit_cast(uint16_t, (_Float16)add.to(s, n, m, M));
         } else {
             sk_ws_store(wsp + (((int64_t)b * a.S + pl.split) * N + n) * 16 + rl, s);
         }
@@ -735,7 +735,7 @@ __global__ __launch_bounds__(1024) void k_bsk_f16(SkArgs a) {
         if (m >= M) continue;
         float s = 0.f;
         for (int sp = 0; sp < a.S; ++sp) s += sk_ws_load(wsp + (((int64_t)b * a.S + sp) * N + n) * 16 + rl);
-        Y[(int64_t)n * M + m] = __builtin_bit_cast(uint16_t, (_Float16)s);
+        Y[(int64_t)n * M + m] = __builtin_bit_cast(uint16_t, (_Float16)add.to(s, n, m, M));
     }
     sk_reset(a, pl);
 }
@@ -900,7 +900,8 @@ static void launch_bsks_i(const SkPlan &p, const SkArgs &a, bool xu, hipStream_t
     else { if (xu) launch_bsks_t<NB, TPL, 2, true>(p, a, stream); else launch_bsks_t<NB, TPL, 2, false>(p, a, stream); }
 }
 
-static void launch_bsk(const SkPlan &p, const SkArgs &a, hipStream_t stream) {
+template <class Add = NoAdd>
+static void launch_bsk(const SkPlan &p, const SkArgs &a, hipStream_t stream, const Add &add = Add{}) {
     const dim3 grid(p.grid), block(64 * p.nwaves);
     if (p.streamed) {
         const bool xu = a.K % 8 != 0;
@@ -921,11 +922,13 @@ static void launch_bsk(const SkPlan &p, const SkArgs &a, hipStream_t stream) {
 #undef SK_L4
     } else {
         if (p.nb == 1) {
-            (void)hipFuncSetAttribute((const void *)k_bsk_f16<1>, hipFuncAttributeMaxDynamicSharedMemorySize, (int)p.lds);
-            hipLaunchKernelGGL((k_bsk_f16<1>), grid, block, p.lds, stream, a);
+            (void)hipFuncSetAttribute((const void *)k_bsk_f16<1, Add>, hipFuncAttributeMaxDynamicSharedMemorySize,
+                                      (int)p.lds);
+            hipLaunchKernelGGL((k_bsk_f16<1, Add>), grid, block, p.lds, stream, a, add);
         } else {
-            (void)hipFuncSetAttribute((const void *)k_bsk_f16<2>, hipFuncAttributeMaxDynamicSharedMemorySize, (int)p.lds);
-            hipLaunchKernelGGL((k_bsk_f16<2>), grid, block, p.lds, stream, a);
+            (void)hipFuncSetAttribute((const void *)k_bsk_f16<2, Add>, hipFuncAttributeMaxDynamicSharedMemorySize,
+                                      (int)p.lds);
+            hipLaunchKernelGGL((k_bsk_f16<2, Add>), grid, block, p.lds, stream, a, add);
         }
     }
 }

@@ -17,13 +17,13 @@
 
 #include "bitmap_spmm.h"
 #include "device_common.h"
+#include "kernels_lora.hip"
 #include "kernels_rowwave.hip"
 #include "kernels_bt64.hip"
 #include "kernels_bt64_f16.hip"
 #include "kernels_splitk.hip"
 #include "kernels_union.hip"
 #include "kernels_cbc.hip"
-#include "kernels_lora.hip"
 
 namespace {
 
@@ -260,9 +260,12 @@ bool workspace_usable(const void *ws, int64_t bytes) {
     return ws != nullptr && bytes > 0 && ((uintptr_t)ws & 255u) == 0;
 }
 
+// The product of one call; `add` (fp16 only) is what the kernels add to each
+// sum before rounding it.
+template <class Add = NoAdd>
 int spmm_common(int dtype, const uint64_t *bitmaps, const uint32_t *offsets, const void *payload,
                 int64_t payload_bytes, int64_t M, int64_t K, const void *X, int64_t N, void *Y, void *workspace,
-                int64_t workspace_bytes, int algo, hipStream_t stream) {
+                int64_t workspace_bytes, int algo, hipStream_t stream, const Add &add = Add{}) {
     Shape s;
     int rc = check_args(bitmaps, offsets, payload, payload_bytes, M, K, X, N, Y, algo, &s);
     if (rc != BSP_OK || M == 0 || N == 0) return rc;
@@ -291,15 +294,15 @@ int spmm_common(int dtype, const uint64_t *bitmaps, const uint32_t *offsets, con
             break;
         case PK_BT8F16:
             launch_bt8_f16(p.bf8, bitmaps, offsets, (const uint16_t *)payload, pb, (int)M, (int)K, (const uint16_t *)X,
-                           (int)N, (uint16_t *)Y, stream);
+                           (int)N, (uint16_t *)Y, stream, add);
             break;
         case PK_BT64F16:
             launch_bt64_f16(p.bf, bitmaps, offsets, (const uint16_t *)payload, pb, (int)M, (int)K, (const uint16_t *)X,
-                            (int)N, (uint16_t *)Y, stream);
+                            (int)N, (uint16_t *)Y, stream, add);
             break;
         case PK_BSK:
             launch_bsk(p.sk, sk_args(p.sk, bitmaps, offsets, payload, pb, (int)M, (int)K, X, (int)N, Y, workspace),
-                       stream);
+                       stream, add);
             break;
         default:
             if (dtype == BSP_INT4)
@@ -307,7 +310,7 @@ int spmm_common(int dtype, const uint64_t *bitmaps, const uint32_t *offsets, con
                                     (int)N, (int32_t *)Y, stream);
             else
                 launch_rowwave_f16(bitmaps, offsets, (const uint16_t *)payload, pb, (int)M, (int)K,
-                                   (const uint16_t *)X, (int)N, (uint16_t *)Y, stream);
+                                   (const uint16_t *)X, (int)N, (uint16_t *)Y, stream, add);
             break;
     }
     return launch_status();
@@ -717,11 +720,21 @@ extern "C" int spmspv_cbc_f16(const uint32_t *tile_offsets, const uint32_t *coli
 // Low-rank adapters beside a shared projection.
 namespace {
 
-int64_t lora_t_bytes(int64_t N, int64_t R) { return (N * R * 4 + 255) / 256 * 256; }
+// The adapter calls' workspace: what the projection's plan uses (arrival
+// counters, which must stay zero, and partial sums), then t, then (int4) the
+// projection's int32 sums.
+struct LoraSpace {
+    int64_t t, y32, bytes;
+};
 
-// Where t_n lies in the workspace: past the arrival counters and the partial
-// sums the projection's plan may use.
-int64_t lora_t_offset(int64_t plan_bytes) { return std::max(plan_bytes, sk_ws_counters_bytes()); }
+LoraSpace lora_space(int dtype, int64_t plan_bytes, int64_t M, int64_t N, int64_t R) {
+    const auto up = [](int64_t n) { return (n + 255) / 256 * 256; };
+    LoraSpace s;
+    s.t = up(std::max(plan_bytes, sk_ws_counters_bytes()));
+    s.y32 = s.t + up(N * R * 4);
+    s.bytes = s.y32 + (dtype == BSP_INT4 ? up(N * M * 4) : 0);
+    return s;
+}
 
 int lora_check(const bsp_lora *l, int64_t M, int64_t K, int64_t N, const void *X16, const void *workspace,
                int64_t workspace_bytes) {
@@ -744,10 +757,6 @@ void launch_lora_down(const LoraArgs &a, const uint16_t *X, int64_t N, int64_t K
     hipLaunchKernelGGL(k_lora_down, dim3((unsigned)((N * a.R + 3) / 4)), dim3(256), 0, stream, a, X, (int)N, (int)K);
 }
 
-void launch_lora_up(const LoraArgs &a, int64_t M, int64_t N, uint16_t *Y, hipStream_t stream) {
-    hipLaunchKernelGGL(k_lora_up, dim3((unsigned)((M + 255) / 256), (unsigned)N), dim3(256), 0, stream, a, (int)M, Y);
-}
-
 }  // namespace
 
 extern "C" int lora_workspace_bytes(int dtype, int64_t M, int64_t K, int64_t N, int64_t nnz, int64_t rank,
@@ -757,7 +766,7 @@ extern "C" int lora_workspace_bytes(int dtype, int64_t M, int64_t K, int64_t N, 
     const int rc = bsp_workspace_bytes(dtype, M, K, N, nnz, &plan);
     if (rc != BSP_OK) return rc;
     if (bytes == nullptr) return BSP_E_ARG;
-    *bytes = M == 0 || N == 0 ? 0 : lora_t_offset(dtype == BSP_FP16 ? plan : 0) + lora_t_bytes(N, rank);
+    *bytes = M == 0 || N == 0 ? 0 : lora_space(dtype, plan, M, N, rank).bytes;
     return BSP_OK;
 }
 
@@ -773,15 +782,12 @@ extern "C" int spmm_bitmap_f16_lora(const uint64_t *bitmaps, const uint32_t *off
     Plan p;
     rc = choose_plan(BSP_FP16, s, payload_bytes, BSP_ALGO_AUTO, true, &p);
     if (rc != BSP_OK) return rc;
-    const int64_t at = lora_t_offset(p.ws_bytes());
-    if (workspace == nullptr || workspace_bytes < at + lora_t_bytes(N, lora->rank)) return BSP_E_CAPACITY;
-    const LoraArgs a = lora_args(lora, (uint8_t *)workspace + at);
+    const LoraSpace sp = lora_space(BSP_FP16, p.ws_bytes(), M, N, lora->rank);
+    if (workspace == nullptr || workspace_bytes < sp.bytes) return BSP_E_CAPACITY;
+    const LoraArgs a = lora_args(lora, (uint8_t *)workspace + sp.t);
     launch_lora_down(a, X, N, K, stream);
-    rc = spmm_common(BSP_FP16, bitmaps, offsets, payload, payload_bytes, M, K, X, N, Y, workspace, at, BSP_ALGO_AUTO,
-                     stream);
-    if (rc != BSP_OK) return rc;
-    launch_lora_up(a, M, N, Y, stream);
-    return launch_status();
+    return spmm_common(BSP_FP16, bitmaps, offsets, payload, payload_bytes, M, K, X, N, Y, workspace, sp.t, BSP_ALGO_AUTO,
+                       stream, LoraAdd{a});
 }
 
 extern "C" int spmm_bitmap_w4a4_dq_lora(const uint64_t *bitmaps, const uint32_t *offsets, const uint8_t *payload,
@@ -794,12 +800,19 @@ extern "C" int spmm_bitmap_w4a4_dq_lora(const uint64_t *bitmaps, const uint32_t 
     if (rc != BSP_OK) return rc;
     rc = lora_check(lora, M, K, N, X16, workspace, workspace_bytes);
     if (rc != BSP_OK || M == 0 || N == 0) return rc;
-    const int64_t at = lora_t_offset(0);
-    if (workspace == nullptr || workspace_bytes < at + lora_t_bytes(N, lora->rank)) return BSP_E_CAPACITY;
-    const LoraArgs a = lora_args(lora, (uint8_t *)workspace + at);
-    rc = spmm_bitmap_w4a4_dq(bitmaps, offsets, payload, payload_bytes, M, K, X, N, scale_w, scale_x, Yh, stream);
+    if (scale_w == nullptr || scale_x == nullptr) return BSP_E_ARG;
+    Plan p;
+    rc = choose_plan(BSP_INT4, s, payload_bytes, BSP_ALGO_AUTO, true, &p);
     if (rc != BSP_OK) return rc;
+    const LoraSpace sp = lora_space(BSP_INT4, p.ws_bytes(), M, N, lora->rank);
+    if (workspace == nullptr || workspace_bytes < sp.bytes) return BSP_E_CAPACITY;
+    const LoraArgs a = lora_args(lora, (uint8_t *)workspace + sp.t);
+    int32_t *Y32 = (int32_t *)((uint8_t *)workspace + sp.y32);
     launch_lora_down(a, X16, N, K, stream);
-    launch_lora_up(a, M, N, Yh, stream);
+    rc = spmm_common(BSP_INT4, bitmaps, offsets, payload, payload_bytes, M, K, X, N, Y32, workspace, sp.t, BSP_ALGO_AUTO,
+                     stream);
+    if (rc != BSP_OK) return rc;
+    hipLaunchKernelGGL(k_lora_dq, dim3((unsigned)((M + 255) / 256), (unsigned)N), dim3(256), 0, stream, LoraAdd{a}, Y32,
+                       (int)M, scale_w, scale_x, Yh);
     return launch_status();
 }

@@ -613,9 +613,9 @@ int spmm_bitmap_f16_lora(const uint64_t *bitmaps, const uint32_t *offsets, const
 /*
  * spmm_bitmap_w4a4_dq_lora -- spmm_bitmap_w4a4_dq with adapters: W x_n is the
  * dequantised int4 product (packed X, scale_w, scale_x); the adapters take the
- * fp16 activations X16 [N][K] the packed ones came from. Yh = fp16(fp32(fp32(y)
- * * scale_w[m]) * scale_x[n] + the adapter's part). K <= 16384, X on a 4-byte
- * boundary (else BSP_E_UNSUPPORTED).
+ * fp16 activations X16 [N][K] the packed ones came from. Yh = fp16(fp32(y) *
+ * scale_w[m] * scale_x[n] + the adapter's part), in fp32. Any K
+ * spmm_bitmap_w4a4 takes; the workspace as for spmm_bitmap_f16_lora.
  */
 int spmm_bitmap_w4a4_dq_lora(const uint64_t *bitmaps, const uint32_t *offsets, const uint8_t *payload,
                              int64_t payload_bytes, int64_t M, int64_t K, const uint8_t *X, const uint16_t *X16,
