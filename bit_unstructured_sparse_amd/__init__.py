@@ -649,9 +649,9 @@ class _KVCacheDesc(ctypes.Structure):
                 ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p)]
 
 
-@dataclass
+@dataclass(frozen=True)
 class KVCache:
-    """Paged cache tensors: k, v [pages][kv_heads][page_size][row] (float16
+    """Paged cache tensors (their contents change, the tensors do not): k, v [pages][kv_heads][page_size][row] (float16
     [head_dim] for FP16, uint8 [head_dim] for INT8, uint8 [head_dim / 2] for
     INT4) and, for the quantised kinds, k_scale, v_scale int32
     [pages][kv_heads][page_size] (step as bfloat16 in the high half, offset as
@@ -681,26 +681,14 @@ class KVCache:
                     raise ValueError(f"{n} must be [pages][kv_heads][page_size]")
         if len({t.device for t in (self.k, self.v, self.k_scale, self.v_scale) if t is not None}) != 1:
             raise ValueError("the cache's tensors must lie on one device")
-
-    @property
-    def num_pages(self) -> int:
-        return int(self.k.shape[0])
-
-    @property
-    def kv_heads(self) -> int:
-        return int(self.k.shape[1])
-
-    @property
-    def page_size(self) -> int:
-        return int(self.k.shape[2])
-
-    @property
-    def head_dim(self) -> int:
-        return int(self.k.shape[3]) * (2 if self.dtype == INT4 else 1)
-
-    def _desc(self) -> _KVCacheDesc:
-        return _KVCacheDesc(self.dtype, self.num_pages, self.kv_heads, self.page_size, self.head_dim, _dptr(self.k),
-                            _dptr(self.v), _dptr(self.k_scale), _dptr(self.v_scale))
+        pages, heads, page_size, row = (int(n) for n in self.k.shape)
+        dim = 2 * row if self.dtype == INT4 else row
+        desc = _KVCacheDesc(self.dtype, pages, heads, page_size, dim, _dptr(self.k), _dptr(self.v),
+                            _dptr(self.k_scale), _dptr(self.v_scale))
+        for name, value in (("num_pages", pages), ("kv_heads", heads), ("page_size", page_size), ("head_dim", dim),
+                            ("device", self.k.device), ("_index", self.k.get_device()), ("_desc", desc),
+                            ("_ref", ctypes.byref(desc))):
+            object.__setattr__(self, name, value)
 
 
 def new_kv_cache(dtype: int, num_pages: int, kv_heads: int, page_size: int, head_dim: int, device="cuda") -> KVCache:
@@ -720,31 +708,56 @@ def new_kv_cache(dtype: int, num_pages: int, kv_heads: int, page_size: int, head
     return KVCache(dtype, codes(), codes(), words(), words())
 
 
-def _check_rows(t, name, heads, dim, device):
-    """A float16 [n][heads][dim] tensor whose rows may be strided by token."""
+def _rows(t, name, n, heads, dim, index) -> int:
+    """Check a float16 [n][heads][dim] tensor (n None: any) whose rows may be
+    strided by token; returns the stride between tokens."""
+    import torch
+    width = heads * dim
+    # the common case in few steps; _rows_error names what is wrong
+    if isinstance(t, torch.Tensor) and t.dtype is torch.float16 and t.get_device() == index and t.dim() == 3:
+        m, h, d = t.shape
+        if h == heads and d == dim and (n is None or m == n):
+            s0, s1, s2 = t.stride()
+            if t.is_contiguous():
+                return width
+            if s2 == 1 and (heads == 1 or s1 == dim):
+                if m <= 1:
+                    return width
+                if s0 >= width:
+                    return s0
+    raise _rows_error(t, name, n, heads, dim, index)
+
+
+def _rows_error(t, name, n, heads, dim, index):
     import torch
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA (HIP) tensor")
+        return TypeError(f"{name} must be a CUDA (HIP) tensor")
     if t.dtype != torch.float16:
-        raise TypeError(f"{name} must be torch.float16, got {t.dtype}")
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
-        raise ValueError(f"{name} must be [tokens][{heads}][{dim}], got {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}")
-    if t.numel() and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim)):
-        raise ValueError(f"{name}: the heads of a token must be contiguous")
-    if t.shape[0] > 1 and t.stride(0) < heads * dim:
-        raise ValueError(f"{name}: tokens overlap")
+        return TypeError(f"{name} must be torch.float16, got {t.dtype}")
+    if t.get_device() != index:
+        return ValueError(f"{name} must be on device {index}")
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim or (n is not None and t.shape[0] != n):
+        return ValueError(f"{name} must be [{'tokens' if n is None else n}][{heads}][{dim}], got {tuple(t.shape)}")
+    return ValueError(f"{name}: the heads of a token must be contiguous, and tokens must not overlap")
 
 
-def _row_stride(t) -> int:
-    return int(t.stride(0)) if t.shape[0] > 1 else int(t.shape[1] * t.shape[2])
-
-
-def _check_ints(t, name, dtype, numel, device):
+def _flat(t, name, dtype, numel, index) -> int:
+    """Check a contiguous device tensor; returns its address."""
+    import torch
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index and t.is_contiguous() and \
+            t.numel() == numel:
+        return t.data_ptr()
     _check_dev(t, name, dtype, numel)
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}")
+    raise ValueError(f"{name} must be on device {index}")
+
+
+def _stream_of(stream, index: int) -> int:
+    """The handle of a stream, by default the device's current one (its
+    handle alone: the Stream object around it costs as much as a launch)."""
+    if stream is not None:
+        return stream.cuda_stream
+    import torch
+    return torch._C._cuda_getCurrentRawStream(index)
 
 
 def kv_append(cache: KVCache, K, V, slots, stream=None) -> None:
@@ -752,16 +765,12 @@ def kv_append(cache: KVCache, K, V, slots, stream=None) -> None:
     contiguous) into cache slots (int64 [n], page * page_size + offset; a slot
     outside the cache is skipped)."""
     import torch
-    dev = cache.k.device
-    for t, name in ((K, "K"), (V, "V")):
-        _check_rows(t, name, cache.kv_heads, cache.head_dim, dev)
-    n = int(K.shape[0])
-    if V.shape[0] != n:
-        raise ValueError("K and V must hold the same tokens")
-    _check_ints(slots, "slots", torch.int64, n, dev)
-    d = cache._desc()
-    rc = load_library().kv_cache_append(ctypes.byref(d), _dptr(K), _row_stride(K), _dptr(V), _row_stride(V),
-                                        _dptr(slots), n, _stream_handle(stream))
+    heads, dim, index = cache.kv_heads, cache.head_dim, cache._index
+    ks = _rows(K, "K", None, heads, dim, index)
+    n = K.shape[0]
+    vs = _rows(V, "V", n, heads, dim, index)
+    rc = load_library().kv_cache_append(cache._ref, K.data_ptr(), ks, V.data_ptr(), vs,
+                                        _flat(slots, "slots", torch.int64, n, index), n, _stream_of(stream, index))
     _check(rc, "kv_cache_append")
 
 
@@ -769,19 +778,14 @@ def kv_gather(cache: KVCache, slots, K=None, V=None, stream=None):
     """The rows of the slots (int64 [n]) as float16 K, V [n][kv_heads][head_dim]
     (zeros for a slot outside the cache)."""
     import torch
-    dev = cache.k.device
-    n = int(slots.numel())
-    _check_ints(slots, "slots", torch.int64, n, dev)
-    shape = (n, cache.kv_heads, cache.head_dim)
-    K = torch.empty(shape, dtype=torch.float16, device=dev) if K is None else K
-    V = torch.empty(shape, dtype=torch.float16, device=dev) if V is None else V
-    for t, name in ((K, "K"), (V, "V")):
-        _check_rows(t, name, cache.kv_heads, cache.head_dim, dev)
-        if t.shape[0] != n:
-            raise ValueError(f"{name} must hold {n} tokens")
-    d = cache._desc()
-    rc = load_library().kv_cache_gather(ctypes.byref(d), _dptr(slots), n, _dptr(K), _row_stride(K), _dptr(V),
-                                        _row_stride(V), _stream_handle(stream))
+    heads, dim, index = cache.kv_heads, cache.head_dim, cache._index
+    n = slots.numel()
+    at = _flat(slots, "slots", torch.int64, n, index)
+    K = torch.empty((n, heads, dim), dtype=torch.float16, device=cache.device) if K is None else K
+    V = torch.empty((n, heads, dim), dtype=torch.float16, device=cache.device) if V is None else V
+    ks, vs = _rows(K, "K", n, heads, dim, index), _rows(V, "V", n, heads, dim, index)
+    rc = load_library().kv_cache_gather(cache._ref, at, n, K.data_ptr(), ks, V.data_ptr(), vs,
+                                        _stream_of(stream, index))
     _check(rc, "kv_cache_gather")
     return K, V
 
@@ -791,8 +795,7 @@ def kv_gather(cache: KVCache, slots, K=None, V=None, stream=None):
 def attention_workspace_bytes(cache: KVCache, B: int, max_q: int, q_heads: int, table_width: int) -> int:
     """Bytes of workspace attention_tree uses to split the cached tokens."""
     out = ctypes.c_int64(0)
-    d = cache._desc()
-    _check(load_library().attention_tree_workspace_bytes(ctypes.byref(d), table_width, B, max_q, q_heads,
+    _check(load_library().attention_tree_workspace_bytes(cache._ref, table_width, B, max_q, q_heads,
                                                          ctypes.byref(out)), "attention_tree_workspace_bytes")
     return int(out.value)
 
@@ -815,31 +818,24 @@ def attention_tree(Q, cache: KVCache, block_table, kv_lens, q_start, max_q: int,
     head_dim ** -0.5. workspace: new_attention_workspace(...), or None for no
     split over the cached tokens."""
     import torch
-    dev = cache.k.device
+    dim, index = cache.head_dim, cache._index
     if Q.dim() != 3:
         raise ValueError("Q must be [rows][q_heads][head_dim]")
-    hq = int(Q.shape[1])
-    _check_rows(Q, "Q", hq, cache.head_dim, dev)
-    rows = int(Q.shape[0])
     if block_table.dim() != 2:
         raise ValueError("block_table must be [B][width]")
-    B, width = int(block_table.shape[0]), int(block_table.shape[1])
-    _check_ints(block_table, "block_table", torch.int32, B * width, dev)
-    _check_ints(kv_lens, "kv_lens", torch.int32, B, dev)
-    _check_ints(q_start, "q_start", torch.int32, B + 1, dev)
-    if tree_mask is not None:
-        _check_ints(tree_mask, "tree_mask", torch.int64, rows, dev)
+    rows, hq, _ = Q.shape
+    B, width = block_table.shape
+    qs = _rows(Q, "Q", None, hq, dim, index)
     if O is None:
-        O = torch.empty((rows, hq, cache.head_dim), dtype=torch.float16, device=dev)
-    _check_rows(O, "O", hq, cache.head_dim, dev)
-    if O.shape[0] != rows:
-        raise ValueError(f"O must hold {rows} rows")
+        O = torch.empty((rows, hq, dim), dtype=torch.float16, device=cache.device)
+    os_ = _rows(O, "O", rows, hq, dim, index)
     wp, wb = _ws_args(workspace)
-    d = cache._desc()
+    i32 = torch.int32
     rc = load_library().attention_tree_f16(
-        _dptr(Q), _row_stride(Q), ctypes.byref(d), _dptr(block_table), width, _dptr(kv_lens), _dptr(q_start), B, rows,
-        max_q, hq, _dptr(tree_mask), cache.head_dim ** -0.5 if scale is None else scale, _dptr(O), _row_stride(O),
-        wp, wb, _stream_handle(stream))
+        Q.data_ptr(), qs, cache._ref, _flat(block_table, "block_table", i32, B * width, index), width,
+        _flat(kv_lens, "kv_lens", i32, B, index), _flat(q_start, "q_start", i32, B + 1, index), B, rows, max_q, hq,
+        None if tree_mask is None else _flat(tree_mask, "tree_mask", torch.int64, rows, index),
+        dim ** -0.5 if scale is None else scale, O.data_ptr(), os_, wp, wb, _stream_of(stream, index))
     _check(rc, "attention_tree_f16")
     return O
 
@@ -853,7 +849,7 @@ class _LoraDesc(ctypes.Structure):
                 ("index", ctypes.c_void_p)]
 
 
-@dataclass
+@dataclass(frozen=True)
 class LoraAdapters:
     """The adapters of one projection: A float16 [adapters][R][K], B float16
     [adapters][M][R] (R a multiple of 8, at most 256); scale float32 [adapters]
@@ -868,29 +864,23 @@ class LoraAdapters:
         if self.A.dim() != 3 or self.B.dim() != 3 or self.A.shape[0] != self.B.shape[0] or \
                 self.A.shape[1] != self.B.shape[2]:
             raise ValueError("A must be [adapters][R][K] and B [adapters][M][R]")
-        dev = self.A.device
         _check_dev(self.A, "A", torch.float16)
-        _check_ints(self.B, "B", torch.float16, self.B.numel(), dev)
+        n, R, K = (int(x) for x in self.A.shape)
+        index = self.A.get_device()
+        _flat(self.B, "B", torch.float16, self.B.numel(), index)
         if self.scale is not None:
-            _check_ints(self.scale, "scale", torch.float32, self.adapters, dev)
+            _flat(self.scale, "scale", torch.float32, n, index)
         if self.rank is not None:
-            _check_ints(self.rank, "rank", torch.int32, self.adapters, dev)
+            _flat(self.rank, "rank", torch.int32, n, index)
+        for name, value in (("adapters", n), ("R", R), ("K", K), ("M", int(self.B.shape[1])), ("_index", index)):
+            object.__setattr__(self, name, value)
 
-    @property
-    def adapters(self) -> int:
-        return int(self.A.shape[0])
-
-    @property
-    def R(self) -> int:
-        return int(self.A.shape[1])
-
-    def _desc(self, M, K, index, N) -> _LoraDesc:
+    def _desc(self, W, index, N) -> _LoraDesc:
         import torch
-        if self.A.shape[2] != K or self.B.shape[1] != M:
-            raise ValueError(f"the adapters are for a {self.B.shape[1]} x {self.A.shape[2]} projection, not {M} x {K}")
-        _check_ints(index, "index", torch.int32, N, self.A.device)
+        if self.K != W.K or self.M != W.M:
+            raise ValueError(f"the adapters are for a {self.M} x {self.K} projection, not {W.M} x {W.K}")
         return _LoraDesc(self.adapters, self.R, _dptr(self.A), _dptr(self.B), _dptr(self.scale), _dptr(self.rank),
-                         _dptr(index))
+                         _flat(index, "index", torch.int32, N, self._index))
 
 
 def lora_workspace_bytes(dtype: int, M: int, K: int, N: int, rank: int, nnz: int = -1) -> int:
@@ -916,18 +906,18 @@ def spmm_f16_lora(W: DeviceMatrix, X, adapters: LoraAdapters, index, Y=None, wor
         raise TypeError("spmm_f16_lora needs an fp16 DeviceMatrix")
     if X.dim() != 2 or X.shape[1] != W.K:
         raise ValueError("X must be [N][K]")
-    N = int(X.shape[0])
-    _check_dev(X, "X", torch.float16)
-    d = adapters._desc(W.M, W.K, index, N)
+    N, dev = X.shape[0], adapters._index
+    x = _flat(X, "X", torch.float16, N * W.K, dev)
+    d = adapters._desc(W, index, N)
     if Y is None:
         Y = torch.empty((N, W.M), dtype=torch.float16, device=X.device)
-    _check_dev(Y, "Y", torch.float16, N * W.M)
+    y = _flat(Y, "Y", torch.float16, N * W.M, dev)
     if workspace is None:
         workspace = new_lora_workspace(W, N, adapters, device=X.device)
     wp, wb = _ws_args(workspace)
     rc = load_library().spmm_bitmap_f16_lora(
-        _dptr(W.bitmaps), _dptr(W.offsets), _dptr(W.payload), W.payload.numel(), W.M, W.K, _dptr(X), N,
-        ctypes.byref(d), _dptr(Y), wp, wb, _stream_handle(stream))
+        _dptr(W.bitmaps), _dptr(W.offsets), _dptr(W.payload), W.payload.numel(), W.M, W.K, x, N, ctypes.byref(d), y,
+        wp, wb, _stream_of(stream, dev))
     _check(rc, "spmm_bitmap_f16_lora")
     return Y
 
@@ -943,20 +933,19 @@ def spmm_w4a4_dq_lora(W: DeviceMatrix, X, X16, scale_w, scale_x, adapters: LoraA
         raise TypeError("spmm_w4a4_dq_lora needs an int4 DeviceMatrix")
     if X16.dim() != 2 or X16.shape[1] != W.K:
         raise ValueError("X16 must be [N][K]")
-    N = int(X16.shape[0])
-    _check_dev(X16, "X16", torch.float16)
-    _check_dev(X, "X", torch.uint8, N * ((W.K + 1) // 2))
-    _check_dev(scale_w, "scale_w", torch.float32, W.M)
-    _check_dev(scale_x, "scale_x", torch.float32, N)
-    d = adapters._desc(W.M, W.K, index, N)
+    N, dev = X16.shape[0], adapters._index
+    x16 = _flat(X16, "X16", torch.float16, N * W.K, dev)
+    x = _flat(X, "X", torch.uint8, N * ((W.K + 1) // 2), dev)
+    sw, sx = _flat(scale_w, "scale_w", torch.float32, W.M, dev), _flat(scale_x, "scale_x", torch.float32, N, dev)
+    d = adapters._desc(W, index, N)
     if Yh is None:
         Yh = torch.empty((N, W.M), dtype=torch.float16, device=X16.device)
-    _check_dev(Yh, "Yh", torch.float16, N * W.M)
+    y = _flat(Yh, "Yh", torch.float16, N * W.M, dev)
     if workspace is None:
         workspace = new_lora_workspace(W, N, adapters, device=X16.device)
     wp, wb = _ws_args(workspace)
     rc = load_library().spmm_bitmap_w4a4_dq_lora(
-        _dptr(W.bitmaps), _dptr(W.offsets), _dptr(W.payload), W.payload.numel(), W.M, W.K, _dptr(X), _dptr(X16), N,
-        _dptr(scale_w), _dptr(scale_x), ctypes.byref(d), _dptr(Yh), wp, wb, _stream_handle(stream))
+        _dptr(W.bitmaps), _dptr(W.offsets), _dptr(W.payload), W.payload.numel(), W.M, W.K, x, x16, N, sw, sx,
+        ctypes.byref(d), y, wp, wb, _stream_of(stream, dev))
     _check(rc, "spmm_bitmap_w4a4_dq_lora")
     return Yh

@@ -25,24 +25,34 @@ struct AtArgs {
     int total_q, max_q, hq, hkv, num_pages, page_shift, B;
     int q_vec, o_vec;              // Q / O rows on 16-byte boundaries
     int row_blocks;                // blocks of query rows
-    int chunks, min_per, max_chunks;   // pieces aimed at (0: one per sequence), least tiles of one, most pieces
+    int chunks, min_per, max_chunks;   // chunks (0: one per sequence), least tiles of one, chunks launched
     float scale;
-    float *part;                   // partial sums of the pieces
+    int join;                      // partial sums are joined by k_at_join, not by the last chunk
+    float *part;                   // partial sums, two places per chunk, kv head and row block
     uint32_t *counters;            // arrivals per (sequence, kv head, row block), zero between calls
 };
 
 typedef float at_f4 __attribute__((ext_vector_type(4)));
 typedef uint32_t at_u4 __attribute__((ext_vector_type(4)));
 
+// The kernel's arguments, read again where they are needed: what only the ends
+// of a sequence's part use must not hold scalar registers through its tiles.
+typedef const __attribute__((address_space(4))) AtArgs *AtLate;
+__device__ __forceinline__ AtLate at_late() {
+    AtLate p = (AtLate)__builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(p));
+    return p;
+}
+
 // 8 channels of a finished row: sums times inv, rounded to fp16.
-__device__ __forceinline__ void at_write(const AtArgs &a, int q0, int kvh, int G, int row, int d, int D, at_f4 y0,
+__device__ __forceinline__ void at_write(AtLate ap, int q0, int kvh, int G, int row, int d, int D, at_f4 y0,
                                          at_f4 y1, float inv) {
     const int t = row / G, g = row - t * G;
-    uint16_t *o = a.O + (int64_t)(q0 + t) * a.o_stride + (int64_t)(kvh * G + g) * D + d;
+    uint16_t *o = ap->O + (int64_t)(q0 + t) * ap->o_stride + (int64_t)(kvh * G + g) * D + d;
     uint16_t h[8];
 #pragma unroll
     for (int e = 0; e < 4; ++e) h[e] = bsp_f2h(y0[e] * inv), h[4 + e] = bsp_f2h(y1[e] * inv);
-    if (a.o_vec) {
+    if (ap->o_vec) {
         at_u4 v;
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[e] = (uint32_t)h[2 * e] | ((uint32_t)h[2 * e + 1] << 16);
@@ -56,22 +66,72 @@ __device__ __forceinline__ void at_write(const AtArgs &a, int q0, int kvh, int G
 typedef _Float16 at_h8 __attribute__((ext_vector_type(8)));
 typedef _Float16 at_h2 __attribute__((ext_vector_type(2)));
 
+#ifndef AT_GROUPS
+#define AT_GROUPS 512
+#endif
+#ifndef AT_OCC1
+#define AT_OCC1 2
+#endif
+#ifndef AT_OCC4
+#define AT_OCC4 2
+#endif
+#ifndef AT_MINPER
+#define AT_MINPER 8
+#endif
 #define AT_WAVES 4
 #define AT_TILE 32                 // cached tokens per wavefront and step
 #define AT_BOOST 6.0f              // log2: the weights' scale, 2^6 at the running maximum
 #define AT_SLACK 8.0f              // log2: how far a score may pass the running maximum before it is moved
-#define AT_LOW -1e30f              // the running maximum before any score
+#define AT_LOW -1e30f              // stands for the maximum of no scores when sums are joined
+#define AT_NONE -3e38f
 
-// Bytes a lane reads of a K row (its quarter of the channels) and of a V row
-// (its sixteenth), in dwords (V: at least one).
+// What a lane reads of a K row and of a V row. A K row goes to the four lanes
+// of its A row in pieces of PIECE bytes in turn, so that one load instruction
+// takes whole 64-byte stretches of 16 rows (a contiguous quarter of the row
+// per lane instead touched every line of the rows with each of its loads:
+// 131072 fp16 tokens 224 -> NEW us). A V row goes to 16 lanes, a sixteenth each.
 template <int KIND, int D>
 struct AtShape {
     static constexpr int ROW = KIND == BSP_FP16 ? 2 * D : KIND == BSP_INT8 ? D : D / 2;
     static constexpr int KW = ROW / 16;                      // dwords per K row and lane
+    static constexpr int PIECE = ROW < 64 ? ROW / 4 : 16;
+    static constexpr int PIECES = ROW / (4 * PIECE);
+    static constexpr int PCH = PIECE * D / ROW;              // channels of a piece
     static constexpr int VB = ROW / 16;                      // bytes per V row and lane
     static constexpr int VW = VB < 4 ? 1 : VB / 4;
     static constexpr int NT = D / 16;                        // 16-channel blocks of the output
     static constexpr int STEPS = D / 32;                     // MFMAs along the channels
+};
+
+// Agent-scope 16-byte stores and loads of the partial sums: they go to the
+// coherence point all XCDs share, so partials are visible to the workgroup
+// that joins them once the stores have completed (aux 16: sc1).
+__device__ __forceinline__ void at_ws_store(__amdgpu_buffer_rsrc_t rs, uint32_t off, at_f4 v) {
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(at_u4, v), rs, off, 0, 16);
+}
+__device__ __forceinline__ at_f4 at_ws_load(__amdgpu_buffer_rsrc_t rs, uint32_t off) {
+    return __builtin_bit_cast(at_f4, __builtin_amdgcn_raw_buffer_load_b128(rs, off, 0, 16));
+}
+
+// Eight channels of a row summed over chunks: sums and normalisation relative
+// to the largest of the chunks' maxima so far.
+struct AtSum {
+    at_f4 y0 = {0.f, 0.f, 0.f, 0.f}, y1 = {0.f, 0.f, 0.f, 0.f};
+    float m = AT_LOW, l = 0.f;
+    __device__ __forceinline__ void add(at_f4 z0, at_f4 z1, float zm, float zl) {
+        const float mn = fmaxf(m, zm);
+        const float f = __builtin_amdgcn_exp2f(m - mn), g = __builtin_amdgcn_exp2f(zm - mn);
+        m = mn;
+        l = l * f + zl * g;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y0[e] = y0[e] * f + z0[e] * g, y1[e] = y1[e] * f + z1[e] * g;
+    }
+    // a posted part: the place's first float, its bytes, where the channels and (m, l) lie
+    __device__ __forceinline__ void add(const float *place, uint32_t bytes, uint32_t at, uint32_t at_ml) {
+        const __amdgpu_buffer_rsrc_t rs = bsp_rsrc(place, bytes);
+        const at_f4 ml = at_ws_load(rs, at_ml), z0 = at_ws_load(rs, at), z1 = at_ws_load(rs, at + 16);
+        add(z0, z1, ml.x, ml.y);
+    }
 };
 
 template <int N>
@@ -88,16 +148,6 @@ __device__ __forceinline__ void at_load(const uint8_t *p, uint32_t (&r)[N]) {
     } else {
         r[0] = *reinterpret_cast<const uint32_t *>(p);
     }
-}
-
-// Agent-scope 16-byte stores and loads of the partial sums: they go to the
-// coherence point all XCDs share, so partials are visible to the workgroup
-// that joins them once the stores have completed (aux 16: sc1).
-__device__ __forceinline__ void at_ws_store(__amdgpu_buffer_rsrc_t rs, uint32_t off, at_f4 v) {
-    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(at_u4, v), rs, off, 0, 16);
-}
-__device__ __forceinline__ at_f4 at_ws_load(__amdgpu_buffer_rsrc_t rs, uint32_t off) {
-    return __builtin_bit_cast(at_f4, __builtin_amdgcn_raw_buffer_load_b128(rs, off, 0, 16));
 }
 
 // Bytes 2k, 2k + 1 of a dword, or byte k of two dwords, as the low bytes of
@@ -170,50 +220,79 @@ __device__ __forceinline__ float at_group_max(float v) {
     return fmaxf(v, __shfl_xor(v, 32, 64));
 }
 
-template <int KIND, int D, int RT>
+__device__ __forceinline__ int at_uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+// One wavefront's share; it takes every WT-th tile.
+template <int KIND, int D, int RT, int WT>
 struct AtWave {
     using Sh = AtShape<KIND, D>;
     static constexpr bool QUANT = KIND != BSP_FP16;
     const AtArgs &a;
     int lane, col, grp;
-    int kvh, len, past, T;
+    int kvh, len, past;
     const int32_t *table;
-    // per query row (the lane's column)
-    at_h8 q[RT][Sh::STEPS];
+    // per query row (the lane's column); q in registers, or in LDS where those
+    // are short: [RT][STEPS][64 lanes], the workgroup's wavefronts share the rows
+    static constexpr bool Q_LDS = RT > 1 || D == 256;
+    at_h8 q[Q_LDS ? 1 : RT][Q_LDS ? 1 : Sh::STEPS];
+    const at_h8 *q_lds;
     float qc[RT];                  // sum of the row's q, times the score factor
     uint64_t seen[RT];
-    float m[RT], l[RT], osum[RT], psum[RT];
+    // the running maximum less AT_BOOST, and the sums of the weights 2^(x - mb)
+    float mb[RT], l[RT], osum[RT], psum[RT];
+    float limit[RT];               // a score past it moves the maximum (AT_NONE: the row has none yet)
     at_f4 acc[RT][Sh::NT];
     float sig, rsig;               // the value steps' common power of two, and 1 / it
     float c;                       // score factor: scale * log2(e)
     // the tile in flight
     uint32_t k[2][Sh::KW], v[8][Sh::VW], kw[8], vw[8];
-    int pk, pv;                    // its pages: of the lane's K rows, of its V rows
+    // Cache pages of the wavefront's next 32 tiles, looked up at once: lane
+    // 2 i + h has the page of the i-th tile's 16 tokens h (a page holds whole
+    // groups of 16).
+    int pages;
+    int64_t base0, base1;          // rows of the next tile's two groups (uniform)
 
     __device__ AtWave(const AtArgs &args) : a(args) {}
 
-    __device__ __forceinline__ int page_of(int j) const {
-        const int p = table[min(j, len - 1) >> a.page_shift];
-        return (unsigned)p < (unsigned)a.num_pages ? p : 0;
+    __device__ __forceinline__ at_h8 q_frag(int rt, int s) const {
+        if constexpr (Q_LDS)
+            return q_lds[(rt * Sh::STEPS + s) * 64 + lane];
+        else
+            return q[rt][s];
     }
-    __device__ __forceinline__ int64_t row_of(int page, int j) const {
-        return (((int64_t)page * a.hkv + kvh) << a.page_shift) + (j & ((1 << a.page_shift) - 1));
+
+    __device__ __forceinline__ void load_pages(int tile) {
+        const int j = min((tile + WT * (lane >> 1)) * AT_TILE + 16 * (lane & 1), len - 1);
+        const int p = table[j >> a.page_shift];
+        pages = (unsigned)p < (unsigned)a.num_pages ? p : 0;
+    }
+    // The row of the wavefront's tile i (mod 32), at token j0 of the sequence.
+    __device__ __forceinline__ void set_tile(int i, int j0) {
+        const int in = (1 << a.page_shift) - 1;
+        const int p0 = __builtin_amdgcn_readlane(pages, 2 * (i & 31)), p1 = __builtin_amdgcn_readlane(pages, 2 * (i & 31) + 1);
+        base0 = (((int64_t)p0 * a.hkv + kvh) << a.page_shift) + (j0 & in);
+        base1 = (((int64_t)p1 * a.hkv + kvh) << a.page_shift) + ((j0 + 16) & in);
     }
     // S tile u, A row i: token 8 (i / 4) + 4 u + i % 4, so that the scores of a
     // lane (C rows 4 g .. 4 g + 3 of both tiles) are those of 8 neighbouring
     // tokens, 8 g .. 8 g + 7: its part of the second product's B operand.
-    __device__ __forceinline__ void load_pages(int j0) {
-        pk = page_of(j0 + 8 * (col >> 2));
-        pv = page_of(j0 + 8 * grp);
-    }
-    __device__ __forceinline__ void load_k(int j0) {
-        const int64_t r = row_of(pk, j0 + 8 * (col >> 2) + (col & 3));
+    __device__ __forceinline__ void load_k() {
+        const uint8_t *p = a.k + ((col >> 3) ? base1 : base0) * Sh::ROW + (8 * ((col >> 2) & 1) + (col & 3)) * Sh::ROW +
+                           grp * Sh::PIECE;
 #pragma unroll
-        for (int u = 0; u < 2; ++u) at_load(a.k + (r + 4 * u) * Sh::ROW + grp * (Sh::ROW / 4), k[u]);
-        if constexpr (QUANT) at_load(reinterpret_cast<const uint8_t *>(a.kw + row_of(pv, j0 + 8 * grp)), kw);
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int j = 0; j < Sh::PIECES; ++j) {
+                uint32_t r[Sh::PIECE / 4];
+                at_load(p + 4 * u * Sh::ROW + 64 * j, r);
+#pragma unroll
+                for (int i = 0; i < Sh::PIECE / 4; ++i) k[u][j * (Sh::PIECE / 4) + i] = r[i];
+            }
+        if constexpr (QUANT)
+            at_load(reinterpret_cast<const uint8_t *>(a.kw + ((grp >> 1) ? base1 : base0) + 8 * (grp & 1)), kw);
     }
-    __device__ __forceinline__ void load_v(int j0) {
-        const int64_t r = row_of(pv, j0 + 8 * grp);
+    __device__ __forceinline__ void load_v() {
+        const int64_t r = ((grp >> 1) ? base1 : base0) + 8 * (grp & 1);
         const uint8_t *p = a.v + r * Sh::ROW + col * Sh::VB;
 #pragma unroll
         for (int t = 0; t < 8; ++t) {
@@ -225,96 +304,144 @@ struct AtWave {
         if constexpr (QUANT) at_load(reinterpret_cast<const uint8_t *>(a.vw + r), vw);
     }
 
-    // One tile: scores, running maximum, weights, output. MASKED: the tile
-    // holds drafted tokens or the end of the sequence. The next tile's loads
-    // are issued as the registers they fill fall free.
-    template <bool MASKED>
-    __device__ __forceinline__ void tile(int j0, int jn) {
+    // Bits 0 .. 7: whether a row that sees drafted tokens `bits` sees tokens j .. j + 7.
+    __device__ __forceinline__ uint32_t visible(int j, uint64_t bits) const {
+        const int d = j - past, n = len - j;       // first token's place among the drafted ones; tokens there are
+        uint32_t m = d >= 0 ? (d < 64 ? (uint32_t)(bits >> d) : 0u)
+                            : (d > -8 ? ((uint32_t)bits << (-d & 7)) | ((1u << (-d & 7)) - 1u) : 0xFFu);
+        m &= n >= 8 ? 0xFFu : (1u << max(n, 0)) - 1u;
+        return m & 0xFFu;
+    }
+
+    // One tile: scores, running maximum, weights, output. The next tile's loads
+    // (base0, base1: set_tile) are issued as the registers they fill fall free.
+    __device__ __forceinline__ void tile(int j0) {
         at_f4 x[RT][2];
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
+        for (int rt = 0; rt < RT; ++rt) x[rt][0] = x[rt][1] = at_f4{0.f, 0.f, 0.f, 0.f};
+        if constexpr (KIND == BSP_INT4) {
+            at_f4 hi[RT][2];
 #pragma unroll
-            for (int rt = 0; rt < RT; ++rt) x[rt][u] = at_f4{0.f, 0.f, 0.f, 0.f};
-            if constexpr (KIND == BSP_INT4) {
-                at_f4 hi[RT];
+            for (int rt = 0; rt < RT; ++rt) hi[rt][0] = hi[rt][1] = at_f4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int rt = 0; rt < RT; ++rt) hi[rt] = at_f4{0.f, 0.f, 0.f, 0.f};
+            for (int s = 0; s < Sh::STEPS; s += 2) {
+                const at_h8 f0 = at_k_frag<KIND>(k[0], s), f1 = at_k_frag<KIND>(k[0], s + 1);
+                const at_h8 g0 = at_k_frag<KIND>(k[1], s), g1 = at_k_frag<KIND>(k[1], s + 1);
 #pragma unroll
-                for (int s = 0; s < Sh::STEPS; s += 2) {
-                    const at_h8 f0 = at_k_frag<KIND>(k[u], s), f1 = at_k_frag<KIND>(k[u], s + 1);
-#pragma unroll
-                    for (int rt = 0; rt < RT; ++rt) {
-                        x[rt][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f0, q[rt][s], x[rt][u], 0, 0, 0);
-                        hi[rt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f1, q[rt][s + 1], hi[rt], 0, 0, 0);
-                    }
+                for (int rt = 0; rt < RT; ++rt) {
+                    const at_h8 q0 = q_frag(rt, s), q1 = q_frag(rt, s + 1);
+                    x[rt][0] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f0, q0, x[rt][0], 0, 0, 0);
+                    x[rt][1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(g0, q0, x[rt][1], 0, 0, 0);
+                    hi[rt][0] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f1, q1, hi[rt][0], 0, 0, 0);
+                    hi[rt][1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(g1, q1, hi[rt][1], 0, 0, 0);
                 }
+            }
 #pragma unroll
-                for (int rt = 0; rt < RT; ++rt)
+            for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) x[rt][u][r] = fmaf(hi[rt][r], 0.0625f, x[rt][u][r]);
-            } else {
+                for (int e = 0; e < 8; ++e) x[rt][e >> 2][e & 3] = fmaf(hi[rt][e >> 2][e & 3], 0.0625f, x[rt][e >> 2][e & 3]);
+        } else {
 #pragma unroll
-                for (int s = 0; s < Sh::STEPS; ++s) {
-                    const at_h8 f = at_k_frag<KIND>(k[u], s);
+            for (int s = 0; s < Sh::STEPS; ++s) {
+                const at_h8 f = at_k_frag<KIND>(k[0], s), g = at_k_frag<KIND>(k[1], s);
 #pragma unroll
-                    for (int rt = 0; rt < RT; ++rt)
-                        x[rt][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f, q[rt][s], x[rt][u], 0, 0, 0);
+                for (int rt = 0; rt < RT; ++rt) {
+                    const at_h8 qs = q_frag(rt, s);
+                    x[rt][0] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f, qs, x[rt][0], 0, 0, 0);
+                    x[rt][1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(g, qs, x[rt][1], 0, 0, 0);
                 }
             }
         }
-        // scores in log2 units: scale * log2(e) * (s u.q 2^-24 2^24 + o sum(q))
-        float ks[8], ko[8];
-        if constexpr (QUANT) {
-            const float cc = c * 16777216.0f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) ks[e] = kv_word_step(kw[e]) * cc, ko[e] = kv_word_offset(kw[e]);
-        }
-        load_pages(jn);
-        load_k(jn);
-        uint32_t ok[RT];
+        __builtin_amdgcn_sched_barrier(0);
+        // scores in log2 units, less the running maximum (mb):
+        // scale * log2(e) * (s u.q 2^-24 2^24 + o sum(q)) - mb
         float top[RT];
+        const float cc = c * 16777216.0f;
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt) {
-            ok[rt] = 0xFFu;
-            top[rt] = -INFINITY;
+        for (int rt = 0; rt < RT; ++rt) top[rt] = -INFINITY;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
+        for (int e = 0; e < 8; ++e) {
+            float ks, ko;
+            if constexpr (QUANT) ks = kv_word_step(kw[e]) * cc, ko = kv_word_offset(kw[e]);
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {
                 float y = x[rt][e >> 2][e & 3];
                 if constexpr (QUANT)
-                    y = fmaf(y, ks[e], ko[e] * qc[rt]);
+                    y = fmaf(y, ks, fmaf(ko, qc[rt], -mb[rt]));
                 else
-                    y *= c;
-                if constexpr (MASKED) {
-                    const int j = j0 + 8 * grp + e, dj = j - past;
-                    const bool see = j < len && (dj < 0 || (dj < BSP_TREE_MAX && (seen[rt] >> (dj & 63) & 1)));
-                    y = see ? y : -INFINITY;
-                    if (!see) ok[rt] &= ~(1u << e);
-                }
+                    y = fmaf(y, c, -mb[rt]);
                 x[rt][e >> 2][e & 3] = y;
                 top[rt] = fmaxf(top[rt], y);
             }
         }
-        float vs[8], vo[8];
-        float smax = 0.f;
-        if constexpr (QUANT) {
+        load_k();
+        if (j0 + AT_TILE > past) {
+            // Drafted tokens or the end of the sequence: what a row does not
+            // see scores -inf; rows past the end hold anything, NaN too, and
+            // count as zeros. A value row (or its word) that is not finite
+            // counts as zero too, and makes the query rows that see it NaN.
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {
+                const uint32_t ok = visible(j0 + 8 * grp, seen[rt]);
+                top[rt] = -INFINITY;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float y = (ok >> e & 1u) != 0u ? x[rt][e >> 2][e & 3] : -INFINITY;
+                    x[rt][e >> 2][e & 3] = y;
+                    top[rt] = fmaxf(top[rt], y);
+                    // (one comparison at a time: 16 masks in flight would spill)
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            }
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                uint32_t w = vw[e];
-                if constexpr (MASKED) w = j0 + 8 * grp + e < len ? w : 0u;
-                vs[e] = kv_word_step(w), vo[e] = kv_word_offset(w);
-                smax = fmaxf(smax, vs[e] < INFINITY ? vs[e] : 0.f);
+                __builtin_amdgcn_sched_barrier(0);
+                const bool in = j0 + 8 * grp + e < len;
+                bool nf = false;
+                if constexpr (QUANT) {
+                    nf = in & (((vw[e] & 0x7F800000u) == 0x7F800000u) | ((vw[e] & 0x7C00u) == 0x7C00u));
+                    vw[e] = (in && !nf) ? vw[e] : 0u;
+                } else {
+#pragma unroll
+                    for (int i = 0; i < Sh::VW; ++i) {
+                        const uint32_t h = v[e][i];
+                        const bool lo = (h & 0x7C00u) == 0x7C00u, hi = (h & 0x7C000000u) == 0x7C000000u;
+                        nf |= in & (lo | hi);
+                        v[e][i] = ((in && !lo) ? h & 0xFFFFu : 0u) | ((in && !hi) ? h & 0xFFFF0000u : 0u);
+                    }
+                    // any of the 16 lanes that hold the row
+                    nf = ((__ballot(nf) >> (16 * grp)) & 0xFFFFu) != 0;
+                }
+                if (__ballot(nf) != 0) {
+#pragma unroll
+                    for (int rt = 0; rt < RT; ++rt)
+                        l[rt] = (nf && x[rt][e >> 2][e & 3] != -INFINITY) ? __builtin_nanf("") : l[rt];
+                }
             }
+        }
+        // the largest value step (positive floats order as integers)
+        uint32_t smax = 0;
+        if constexpr (QUANT) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) smax = max(smax, vw[e]);
         }
         // Move the running maximum only when a score passes it by more than
         // the slack (the weights stay fp16: 2^(6 + 8) at most), and the value
         // steps' scale when a step passes it.
-        bool move = QUANT && smax > sig;
+        bool move = QUANT && (smax & 0xFFFF0000u) > __builtin_bit_cast(uint32_t, sig);
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt) move |= top[rt] > m[rt] + AT_SLACK;
-        if (__ballot(move) != 0) {
-            float f[RT], fs = 1.f;
+        for (int rt = 0; rt < RT; ++rt) move |= top[rt] > limit[rt];
+        float f[RT];
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) f[rt] = 1.f;
+        const bool moved = __ballot(move) != 0;
+        if (moved) {
+            float fs = 1.f;
             if constexpr (QUANT) {
-                const float sm = fmaxf(at_group_max(smax), sig);
+                float sm = 0.f;            // the largest finite step
+#pragma unroll
+                for (int e = 0; e < 8; ++e) sm = fmaxf(sm, vw[e] < 0x7F800000u ? kv_word_step(vw[e]) : 0.f);
+                sm = fmaxf(at_group_max(sm), sig);
                 const uint32_t b = (__builtin_bit_cast(uint32_t, sm) + 0x7FFFFFu) & 0x7F800000u;
                 fs = sig * __builtin_bit_cast(float, 0x7F000000u - b);
                 sig = __builtin_bit_cast(float, b);
@@ -322,365 +449,443 @@ struct AtWave {
             }
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt) {
-                const float mn = fmaxf(m[rt], at_group_max(top[rt]));
-                f[rt] = __builtin_amdgcn_exp2f(m[rt] - mn);
-                m[rt] = mn;
-                l[rt] *= f[rt], osum[rt] *= f[rt];
-                f[rt] *= fs;
+                // how far it moves: up only, but for the row's first scores
+                const float most = at_group_max(top[rt]);
+                const bool first = limit[rt] == AT_NONE && most > AT_NONE;
+                const float up = first ? most - AT_BOOST : fmaxf(0.f, most - AT_BOOST);
+                const float g = first ? 1.f : __builtin_amdgcn_exp2f(-up);
+                limit[rt] = first ? AT_BOOST + AT_SLACK : limit[rt];
+                mb[rt] += up;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[rt][e >> 2][e & 3] -= up;
+                l[rt] *= g, osum[rt] *= g;
+                f[rt] = g * fs;
                 psum[rt] *= f[rt];
-#pragma unroll
-                for (int t = 0; t < Sh::NT; ++t)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) acc[rt][t][r] *= f[rt];
             }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        if (moved) {       // (apart from the block above: the accumulators stay in place)
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                for (int t = 0; t < Sh::NT; ++t) acc[rt][t] *= f[rt];
         }
         at_h8 p[RT];
+        const at_h2 one = {(_Float16)1.f, (_Float16)1.f};
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt) {
-            const float mb = m[rt] - AT_BOOST;
-            float w[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float ex = __builtin_amdgcn_exp2f(x[rt][e >> 2][e & 3] - mb);
-                l[rt] += ex;
-                if constexpr (QUANT) {
-                    constexpr float mid = KIND == BSP_INT8 ? 128.0f : 8.0f;
-                    float wt = ex * (vs[e] * rsig), wo = ex * fmaf(mid, vs[e], vo[e]);
-                    if constexpr (MASKED) {      // a masked row's word may be NaN
-                        const bool see = ok[rt] >> e & 1;
-                        wt = see ? wt : 0.f, wo = see ? wo : 0.f;
-                    }
-                    osum[rt] += wo;
-                    w[e] = wt;
-                } else {
-                    w[e] = ex;
-                }
-            }
-            // to fp16, nearest even: 11 bits of each weight, which average out over the tokens
-#pragma unroll
-            for (int e = 0; e < 8; ++e) p[rt][e] = (_Float16)w[e];
+        for (int e = 0; e < 8; ++e) {
+            float vs, vo;
             if constexpr (QUANT) {
-                const at_h2 one = {(_Float16)1.f, (_Float16)1.f};
+                const float st = kv_word_step(vw[e]);
+                vs = st * rsig, vo = fmaf(KIND == BSP_INT8 ? 128.0f : 8.0f, st, kv_word_offset(vw[e]));
+            }
 #pragma unroll
-                for (int e = 0; e < 8; e += 2)
-                    psum[rt] = __builtin_amdgcn_fdot2(at_h2{p[rt][e], p[rt][e + 1]}, one, psum[rt], false);
+            for (int rt = 0; rt < RT; ++rt) {
+                float w = __builtin_amdgcn_exp2f(x[rt][e >> 2][e & 3]);
+                if constexpr (QUANT) {
+                    l[rt] += w;
+                    osum[rt] = fmaf(w, vo, osum[rt]);
+                    w *= vs;
+                }
+                p[rt][e] = (_Float16)w;          // nearest even: errors of 11 bits that average out over the tokens
             }
         }
-        bool bad = false;
-        if constexpr (MASKED && !QUANT) {
-            // rows past the end: whatever lies there is not a number to multiply with zero
+        // the sum of the rounded weights: what the codes' middle is taken off
+        // with, and (fp16 cache) the row's normalisation
 #pragma unroll
-            for (int t = 0; t < 8; ++t)
+        for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-                for (int i = 0; i < Sh::VW; ++i) {
-                    v[t][i] = j0 + 8 * grp + t < len ? v[t][i] : 0u;
-                    bad |= (v[t][i] & 0x7C00u) == 0x7C00u || (v[t][i] & 0x7C000000u) == 0x7C000000u;
-                }
-            bad = __ballot(bad) != 0;
-        }
-        if (MASKED && !QUANT && bad) {
-            // An infinite or NaN value: out of the product, and NaN in that
-            // channel for the rows that see its token.
-#pragma unroll
-            for (int t = 0; t < Sh::NT; ++t) {
-                at_h8 f = at_v_frag<KIND>(v, t), g;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const _Float16 fe = f[e];
-                    const bool nf = (__builtin_bit_cast(uint16_t, fe) & 0x7C00u) == 0x7C00u;
-                    g[e] = nf ? (_Float16)1.f : (_Float16)0.f;
-                    f[e] = nf ? (_Float16)0.f : fe;
-                }
-#pragma unroll
-                for (int rt = 0; rt < RT; ++rt) {
-                    at_h8 see;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) see[e] = (ok[rt] >> e & 1) ? (_Float16)1.f : (_Float16)0.f;
-                    acc[rt][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f, p[rt], acc[rt][t], 0, 0, 0);
-                    const at_f4 n = __builtin_amdgcn_mfma_f32_16x16x32_f16(g, see, at_f4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) acc[rt][t][r] = n[r] > 0.f ? __builtin_nanf("") : acc[rt][t][r];
-                }
+            for (int e = 0; e < 8; e += 2) {
+                const at_h2 pair = {p[rt][e], p[rt][e + 1]};
+                if constexpr (QUANT)
+                    psum[rt] = __builtin_amdgcn_fdot2(pair, one, psum[rt], false);
+                else
+                    l[rt] = __builtin_amdgcn_fdot2(pair, one, l[rt], false);
             }
-        } else {
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int t = 0; t < Sh::NT; ++t) {
-                const at_h8 f = at_v_frag<KIND>(v, t);
+        for (int t = 0; t < Sh::NT; ++t) {
+            const at_h8 f = at_v_frag<KIND>(v, t);
 #pragma unroll
-                for (int rt = 0; rt < RT; ++rt)
-                    acc[rt][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f, p[rt], acc[rt][t], 0, 0, 0);
-            }
+            for (int rt = 0; rt < RT; ++rt)
+                acc[rt][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f, p[rt], acc[rt][t], 0, 0, 0);
+            if (t & 1) __builtin_amdgcn_sched_barrier(0);
         }
-        load_v(jn);
+        load_v();
     }
 };
 
-// Which sequence and which of its chunks workgroup `ch` of a (kv head, row
-// block) has. A chunk is per tiles of AT_TILE tokens; per follows from all the
-// sequences' lengths, so that chunks are alike whatever the lengths are.
-struct AtPlace {
-    int b, first, count, per;      // sequence; its first chunk's number; its chunks; tiles per chunk
+// The sequences, 64 at a time, one a lane: cached tokens, first and last query
+// row, and tiles of work (at least one where there are query rows).
+struct AtSeqs {
+    int block = -1, len = 0, q0 = 0, q1 = 0, work = 0;
+
+    __device__ __forceinline__ void load(int blk) {
+        if (blk == block) return;
+        block = blk;
+        const AtLate a = at_late();
+        const int b = blk * 64 + (threadIdx.x & 63);
+        len = q0 = q1 = work = 0;
+        if (b < a->B) {
+            len = (int)min((int64_t)max(a->kv_lens[b], 0), a->table_width << a->page_shift);
+            q0 = min(max(a->q_start[b], 0), a->total_q);
+            q1 = min(max(a->q_start[b + 1], q0), a->total_q);
+            work = q1 > q0 ? max(1, (len + AT_TILE - 1) / AT_TILE) : 0;
+        }
+    }
+    __device__ __forceinline__ int of(int v, int b) const { return __builtin_amdgcn_readlane(v, b & 63); }
 };
 
-__device__ __forceinline__ int at_len(const AtArgs &a, int b) {
-    return (int)min((int64_t)max(a.kv_lens[b], 0), a.table_width << a.page_shift);
-}
-
-__device__ __forceinline__ AtPlace at_place(const AtArgs &a, int ch) {
-    const int lane = threadIdx.x & 63;
-    AtPlace p{-1, 0, 1, 1 << 30};
-    if (a.chunks == 0) {           // no split
-        p.b = ch < a.B ? ch : -1;
-        p.first = ch;
-        return p;
-    }
-    int total = 0;
-    for (int b = lane; b < a.B; b += 64) total += (at_len(a, b) + AT_TILE - 1) / AT_TILE;
-    total = bsp_wave_sum(total);
-    p.per = max(a.min_per, (total + a.chunks - 1) / a.chunks);
-    int before = 0;
-    for (int b0 = 0; b0 < a.B; b0 += 64) {
-        const int b = b0 + lane;
-        const int n = b < a.B ? max(1, ((at_len(a, b) + AT_TILE - 1) / AT_TILE + p.per - 1) / p.per) : 0;
-        int s = n;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const int o = __shfl_up(s, d, 64);
-            if (lane >= d) s += o;
-        }
-        const uint64_t hit = __ballot(ch < before + s);
-        if (hit != 0) {
-            const int at = __builtin_ctzll(hit);
-            p.b = b0 + at;
-            p.count = __shfl(n, at, 64);
-            p.first = before + __shfl(s, at, 64) - p.count;
-            return p;
-        }
-        before += __shfl(s, 63, 64);
-    }
-    return p;
-}
-
-template <int KIND, int D, int RT>
-__global__ __launch_bounds__(64 * AT_WAVES) void k_at(const AtArgs a) {
+// One workgroup: a kv head, a block of 16 RT WR query rows, and an equal share
+// of the tiles of all sequences laid end to end (its chunk), which may hold
+// the end of one sequence, whole ones, and the start of another. WR wavefronts
+// side by side take 16 RT rows each of the same tiles (their reads of the
+// cache meet in the CU's L1), 4 / WR such sets take the tiles in turn.
+template <int KIND, int D, int RT, int WR>
+__global__ __launch_bounds__(64 * AT_WAVES, D == 256 ? 1 : 2) void k_at(const AtArgs a) {
     using Sh = AtShape<KIND, D>;
+    using Wave = AtWave<KIND, D, RT, AT_WAVES / WR>;
     extern __shared__ __attribute__((aligned(16))) float at_smem[];
     constexpr int LD = D + 4;                      // floats per row of a wavefront's output in LDS
+    constexpr int WT = AT_WAVES / WR;
     float *s_acc = at_smem;                        // [AT_WAVES][16][LD]
     float *s_m = s_acc + AT_WAVES * 16 * LD;       // [AT_WAVES][16]
     float *s_l = s_m + AT_WAVES * 16;
     int *s_flag = reinterpret_cast<int *>(s_l + AT_WAVES * 16);
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wave = at_uniform(threadIdx.x >> 6), wr = wave % WR, wt = wave / WR;
     // workgroups 8 apart share an XCD and its L2: the row blocks of one piece
     // of the cache are 8 apart
     const int group = blockIdx.x / (8 * a.row_blocks), in = blockIdx.x % (8 * a.row_blocks);
     const int rb = in >> 3, piece = group * 8 + (in & 7);
     const int ch = piece / a.hkv;
     if (ch >= a.max_chunks) return;
-    AtWave<KIND, D, RT> w(a);
+    Wave w(a);
     w.kvh = piece - ch * a.hkv;
-    const AtPlace pl = at_place(a, ch);
-    if (pl.b < 0) return;
-    const int b = __builtin_amdgcn_readfirstlane(pl.b);
-    const int q0 = min(max(a.q_start[b], 0), a.total_q), q1 = min(max(a.q_start[b + 1], q0), a.total_q);
-    const int G = a.hq / a.hkv;
-    const int rows = min(q1 - q0, a.max_q) * G;    // query rows of this kv head
-    const int r0 = rb * 16 * RT;
-    if (r0 >= rows) return;
     w.lane = threadIdx.x & 63, w.col = w.lane & 15, w.grp = w.lane >> 4;
-    w.len = at_len(a, b);
-    w.T = q1 - q0;
-    w.past = w.len - w.T;
-    w.table = a.table + (int64_t)b * a.table_width;
     w.c = a.scale * 1.44269504088896341f;
-    w.sig = 0x1p-100f, w.rsig = 0x1p100f;
-    const int nt = (w.len + AT_TILE - 1) / AT_TILE;
-    const int t0 = min(nt, (ch - pl.first) * pl.per), t1 = min(nt, t0 + min(pl.per, nt));
-    const int tile0 = t0 + wave;
-    if (tile0 < t1) {
-        w.load_pages(tile0 * AT_TILE);
-        w.load_k(tile0 * AT_TILE);
-        w.load_v(tile0 * AT_TILE);
-    }
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-        const int row = r0 + 16 * rt + w.col;
-        const bool in_rows = row < rows;
-        const int t = in_rows ? row / G : 0, g = in_rows ? row - t * G : 0;
-        const uint16_t *src = a.Q + (int64_t)(q0 + t) * a.q_stride + (int64_t)(w.kvh * G + g) * D + w.grp * (D / 4);
-        uint32_t qr[D / 8];
-        if (a.q_vec) {
-            at_load(reinterpret_cast<const uint8_t *>(src), qr);
-        } else {
-#pragma unroll
-            for (int i = 0; i < D / 8; ++i) qr[i] = (uint32_t)src[2 * i] | ((uint32_t)src[2 * i + 1] << 16);
+    w.q_lds = reinterpret_cast<at_h8 *>(at_smem) + wr * (RT * Sh::STEPS * 64);
+    const int G = a.hq / a.hkv;
+    const int r0 = (rb * WR + wr) * 16 * RT;       // the wavefront's first row
+
+    // the chunk's first sequence, and where that one's tiles begin
+    AtSeqs seqs;
+    int b = ch, begin = 0, per = 0, pos = 0, end = 0;
+    if (a.chunks == 0) {                           // no split: a workgroup per sequence
+        seqs.load(b >> 6);
+        end = seqs.of(seqs.work, b);
+        per = max(end, 1);
+    } else {
+        int total = 0;
+        for (int k = (a.B - 1) >> 6; k >= 0; --k) {
+            seqs.load(k);
+            total += bsp_wave_sum(seqs.work);
         }
-        float sum = 0.f;
+        total = at_uniform(total);
+        per = max(a.min_per, (total + a.chunks - 1) / a.chunks);
+        pos = ch * per, end = min(total, pos + per);
+        if (pos >= end) return;
+        int before = 0;
+        for (int k = 0;; ++k) {
+            seqs.load(k);
+            int s = seqs.work;
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-            if (!in_rows) qr[i] = 0u;
-            const at_h2 h = __builtin_bit_cast(at_h2, qr[i]);
-            sum += (float)h.x + (float)h.y;
+            for (int d = 1; d < 64; d <<= 1) {
+                const int o = __shfl_up(s, d, 64);
+                if (w.lane >= d) s += o;
+            }
+            const uint64_t hit = __ballot(pos < before + s);
+            if (hit != 0) {
+                b = __builtin_ctzll(hit);
+                begin = before + seqs.of(s, b) - seqs.of(seqs.work, b);
+                b += 64 * k;
+                break;
+            }
+            before += seqs.of(s, 63);
         }
-        w.qc[rt] = at_group_sum(sum) * w.c;
-#pragma unroll
-        for (int s = 0; s < Sh::STEPS; ++s) w.q[rt][s] = at_q_frag<KIND>(qr, s);
-        w.seen[rt] = a.mask != nullptr ? a.mask[q0 + t] : (uint64_t)-1 >> (63 - min(t, 63));
-        w.m[rt] = AT_LOW, w.l[rt] = 0.f, w.osum[rt] = 0.f, w.psum[rt] = 0.f;
-#pragma unroll
-        for (int i = 0; i < Sh::NT; ++i) w.acc[rt][i] = at_f4{0.f, 0.f, 0.f, 0.f};
-    }
-    for (int t = tile0; t < t1; t += AT_WAVES) {
-        const int j0 = t * AT_TILE, jn = (t + AT_WAVES < t1 ? t + AT_WAVES : t) * AT_TILE;
-        if (j0 + AT_TILE <= w.past)
-            w.template tile<false>(j0, jn);
-        else
-            w.template tile<true>(j0, jn);
     }
 
-    // Join the wavefronts, row tile by row tile; then write the rows, or post
-    // them for the last workgroup of the sequence to join.
-    const int unit = (b * a.hkv + w.kvh) * a.row_blocks + rb;
-    const uint32_t slot_bytes = 16u * RT * (D + 4) * 4u;     // [row][D] sums, then [row] (m, l, 0, 0)
-    const int64_t slot = (int64_t)ch * a.hkv * a.row_blocks + w.kvh * a.row_blocks + rb;
-    const bool split = pl.count > 1;
-    const int chunk = 16 * D / 8;                            // 8-channel pieces of a row tile
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-        if (r0 + 16 * rt >= rows) break;
-        if (rt > 0) __syncthreads();
-        const float l = at_group_sum(w.l[rt]);
-        float os = 0.f, ps = 0.f, up = 1.f;
-        if constexpr (AtWave<KIND, D, RT>::QUANT) {
-            os = at_group_sum(w.osum[rt]);
-            ps = at_group_sum(w.psum[rt]) * (KIND == BSP_INT8 ? 128.0f : 8.0f);
-            up = 16777216.0f;
+    for (; pos < end; ++b) {
+        const AtLate as = at_late();
+        seqs.load(b >> 6);
+        const int work = seqs.of(seqs.work, b);
+        if (work == 0) continue;
+        const int q0 = seqs.of(seqs.q0, b), T = seqs.of(seqs.q1, b) - q0;
+        const int rows = min(T, as->max_q) * G;      // query rows of this kv head
+        w.len = seqs.of(seqs.len, b);
+        w.past = w.len - T;
+        w.table = as->table + (int64_t)b * as->table_width;
+        const int nt = (w.len + AT_TILE - 1) / AT_TILE;
+        const int t0 = min(nt, pos - begin), t1 = min(nt, end - begin);
+        // chunks that hold tiles of the sequence, and this one's place for its part
+        const int c0 = begin / per, count = as->chunks == 0 ? 1 : (begin + work - 1) / per - c0 + 1;
+        begin += work;
+        pos = begin;
+        if (rb * WR * 16 * RT >= rows) continue;
+        const int tile0 = t0 + wt;
+        if (tile0 < t1) {
+            w.load_pages(tile0);
+            w.set_tile(0, tile0 * AT_TILE);
+            w.load_k();
+            w.load_v();
         }
-        if (w.grp == 0) s_m[wave * 16 + w.col] = w.m[rt], s_l[wave * 16 + w.col] = l;
-        float *o = s_acc + (wave * 16 + w.col) * LD;
+        w.sig = 0x1p-100f, w.rsig = 0x1p100f;
+        if constexpr (Wave::Q_LDS) __syncthreads();      // the LDS area's last readers
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
+        for (int rt = 0; rt < RT; ++rt) {
+            const int row = r0 + 16 * rt + w.col;
+            const bool in_rows = row < rows;
+            const int t = in_rows ? row / G : 0, g = in_rows ? row - t * G : 0;
+            const uint16_t *src = as->Q + (int64_t)(q0 + t) * as->q_stride + (int64_t)(w.kvh * G + g) * D;
+            uint32_t qr[D / 8];                    // the channels of the lane's K pieces
 #pragma unroll
-            for (int t = 0; t < Sh::NT; t += 4) {
-                at_f4 y;
+            for (int j = 0; j < Sh::PIECES; ++j) {
+                const uint16_t *sp = src + (4 * j + w.grp) * Sh::PCH;
+                uint32_t piece[Sh::PCH / 2];
+                if (as->q_vec) {
+                    at_load(reinterpret_cast<const uint8_t *>(sp), piece);
+                } else {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    float z = w.acc[rt][t + i][r];
-                    if constexpr (AtWave<KIND, D, RT>::QUANT) {
-                        const float h = KIND == BSP_INT4 && (i & 1) ? up * 0.0625f : up;
-                        z = fmaf(w.sig, fmaf(z, h, -ps), os);
-                    }
-                    y[i] = z;
+                    for (int i = 0; i < Sh::PCH / 2; ++i) piece[i] = (uint32_t)sp[2 * i] | ((uint32_t)sp[2 * i + 1] << 16);
                 }
-                *reinterpret_cast<at_f4 *>(o + (4 * w.grp + r) * Sh::NT + t) = y;
+#pragma unroll
+                for (int i = 0; i < Sh::PCH / 2; ++i) qr[j * (Sh::PCH / 2) + i] = piece[i];
             }
+            float sum = 0.f;
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) {
+                if (!in_rows) qr[i] = 0u;
+                const at_h2 h = __builtin_bit_cast(at_h2, qr[i]);
+                sum += (float)h.x + (float)h.y;
+            }
+            w.qc[rt] = at_group_sum(sum) * w.c;
+#pragma unroll
+            for (int s = 0; s < Sh::STEPS; ++s) {
+                if constexpr (Wave::Q_LDS) {
+                    if (rt % WT == wt)                   // shared by the WT wavefronts of these rows
+                        const_cast<at_h8 *>(w.q_lds)[(rt * Sh::STEPS + s) * 64 + w.lane] = at_q_frag<KIND>(qr, s);
+                } else {
+                    w.q[rt][s] = at_q_frag<KIND>(qr, s);
+                }
+            }
+            w.seen[rt] = as->mask != nullptr ? as->mask[q0 + t] : (uint64_t)-1 >> (63 - min(t, 63));
+            w.mb[rt] = 0.f, w.limit[rt] = AT_NONE, w.l[rt] = 0.f, w.osum[rt] = 0.f, w.psum[rt] = 0.f;
+#pragma unroll
+            for (int i = 0; i < Sh::NT; ++i) w.acc[rt][i] = at_f4{0.f, 0.f, 0.f, 0.f};
+        }
+        if constexpr (Wave::Q_LDS) __syncthreads();
+        for (int t = tile0, i = 1; t < t1; t += WT, ++i) {
+            if (t + WT < t1) {         // (past the last tile its own rows are loaded again, unused)
+                if ((i & 31) == 0) w.load_pages(t + WT);
+                w.set_tile(i, (t + WT) * AT_TILE);
+            }
+            w.tile(t * AT_TILE);
+        }
+
+        const AtLate ap = at_late();
+        // Join the wavefronts of each row tile, one row tile of each at a time;
+        // then write the rows, or post them for the sequence's last chunk to join.
+        const bool split = count > 1;
+        constexpr int ROWS = 16 * RT * WR;
+        constexpr uint32_t slot_floats = ROWS * (D + 4);     // [row][D] sums, then [row] (m, l, 0, 0)
+        const int64_t head = (int64_t)w.kvh * ap->row_blocks + rb, heads = (int64_t)ap->hkv * ap->row_blocks;
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+            __syncthreads();                             // the LDS area's last readers
+            const float l = at_group_sum(w.l[rt]);
+            float os = 0.f, ps = 0.f, up = 1.f;
+            if constexpr (Wave::QUANT) {
+                os = at_group_sum(w.osum[rt]);
+                ps = at_group_sum(w.psum[rt]) * (KIND == BSP_INT8 ? 128.0f : 8.0f);
+                up = 16777216.0f;
+            }
+            if (w.grp == 0) {
+                s_m[wave * 16 + w.col] = w.limit[rt] == AT_NONE ? AT_LOW : w.mb[rt];
+                s_l[wave * 16 + w.col] = l;
+            }
+            float *o = s_acc + (wave * 16 + w.col) * LD;
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+#pragma unroll
+                for (int t = 0; t < Sh::NT; t += 4) {
+                    at_f4 y;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        float z = w.acc[rt][t + i][r];
+                        if constexpr (Wave::QUANT) {
+                            const float h = KIND == BSP_INT4 && (i & 1) ? up * 0.0625f : up;
+                            z = fmaf(w.sig, fmaf(z, h, -ps), os);
+                        }
+                        y[i] = z;
+                    }
+                    *reinterpret_cast<at_f4 *>(o + (4 * w.grp + r) * Sh::NT + t) = y;
+                }
+            __syncthreads();
+            for (int i = threadIdx.x; i < WR * 16 * (D / 8); i += 64 * AT_WAVES) {
+                const int d = (i % (D / 8)) * 8, row = i / (D / 8) % 16, g = i / (D / 8) / 16;   // g: the row group
+                const int rl = g * 16 * RT + 16 * rt + row, ri = rb * ROWS + rl;
+                if (ri >= rows) continue;
+                float mx = s_m[g * 16 + row];
+#pragma unroll
+                for (int k = 1; k < WT; ++k) mx = fmaxf(mx, s_m[(k * WR + g) * 16 + row]);
+                at_f4 y0 = {0.f, 0.f, 0.f, 0.f}, y1 = y0;
+                float lt = 0.f;
+#pragma unroll
+                for (int k = 0; k < WT; ++k) {
+                    const int at = (k * WR + g) * 16 + row;
+                    const float f = __builtin_amdgcn_exp2f(s_m[at] - mx);
+                    lt = fmaf(s_l[at], f, lt);
+                    const at_f4 *src = reinterpret_cast<const at_f4 *>(s_acc + at * LD + d);
+                    const at_f4 z0 = src[0], z1 = src[1];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) y0[e] = fmaf(z0[e], f, y0[e]), y1[e] = fmaf(z1[e], f, y1[e]);
+                }
+                if (split) {
+                    const int64_t slot = (2 * (int64_t)ch + (ch == c0)) * heads + head;
+                    const __amdgpu_buffer_rsrc_t rs = bsp_rsrc(ap->part + slot * slot_floats, slot_floats * 4);
+                    const uint32_t at = ((uint32_t)rl * D + d) * 4u;
+                    at_ws_store(rs, at, y0), at_ws_store(rs, at + 16, y1);
+                    if (d == 0) at_ws_store(rs, (uint32_t)(ROWS * D + 4 * rl) * 4u, at_f4{mx, lt, 0.f, 0.f});
+                } else {
+                    at_write(ap, q0, w.kvh, G, ri, d, D, y0, y1, lt == 0.f ? 0.f : 1.0f / lt);
+                }
+            }
+        }
+        if (!split || ap->join) continue;
+        const int64_t unit = (int64_t)b * heads + head;
+        __builtin_amdgcn_s_waitcnt(0);      // this thread's partial stores completed
         __syncthreads();
-        for (int i = threadIdx.x; i < chunk; i += 64 * AT_WAVES) {
+        if (threadIdx.x == 0)
+            *s_flag = (int)__hip_atomic_fetch_add(&ap->counters[unit], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        __syncthreads();
+        if (*s_flag != count - 1) continue;
+        for (int i = threadIdx.x; i < min(ROWS, rows - rb * ROWS) * (D / 8); i += 64 * AT_WAVES) {
             const int row = i / (D / 8), d = (i % (D / 8)) * 8;
-            const int ri = r0 + 16 * rt + row;
-            if (ri >= rows) continue;
-            float mx = s_m[row];
-#pragma unroll
-            for (int k = 1; k < AT_WAVES; ++k) mx = fmaxf(mx, s_m[k * 16 + row]);
-            at_f4 y0 = {0.f, 0.f, 0.f, 0.f}, y1 = y0;
-            float lt = 0.f;
-#pragma unroll
-            for (int k = 0; k < AT_WAVES; ++k) {
-                const float f = __builtin_amdgcn_exp2f(s_m[k * 16 + row] - mx);
-                lt = fmaf(s_l[k * 16 + row], f, lt);
-                const at_f4 *src = reinterpret_cast<const at_f4 *>(s_acc + (k * 16 + row) * LD + d);
-                const at_f4 z0 = src[0], z1 = src[1];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) y0[e] = fmaf(z0[e], f, y0[e]), y1[e] = fmaf(z1[e], f, y1[e]);
-            }
-            if (split) {
-                const __amdgpu_buffer_rsrc_t rs = bsp_rsrc(a.part + slot * (slot_bytes / 4), slot_bytes);
-                const uint32_t at = ((uint32_t)(16 * rt + row) * D + d) * 4u;
-                at_ws_store(rs, at, y0), at_ws_store(rs, at + 16, y1);
-                if (d == 0) at_ws_store(rs, (16u * RT * D + 4u * (16 * rt + row)) * 4u, at_f4{mx, lt, 0.f, 0.f});
-            } else {
-                const float inv = lt == 0.f ? 0.f : 1.0f / lt;
-                at_write(a, q0, w.kvh, G, ri, d, D, y0, y1, inv);
-            }
+            const uint32_t at = ((uint32_t)row * D + d) * 4u, at_ml = (uint32_t)(ROWS * D + 4 * row) * 4u;
+            AtSum sum;
+            for (int s = 0; s < count; ++s)        // in chunk order
+                sum.add(ap->part + ((2 * (int64_t)(c0 + s) + (s == 0)) * heads + head) * slot_floats, slot_floats * 4, at, at_ml);
+            at_write(ap, q0, w.kvh, G, rb * ROWS + row, d, D, sum.y0, sum.y1, sum.l == 0.f ? 0.f : 1.0f / sum.l);
         }
+        if (threadIdx.x == 0) __hip_atomic_store(&ap->counters[unit], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
-    if (!split) return;
-    __builtin_amdgcn_s_waitcnt(0);      // this thread's partial stores completed
-    __syncthreads();
-    if (threadIdx.x == 0)
-        *s_flag = (int)__hip_atomic_fetch_add(&a.counters[unit], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    __syncthreads();
-    if (*s_flag != pl.count - 1) return;
-    const int64_t stride = (int64_t)a.hkv * a.row_blocks * (slot_bytes / 4);
-    const float *base = a.part + (int64_t)pl.first * stride + (int64_t)(w.kvh * a.row_blocks + rb) * (slot_bytes / 4);
-    for (int i = threadIdx.x; i < min(16 * RT, rows - r0) * (D / 8); i += 64 * AT_WAVES) {
-        const int row = i / (D / 8), d = (i % (D / 8)) * 8;
-        const uint32_t at = ((uint32_t)row * D + d) * 4u, at_ml = (16u * RT * D + 4u * row) * 4u;
-        at_f4 y0 = {0.f, 0.f, 0.f, 0.f}, y1 = y0;
-        float mx = AT_LOW, lt = 0.f;
-        for (int s = 0; s < pl.count; ++s) {      // in chunk order
-            const __amdgpu_buffer_rsrc_t rs = bsp_rsrc(base + s * stride, slot_bytes);
-            const at_f4 ml = at_ws_load(rs, at_ml), z0 = at_ws_load(rs, at), z1 = at_ws_load(rs, at + 16);
-            const float mn = fmaxf(mx, ml.x);
-            const float f = __builtin_amdgcn_exp2f(mx - mn), g = __builtin_amdgcn_exp2f(ml.x - mn);
-            mx = mn;
-            lt = lt * f + ml.y * g;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) y0[e] = y0[e] * f + z0[e] * g, y1[e] = y1[e] * f + z1[e] * g;
-        }
-        at_write(a, q0, w.kvh, G, r0 + row, d, D, y0, y1, lt == 0.f ? 0.f : 1.0f / lt);
-    }
-    if (threadIdx.x == 0) __hip_atomic_store(&a.counters[unit], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-// The plan of a call: query rows per workgroup, row blocks, and how many
-// pieces the cached tokens of all sequences are cut into.
+// Joins the posted parts of split sequences: a workgroup takes 4 rows of a
+// (sequence, kv head), its wavefronts every fourth chunk; their sums meet in
+// LDS, in wavefront order. ROWS: rows of a row block.
+template <int D>
+__global__ __launch_bounds__(64 * AT_WAVES) void k_at_join(const AtArgs a, int ROWS) {
+    constexpr int P = D / 8, RW = 64 / P;          // 8-channel pieces of a row; rows of a wavefront's 64 lanes
+    __shared__ __attribute__((aligned(16))) float s_y[AT_WAVES][64][8];
+    __shared__ float s_ml[AT_WAVES][64][2];
+    const int lane = threadIdx.x & 63, wave = at_uniform(threadIdx.x >> 6);
+    const int b = blockIdx.z, kvh = blockIdx.y, row = blockIdx.x * RW + lane / P, d = (lane % P) * 8;
+    // the sequence's chunks, as the main kernel cuts them
+    AtSeqs seqs;
+    int total = 0, begin = 0;
+    for (int k = (a.B - 1) >> 6; k >= 0; --k) {
+        seqs.load(k);
+        total += bsp_wave_sum(seqs.work);
+        begin += bsp_wave_sum(k * 64 + lane < b ? seqs.work : 0);
+    }
+    seqs.load(b >> 6);
+    const int work = seqs.of(seqs.work, b), q0 = seqs.of(seqs.q0, b), T = seqs.of(seqs.q1, b) - q0;
+    const int G = a.hq / a.hkv, rows = min(T, a.max_q) * G;
+    total = at_uniform(total), begin = at_uniform(begin);
+    const int per = max(a.min_per, (total + a.chunks - 1) / a.chunks);
+    const int c0 = begin / per, count = work == 0 ? 0 : (begin + work - 1) / per - c0 + 1;
+    if (count <= 1 || (int)blockIdx.x * RW >= rows) return;
+    const int64_t heads = (int64_t)a.hkv * a.row_blocks, head = (int64_t)kvh * a.row_blocks + row / ROWS;
+    const uint32_t slot_floats = (uint32_t)ROWS * (D + 4), rl = (uint32_t)(row % ROWS);
+    AtSum sum;
+    if (row < rows) {
+#pragma unroll 4
+        for (int s = wave; s < count; s += AT_WAVES)
+            sum.add(a.part + ((2 * (int64_t)(c0 + s) + (s == 0)) * heads + head) * slot_floats, slot_floats * 4,
+                    (rl * D + d) * 4u, (ROWS * D + 4 * rl) * 4u);
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s_y[wave][lane][e] = sum.y0[e], s_y[wave][lane][4 + e] = sum.y1[e];
+    s_ml[wave][lane][0] = sum.m, s_ml[wave][lane][1] = sum.l;
+    __syncthreads();
+    if (wave != 0 || row >= rows) return;
+#pragma unroll
+    for (int k = 1; k < AT_WAVES; ++k) {
+        at_f4 z0, z1;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) z0[e] = s_y[k][lane][e], z1[e] = s_y[k][lane][4 + e];
+        sum.add(z0, z1, s_ml[k][lane][0], s_ml[k][lane][1]);
+    }
+    at_write(at_late(), q0, kvh, G, row, d, D, sum.y0, sum.y1, sum.l == 0.f ? 0.f : 1.0f / sum.l);
+}
+
+// The plan of a call: row tiles per wavefront, wavefronts side by side, row
+// blocks, and how many chunks the tiles of all sequences are cut into.
 struct AtPlan {
-    int rt, row_blocks, chunks, min_per, max_chunks;
+    int rt, wr, row_blocks, chunks, min_per, max_chunks, join;
     int64_t ws_bytes;
 };
 
 #define AT_WS_COUNTERS 16384           // arrival counters at the start of a workspace
-#define AT_GROUPS 768                  // workgroups aimed at: three a CU
 
 AtPlan at_plan(const bsp_kv_cache *c, int64_t table_width, int64_t B, int64_t max_q, int64_t hq, bool split) {
     AtPlan p{};
     const int64_t rows = max_q * (hq / c->kv_heads);
     p.rt = rows <= 16 || c->head_dim == 256 ? 1 : 2;
-    p.row_blocks = (int)((rows + 16 * p.rt - 1) / (16 * p.rt));
+    p.wr = rows <= 16 * p.rt ? 1 : rows <= 32 * p.rt ? 2 : 4;
+    p.row_blocks = (int)((rows + 16 * p.rt * p.wr - 1) / (16 * p.rt * p.wr));
     p.max_chunks = (int)B;
-    p.min_per = 8;
-    const int64_t per_chunk = c->kv_heads * p.row_blocks;
+    p.min_per = AT_MINPER;
+    const int64_t heads = c->kv_heads * p.row_blocks;
     const int64_t tiles = (table_width * c->page_size + AT_TILE - 1) / AT_TILE;      // of the longest sequence
-    if (split && B * per_chunk <= AT_WS_COUNTERS && tiles > p.min_per) {
-        const int64_t want = (AT_GROUPS + per_chunk - 1) / per_chunk;
-        const int64_t most = B * ((tiles + p.min_per - 1) / p.min_per);
-        if (2 * want > B) {
-            p.chunks = (int)std::min(want, most);
-            p.max_chunks = (int)(p.chunks + B);
-            p.ws_bytes = AT_WS_COUNTERS * 4 + (int64_t)p.max_chunks * per_chunk * 16 * p.rt * (c->head_dim + 4) * 4;
-        }
+    if (split && B * heads <= AT_WS_COUNTERS) {
+        const int64_t want = std::max<int64_t>(1, AT_GROUPS / heads);
+        const int64_t most = B * std::max<int64_t>(1, (tiles + p.min_per - 1) / p.min_per);
+        p.chunks = p.max_chunks = (int)std::min(want, most);
+        p.join = p.chunks > B && (rows > 16 || p.chunks > 8 * B);
+        p.ws_bytes = AT_WS_COUNTERS * 4 + 2 * p.chunks * heads * 16 * p.rt * p.wr * (c->head_dim + 4) * 4;
     }
     return p;
 }
 
-template <int KIND, int D, int RT>
+template <int KIND, int D, int RT, int WR>
 void at_launch_t(const AtArgs &a, hipStream_t stream) {
+    static_assert(sizeof(AtArgs) <= 512, "the kernels read their arguments in place");
     const size_t lds = (size_t)(AT_WAVES * 16 * (D + 4) + 2 * AT_WAVES * 16 + 4) * 4;
     const int64_t pieces = ((int64_t)a.max_chunks * a.hkv + 7) / 8 * 8;
-    (void)hipFuncSetAttribute((const void *)k_at<KIND, D, RT>, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
-    hipLaunchKernelGGL((k_at<KIND, D, RT>), dim3((unsigned)(pieces * a.row_blocks)), dim3(64 * AT_WAVES), lds, stream, a);
+    if (lds > 65536)
+        (void)hipFuncSetAttribute((const void *)k_at<KIND, D, RT, WR>, hipFuncAttributeMaxDynamicSharedMemorySize,
+                                  (int)lds);
+    hipLaunchKernelGGL((k_at<KIND, D, RT, WR>), dim3((unsigned)(pieces * a.row_blocks)), dim3(64 * AT_WAVES), lds,
+                       stream, a);
+    if (a.join) {
+        const int rw = 64 / (D / 8), rows = a.max_q * (a.hq / a.hkv);
+        hipLaunchKernelGGL((k_at_join<D>), dim3((rows + rw - 1) / rw, a.hkv, a.B), dim3(64 * AT_WAVES), 0, stream, a,
+                           16 * RT * WR);
+    }
+}
+
+template <int KIND, int D>
+void at_launch_r(const AtArgs &a, const AtPlan &p, hipStream_t stream) {
+    constexpr int RT = D == 256 ? 1 : 2;           // row tiles of a wavefront past one
+    if (p.wr == 4)
+        at_launch_t<KIND, D, RT, 4>(a, stream);
+    else if (p.wr == 2)
+        at_launch_t<KIND, D, RT, 2>(a, stream);
+    else if (p.rt == 1)
+        at_launch_t<KIND, D, 1, 1>(a, stream);
+    else
+        at_launch_t<KIND, D, RT, 1>(a, stream);
 }
 
 template <int KIND>
-void at_launch(const AtArgs &a, int64_t D, int rt, hipStream_t stream) {
-    if (D == 64) {
-        if (rt == 1) at_launch_t<KIND, 64, 1>(a, stream); else at_launch_t<KIND, 64, 2>(a, stream);
-    } else if (D == 128) {
-        if (rt == 1) at_launch_t<KIND, 128, 1>(a, stream); else at_launch_t<KIND, 128, 2>(a, stream);
-    } else {
-        at_launch_t<KIND, 256, 1>(a, stream);
-    }
+void at_launch(const AtArgs &a, int64_t D, const AtPlan &p, hipStream_t stream) {
+    if (D == 64)
+        at_launch_r<KIND, 64>(a, p, stream);
+    else if (D == 128)
+        at_launch_r<KIND, 128>(a, p, stream);
+    else
+        at_launch_r<KIND, 256>(a, p, stream);
 }
 
 // Checks shared by the call and its workspace size.
@@ -737,14 +942,14 @@ extern "C" int attention_tree_f16(const uint16_t *Q, int64_t q_stride, const bsp
     a.B = (int)B;
     a.q_vec = ((uintptr_t)Q & 15u) == 0 && (q_stride & 7) == 0;
     a.o_vec = ((uintptr_t)O & 15u) == 0 && (o_stride & 7) == 0;
-    a.row_blocks = p.row_blocks, a.chunks = p.chunks, a.min_per = p.min_per, a.max_chunks = p.max_chunks;
+    a.row_blocks = p.row_blocks, a.chunks = p.chunks, a.min_per = p.min_per, a.max_chunks = p.max_chunks, a.join = p.join;
     a.counters = (uint32_t *)workspace;
     a.part = p.ws_bytes > 0 ? (float *)((uint8_t *)workspace + AT_WS_COUNTERS * 4) : nullptr;
     if (cache->dtype == BSP_FP16)
-        at_launch<BSP_FP16>(a, cache->head_dim, p.rt, stream);
+        at_launch<BSP_FP16>(a, cache->head_dim, p, stream);
     else if (cache->dtype == BSP_INT8)
-        at_launch<BSP_INT8>(a, cache->head_dim, p.rt, stream);
+        at_launch<BSP_INT8>(a, cache->head_dim, p, stream);
     else
-        at_launch<BSP_INT4>(a, cache->head_dim, p.rt, stream);
+        at_launch<BSP_INT4>(a, cache->head_dim, p, stream);
     return hipGetLastError() == hipSuccess ? BSP_OK : BSP_E_HIP;
 }

@@ -57,22 +57,43 @@ struct LoraAdd {
     }
 };
 
-// t[n][r]: one wavefront per (n, r); rows past the rank and tokens without an
-// adapter give zero.
-__global__ __launch_bounds__(256) void k_lora_down(const LoraArgs a, const uint16_t *__restrict__ X, int N, int K) {
-    const int w = blockIdx.x * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
-    const int n = w / a.R, r = w - n * a.R;
-    if (n >= N) return;
+// t[n][r]: one workgroup per (r, n); its wavefronts take pieces of 512
+// channels in turn, so that a row of 4096 is two 16-byte loads a lane, all in
+// flight at once. Rows past the rank and tokens without an adapter give zero.
+// VEC: the rows of A and X lie on 16-byte boundaries (else element by element).
+#define LORA_WAVES 4
+
+template <bool VEC>
+__global__ __launch_bounds__(64 * LORA_WAVES) void k_lora_down(const LoraArgs a, const uint16_t *__restrict__ X, int K) {
+    const int r = blockIdx.x, n = blockIdx.y, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    __shared__ float part[LORA_WAVES];
     int rank;
     const int i = lora_of(a, n, &rank);
     float s = 0.f;
     if (r < rank) {
         const uint16_t *row = a.A + ((int64_t)i * a.R + r) * K, *x = X + (int64_t)n * K;
-        for (int k = lane; k < K; k += 64) s += bsp_h2f(row[k]) * bsp_h2f(x[k]);
+        if constexpr (VEC) {
+#pragma unroll 4
+            for (int k = threadIdx.x * 8; k < K; k += 64 * LORA_WAVES * 8) {
+                const lora_h8 u = *reinterpret_cast<const lora_h8 *>(row + k);
+                const lora_h8 v = *reinterpret_cast<const lora_h8 *>(x + k);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) s = fmaf((float)u[j], (float)v[j], s);
+            }
+        } else {
+            for (int k = threadIdx.x; k < K; k += 64 * LORA_WAVES) s = fmaf(bsp_h2f(row[k]), bsp_h2f(x[k]), s);
+        }
         s = bsp_wave_sum(s);
-        if (a.scale != nullptr) s *= a.scale[i];
     }
-    if (lane == 0) a.t[(int64_t)n * a.R + r] = s;
+    if (lane == 0) part[wave] = s;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        s = part[0];
+#pragma unroll
+        for (int w = 1; w < LORA_WAVES; ++w) s += part[w];
+        if (r < rank && a.scale != nullptr) s *= a.scale[i];
+        a.t[(int64_t)n * a.R + r] = s;
+    }
 }
 
 // The dequantised int32 sums with the adapters' part, rounded once.

@@ -754,7 +754,11 @@ LoraArgs lora_args(const bsp_lora *l, void *t) {
 }
 
 void launch_lora_down(const LoraArgs &a, const uint16_t *X, int64_t N, int64_t K, hipStream_t stream) {
-    hipLaunchKernelGGL(k_lora_down, dim3((unsigned)((N * a.R + 3) / 4)), dim3(256), 0, stream, a, X, (int)N, (int)K);
+    const dim3 grid((unsigned)a.R, (unsigned)N), block(64 * LORA_WAVES);
+    if (K % 8 == 0 && ((uintptr_t)X & 15u) == 0)
+        hipLaunchKernelGGL(k_lora_down<true>, grid, block, 0, stream, a, X, (int)K);
+    else
+        hipLaunchKernelGGL(k_lora_down<false>, grid, block, 0, stream, a, X, (int)K);
 }
 
 }  // namespace

@@ -532,9 +532,9 @@ int kv_cache_gather(const bsp_kv_cache *cache, const int64_t *slots, int64_t n, 
  *   O[row][h] = sum_j softmax_j(scale * Q[row][h] . k_j) v_j over the visible
  *   tokens j, k_j and v_j the rows of kv head h / (q_heads / kv_heads) as the
  *   cache stands for them. A row that sees no token gives zeros. What lies in
- *   the cache at tokens a row does not see, NaN included, has no effect on it;
- *   in an fp16 cache a channel of a seen drafted token's v that is infinite or
- *   NaN gives NaN in that channel.
+ *   the cache at tokens a row does not see, NaN included, has no effect on it.
+ *   A seen drafted token whose v row holds an infinity or a NaN makes the whole
+ *   output row NaN.
  * Scores, softmax statistics and sums are fp32, the exponentials enter the
  * second product as fp16 (their scale chosen so that they stay normal numbers
  * down to 2^-20 of the largest), one rounding to fp16 at the end. Partial sums
