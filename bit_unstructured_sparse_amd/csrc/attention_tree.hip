@@ -24,9 +24,10 @@ struct AtArgs {
     int64_t o_stride;
     int total_q, max_q, hq, hkv, num_pages, page_shift, B;
     int q_vec, o_vec;              // Q / O rows on 16-byte boundaries
-    int row_blocks;                // blocks of query rows
-    int chunks, min_per, max_chunks;   // chunks (0: one per sequence), least tiles of one, chunks launched
-    float scale;
+    int unit_rows;                 // query rows a wavefront takes
+    int row_blocks, slot_rows;     // blocks of query rows; rows of one in the partial sums
+    int chunks, min_per, max_chunks;   // chunks (0: one per sequence), least work of one, chunks launched
+    float scale, inv_group;        // inv_group: 1 / (query heads per kv head)
     int join;                      // partial sums are joined by k_at_join, not by the last chunk
     float *part;                   // partial sums, two places per chunk, kv head and row block
     uint32_t *counters;            // arrivals per (sequence, kv head, row block), zero between calls
@@ -44,10 +45,14 @@ __device__ __forceinline__ AtLate at_late() {
     return p;
 }
 
+// The quotient of a query row by the group size, by the host's reciprocal:
+// exact below 2^21 rows.
+__device__ __forceinline__ int at_div(int row, float inv) { return (int)(((float)row + 0.5f) * inv); }
+
 // 8 channels of a finished row: sums times inv, rounded to fp16.
 __device__ __forceinline__ void at_write(AtLate ap, int q0, int kvh, int G, int row, int d, int D, at_f4 y0,
                                          at_f4 y1, float inv) {
-    const int t = row / G, g = row - t * G;
+    const int t = at_div(row, ap->inv_group), g = row - t * G;
     uint16_t *o = ap->O + (int64_t)(q0 + t) * ap->o_stride + (int64_t)(kvh * G + g) * D + d;
     uint16_t h[8];
 #pragma unroll
@@ -69,19 +74,12 @@ typedef _Float16 at_h2 __attribute__((ext_vector_type(2)));
 #ifndef AT_GROUPS
 #define AT_GROUPS 512
 #endif
-#ifndef AT_OCC1
-#define AT_OCC1 2
-#endif
-#ifndef AT_OCC4
-#define AT_OCC4 2
-#endif
-#ifndef AT_MINPER
-#define AT_MINPER 8
-#endif
 #define AT_WAVES 4
 #define AT_TILE 32                 // cached tokens per wavefront and step
 #define AT_BOOST 6.0f              // log2: the weights' scale, 2^6 at the running maximum
 #define AT_SLACK 8.0f              // log2: how far a score may pass the running maximum before it is moved
+// Query rows of a row block: 16 where a call has no more, else four wavefronts of 16 RT.
+#define AT_ROWS(RT) ((RT) == 1 ? (D == 256 ? 64 : 16) : 64 * (RT))
 #define AT_LOW -1e30f              // stands for the maximum of no scores when sums are joined
 #define AT_NONE -3e38f
 
@@ -211,25 +209,39 @@ __device__ __forceinline__ at_h8 at_v_frag(const uint32_t (&v)[8][VW], int t) {
     return __builtin_bit_cast(at_h8, f);
 }
 
-__device__ __forceinline__ float at_group_sum(float v) {      // over the four lanes of a query row
-    v += __shfl_xor(v, 16, 64);
-    return v + __shfl_xor(v, 32, 64);
+// Over the four lanes of a query row (16 apart): swaps of halves and of
+// 16-lane rows leave a lane's value and its partner's in the two results.
+template <class F>
+__device__ __forceinline__ float at_group(float v, F f) {
+    const uint32_t u = __builtin_bit_cast(uint32_t, v);
+    const auto h = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    const uint32_t h0 = h[0], h1 = h[1];
+    const uint32_t w = __builtin_bit_cast(uint32_t, f(__builtin_bit_cast(float, h0), __builtin_bit_cast(float, h1)));
+    const auto q = __builtin_amdgcn_permlane16_swap(w, w, false, false);
+    const uint32_t q0 = q[0], q1 = q[1];
+    return f(__builtin_bit_cast(float, q0), __builtin_bit_cast(float, q1));
+}
+__device__ __forceinline__ float at_group_sum(float v) {
+    return at_group(v, [](float a, float b) { return a + b; });
 }
 __device__ __forceinline__ float at_group_max(float v) {
-    v = fmaxf(v, __shfl_xor(v, 16, 64));
-    return fmaxf(v, __shfl_xor(v, 32, 64));
+    return at_group(v, [](float a, float b) { return fmaxf(a, b); });
 }
 
 __device__ __forceinline__ int at_uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
-// One wavefront's share; it takes every WT-th tile.
-template <int KIND, int D, int RT, int WT>
+// All ones where bit e of m is set, else zero.
+__device__ __forceinline__ uint32_t at_spread(uint32_t m, int e) { return (uint32_t)((int32_t)(m << (31 - e)) >> 31); }
+
+// One wavefront's share: 16 RT query rows, every wt_n-th tile.
+template <int KIND, int D, int RT>
 struct AtWave {
     using Sh = AtShape<KIND, D>;
     static constexpr bool QUANT = KIND != BSP_FP16;
     const AtArgs &a;
     int lane, col, grp;
     int kvh, len, past;
+    int wt_n;                      // wavefronts that take the tiles in turn
     const int32_t *table;
     // per query row (the lane's column); q in registers, or in LDS where those
     // are short: [RT][STEPS][64 lanes], the workgroup's wavefronts share the rows
@@ -262,7 +274,7 @@ struct AtWave {
     }
 
     __device__ __forceinline__ void load_pages(int tile) {
-        const int j = min((tile + WT * (lane >> 1)) * AT_TILE + 16 * (lane & 1), len - 1);
+        const int j = min((tile + wt_n * (lane >> 1)) * AT_TILE + 16 * (lane & 1), len - 1);
         const int p = table[j >> a.page_shift];
         pages = (unsigned)p < (unsigned)a.num_pages ? p : 0;
     }
@@ -304,13 +316,12 @@ struct AtWave {
         if constexpr (QUANT) at_load(reinterpret_cast<const uint8_t *>(a.vw + r), vw);
     }
 
-    // Bits 0 .. 7: whether a row that sees drafted tokens `bits` sees tokens j .. j + 7.
-    __device__ __forceinline__ uint32_t visible(int j, uint64_t bits) const {
-        const int d = j - past, n = len - j;       // first token's place among the drafted ones; tokens there are
-        uint32_t m = d >= 0 ? (d < 64 ? (uint32_t)(bits >> d) : 0u)
-                            : (d > -8 ? ((uint32_t)bits << (-d & 7)) | ((1u << (-d & 7)) - 1u) : 0xFFu);
-        m &= n >= 8 ? 0xFFu : (1u << max(n, 0)) - 1u;
-        return m & 0xFFu;
+    // Bits 0 .. 7: whether a row that sees drafted tokens `bits` sees the 8
+    // tokens from the drafted one d on (negative: before them) on.
+    __device__ __forceinline__ uint32_t visible(int d, uint64_t bits) const {
+        const int b = min(max(-d, 0), 8);          // tokens before the drafted ones
+        const uint32_t m = d < 64 ? (uint32_t)(bits >> max(d, 0)) : 0u;
+        return (m << b) | ((1u << b) - 1u);
     }
 
     // One tile: scores, running maximum, weights, output. The next tile's loads
@@ -380,43 +391,53 @@ struct AtWave {
             // see scores -inf; rows past the end hold anything, NaN too, and
             // count as zeros. A value row (or its word) that is not finite
             // counts as zero too, and makes the query rows that see it NaN.
+            // (Masks are spread over registers: comparisons would hold 16
+            // pairs of scalar registers at a time.)
+            const int n = min(max(len - (j0 + 8 * grp), 0), 8);     // tokens there are
+            const uint32_t in = (1u << n) - 1u;
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt) {
-                const uint32_t ok = visible(j0 + 8 * grp, seen[rt]);
+                const uint32_t ok = visible(j0 + 8 * grp - past, seen[rt]) & in;
                 top[rt] = -INFINITY;
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    const float y = (ok >> e & 1u) != 0u ? x[rt][e >> 2][e & 3] : -INFINITY;
-                    x[rt][e >> 2][e & 3] = y;
-                    top[rt] = fmaxf(top[rt], y);
-                    // (one comparison at a time: 16 masks in flight would spill)
-                    __builtin_amdgcn_sched_barrier(0);
+                    const float x0 = x[rt][e >> 2][e & 3];
+                    const uint32_t m = at_spread(ok, e), y = __builtin_bit_cast(uint32_t, x0);
+                    const float z = __builtin_bit_cast(float, (m & y) | (~m & 0xFF800000u));
+                    x[rt][e >> 2][e & 3] = z;
+                    top[rt] = fmaxf(top[rt], z);
                 }
             }
+            uint32_t odd = 0;              // bit e: token e's row is not finite
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                __builtin_amdgcn_sched_barrier(0);
-                const bool in = j0 + 8 * grp + e < len;
-                bool nf = false;
+                const uint32_t m = at_spread(in, e);
                 if constexpr (QUANT) {
-                    nf = in & (((vw[e] & 0x7F800000u) == 0x7F800000u) | ((vw[e] & 0x7C00u) == 0x7C00u));
-                    vw[e] = (in && !nf) ? vw[e] : 0u;
+                    // an exponent of all ones carries into the bit above it
+                    const uint32_t w = vw[e] & m;
+                    const uint32_t nf = ((((w & 0x7F800000u) + 0x00800000u) >> 31) | (((w & 0x7C00u) + 0x0400u) >> 15)) & 1u;
+                    vw[e] = w & (nf - 1u);
+                    odd |= nf << e;
                 } else {
+                    uint32_t any = 0;
 #pragma unroll
                     for (int i = 0; i < Sh::VW; ++i) {
-                        const uint32_t h = v[e][i];
-                        const bool lo = (h & 0x7C00u) == 0x7C00u, hi = (h & 0x7C000000u) == 0x7C000000u;
-                        nf |= in & (lo | hi);
-                        v[e][i] = ((in && !lo) ? h & 0xFFFFu : 0u) | ((in && !hi) ? h & 0xFFFF0000u : 0u);
+                        const uint32_t h = v[e][i] & m, nf = (((h & 0x7C007C00u) + 0x04000400u) >> 15) & 0x00010001u;
+                        v[e][i] = h & ~(nf * 0xFFFFu);
+                        any |= nf;
                     }
-                    // any of the 16 lanes that hold the row
-                    nf = ((__ballot(nf) >> (16 * grp)) & 0xFFFFu) != 0;
+                    odd |= any != 0u ? 1u << e : 0u;
                 }
-                if (__ballot(nf) != 0) {
+            }
+            if (__ballot(odd != 0) != 0) {
+                // a row's 16 lanes hold pieces of it
 #pragma unroll
-                    for (int rt = 0; rt < RT; ++rt)
-                        l[rt] = (nf && x[rt][e >> 2][e & 3] != -INFINITY) ? __builtin_nanf("") : l[rt];
-                }
+                for (int d = 1; d < 16; d <<= 1) odd |= (uint32_t)__shfl_xor((int)odd, d, 64);
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        if ((odd >> e & 1u) != 0u && x[rt][e >> 2][e & 3] != -INFINITY) l[rt] = __builtin_nanf("");
             }
         }
         // the largest value step (positive floats order as integers)
@@ -515,8 +536,13 @@ struct AtWave {
     }
 };
 
+// Wavefronts side by side that `rows` query rows of a row block take, at `unit`
+// (16 RT) rows each.
+__device__ __forceinline__ int at_side(int rows, int unit) { return rows <= unit ? 1 : rows <= 2 * unit ? 2 : 4; }
+
 // The sequences, 64 at a time, one a lane: cached tokens, first and last query
-// row, and tiles of work (at least one where there are query rows).
+// row, and work: tiles (at least one where there are query rows) times the
+// wavefronts side by side that take each.
 struct AtSeqs {
     int block = -1, len = 0, q0 = 0, q1 = 0, work = 0;
 
@@ -530,29 +556,31 @@ struct AtSeqs {
             len = (int)min((int64_t)max(a->kv_lens[b], 0), a->table_width << a->page_shift);
             q0 = min(max(a->q_start[b], 0), a->total_q);
             q1 = min(max(a->q_start[b + 1], q0), a->total_q);
-            work = q1 > q0 ? max(1, (len + AT_TILE - 1) / AT_TILE) : 0;
+            const int side = at_side(min(q1 - q0, a->max_q) * (a->hq / a->hkv), a->unit_rows);
+            work = q1 > q0 ? max(1, (len + AT_TILE - 1) / AT_TILE) * side : 0;
         }
     }
     __device__ __forceinline__ int of(int v, int b) const { return __builtin_amdgcn_readlane(v, b & 63); }
 };
 
-// One workgroup: a kv head, a block of 16 RT WR query rows, and an equal share
-// of the tiles of all sequences laid end to end (its chunk), which may hold
-// the end of one sequence, whole ones, and the start of another. WR wavefronts
-// side by side take 16 RT rows each of the same tiles (their reads of the
-// cache meet in the CU's L1), 4 / WR such sets take the tiles in turn.
-template <int KIND, int D, int RT, int WR>
+// One workgroup: a kv head, a block of query rows, and an equal share of the
+// work of all sequences laid end to end (its chunk), which may hold the end of
+// one sequence, whole ones, and the start of another. As many wavefronts side
+// by side (1, 2 or 4) as the sequence's rows need take 16 RT rows each of the
+// same tiles (their reads of the cache meet in the CU's L1); the sets so
+// formed take the tiles in turn. RT 1 is for calls of at most 16 rows.
+template <int KIND, int D, int RT>
 __global__ __launch_bounds__(64 * AT_WAVES, D == 256 ? 1 : 2) void k_at(const AtArgs a) {
     using Sh = AtShape<KIND, D>;
-    using Wave = AtWave<KIND, D, RT, AT_WAVES / WR>;
+    using Wave = AtWave<KIND, D, RT>;
     extern __shared__ __attribute__((aligned(16))) float at_smem[];
     constexpr int LD = D + 4;                      // floats per row of a wavefront's output in LDS
-    constexpr int WT = AT_WAVES / WR;
+    constexpr int ROWS = AT_ROWS(RT);              // query rows of a row block
     float *s_acc = at_smem;                        // [AT_WAVES][16][LD]
     float *s_m = s_acc + AT_WAVES * 16 * LD;       // [AT_WAVES][16]
     float *s_l = s_m + AT_WAVES * 16;
     int *s_flag = reinterpret_cast<int *>(s_l + AT_WAVES * 16);
-    const int wave = at_uniform(threadIdx.x >> 6), wr = wave % WR, wt = wave / WR;
+    const int wave = at_uniform(threadIdx.x >> 6);
     // workgroups 8 apart share an XCD and its L2: the row blocks of one piece
     // of the cache are 8 apart
     const int group = blockIdx.x / (8 * a.row_blocks), in = blockIdx.x % (8 * a.row_blocks);
@@ -563,9 +591,7 @@ __global__ __launch_bounds__(64 * AT_WAVES, D == 256 ? 1 : 2) void k_at(const At
     w.kvh = piece - ch * a.hkv;
     w.lane = threadIdx.x & 63, w.col = w.lane & 15, w.grp = w.lane >> 4;
     w.c = a.scale * 1.44269504088896341f;
-    w.q_lds = reinterpret_cast<at_h8 *>(at_smem) + wr * (RT * Sh::STEPS * 64);
     const int G = a.hq / a.hkv;
-    const int r0 = (rb * WR + wr) * 16 * RT;       // the wavefront's first row
 
     // the chunk's first sequence, and where that one's tiles begin
     AtSeqs seqs;
@@ -614,13 +640,19 @@ __global__ __launch_bounds__(64 * AT_WAVES, D == 256 ? 1 : 2) void k_at(const At
         w.len = seqs.of(seqs.len, b);
         w.past = w.len - T;
         w.table = as->table + (int64_t)b * as->table_width;
-        const int nt = (w.len + AT_TILE - 1) / AT_TILE;
-        const int t0 = min(nt, pos - begin), t1 = min(nt, end - begin);
-        // chunks that hold tiles of the sequence, and this one's place for its part
+        const int nt = (w.len + AT_TILE - 1) / AT_TILE, side = at_side(rows, 16 * RT);
+        const int t0 = min(nt, (pos - begin) / side), t1 = min(nt, (end - begin) / side);
+        // chunks that hold work of the sequence, and this one's place for its part
         const int c0 = begin / per, count = as->chunks == 0 ? 1 : (begin + work - 1) / per - c0 + 1;
         begin += work;
         pos = begin;
-        if (rb * WR * 16 * RT >= rows) continue;
+        const int rows_here = min(rows - rb * ROWS, ROWS);
+        if (rows_here <= 0) continue;
+        // wavefronts side by side, the wavefront's place among them, its first row
+        const int wr_n = at_side(rows_here, 16 * RT);
+        const int wr = wave & (wr_n - 1), wt = wave / wr_n, r0 = rb * ROWS + wr * 16 * RT;
+        w.wt_n = AT_WAVES / wr_n;
+        w.q_lds = reinterpret_cast<at_h8 *>(at_smem) + wr * (RT * Sh::STEPS * 64);
         const int tile0 = t0 + wt;
         if (tile0 < t1) {
             w.load_pages(tile0);
@@ -634,7 +666,7 @@ __global__ __launch_bounds__(64 * AT_WAVES, D == 256 ? 1 : 2) void k_at(const At
         for (int rt = 0; rt < RT; ++rt) {
             const int row = r0 + 16 * rt + w.col;
             const bool in_rows = row < rows;
-            const int t = in_rows ? row / G : 0, g = in_rows ? row - t * G : 0;
+            const int t = in_rows ? at_div(row, as->inv_group) : 0, g = in_rows ? row - t * G : 0;
             const uint16_t *src = as->Q + (int64_t)(q0 + t) * as->q_stride + (int64_t)(w.kvh * G + g) * D;
             uint32_t qr[D / 8];                    // the channels of the lane's K pieces
 #pragma unroll
@@ -661,7 +693,7 @@ __global__ __launch_bounds__(64 * AT_WAVES, D == 256 ? 1 : 2) void k_at(const At
 #pragma unroll
             for (int s = 0; s < Sh::STEPS; ++s) {
                 if constexpr (Wave::Q_LDS) {
-                    if (rt % WT == wt)                   // shared by the WT wavefronts of these rows
+                    if (rt % w.wt_n == wt)               // shared by the wavefronts of these rows
                         const_cast<at_h8 *>(w.q_lds)[(rt * Sh::STEPS + s) * 64 + w.lane] = at_q_frag<KIND>(qr, s);
                 } else {
                     w.q[rt][s] = at_q_frag<KIND>(qr, s);
@@ -673,10 +705,11 @@ __global__ __launch_bounds__(64 * AT_WAVES, D == 256 ? 1 : 2) void k_at(const At
             for (int i = 0; i < Sh::NT; ++i) w.acc[rt][i] = at_f4{0.f, 0.f, 0.f, 0.f};
         }
         if constexpr (Wave::Q_LDS) __syncthreads();
-        for (int t = tile0, i = 1; t < t1; t += WT, ++i) {
-            if (t + WT < t1) {         // (past the last tile its own rows are loaded again, unused)
-                if ((i & 31) == 0) w.load_pages(t + WT);
-                w.set_tile(i, (t + WT) * AT_TILE);
+        const int te = r0 < rows ? t1 : tile0;           // (no rows: no tiles)
+        for (int t = tile0, i = 1; t < te; t += w.wt_n, ++i) {
+            if (t + w.wt_n < t1) {     // (past the last tile its own rows are loaded again, unused)
+                if ((i & 31) == 0) w.load_pages(t + w.wt_n);
+                w.set_tile(i, (t + w.wt_n) * AT_TILE);
             }
             w.tile(t * AT_TILE);
         }
@@ -685,69 +718,67 @@ __global__ __launch_bounds__(64 * AT_WAVES, D == 256 ? 1 : 2) void k_at(const At
         // Join the wavefronts of each row tile, one row tile of each at a time;
         // then write the rows, or post them for the sequence's last chunk to join.
         const bool split = count > 1;
-        constexpr int ROWS = 16 * RT * WR;
-        constexpr uint32_t slot_floats = ROWS * (D + 4);     // [row][D] sums, then [row] (m, l, 0, 0)
+        const uint32_t slot_floats = ap->slot_rows * (D + 4);     // [row][D] sums, then [row] (m, l, 0, 0)
         const int64_t head = (int64_t)w.kvh * ap->row_blocks + rb, heads = (int64_t)ap->hkv * ap->row_blocks;
+        const auto put = [&](int rl, int d, at_f4 y0, at_f4 y1, float mx, float lt) {
+            if (split) {
+                float *place = ap->part + ((2 * (int64_t)ch + (ch == c0)) * heads + head) * slot_floats;
+                if (ap->join) {                          // for another kernel: plain stores
+                    at_f4 *y = reinterpret_cast<at_f4 *>(place + rl * D + d);
+                    y[0] = y0, y[1] = y1;
+                    if (d == 0) *reinterpret_cast<float2 *>(place + ap->slot_rows * D + 4 * rl) = float2{mx, lt};
+                    return;
+                }
+                const __amdgpu_buffer_rsrc_t rs = bsp_rsrc(place, slot_floats * 4);
+                const uint32_t at = ((uint32_t)rl * D + d) * 4u;
+                at_ws_store(rs, at, y0), at_ws_store(rs, at + 16, y1);
+                if (d == 0) at_ws_store(rs, (uint32_t)(ap->slot_rows * D + 4 * rl) * 4u, at_f4{mx, lt, 0.f, 0.f});
+            } else {
+                at_write(ap, q0, w.kvh, G, rb * ROWS + rl, d, D, y0, y1, lt == 0.f ? 0.f : 1.0f / lt);
+            }
+        };
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
-            __syncthreads();                             // the LDS area's last readers
-            const float l = at_group_sum(w.l[rt]);
+            const float l = at_group_sum(w.l[rt]), m = w.limit[rt] == AT_NONE ? AT_LOW : w.mb[rt];
             float os = 0.f, ps = 0.f, up = 1.f;
             if constexpr (Wave::QUANT) {
                 os = at_group_sum(w.osum[rt]);
                 ps = at_group_sum(w.psum[rt]) * (KIND == BSP_INT8 ? 128.0f : 8.0f);
                 up = 16777216.0f;
             }
-            if (w.grp == 0) {
-                s_m[wave * 16 + w.col] = w.limit[rt] == AT_NONE ? AT_LOW : w.mb[rt];
-                s_l[wave * 16 + w.col] = l;
-            }
+            // the lane's channels: NT from (4 grp + r) NT on, for r = 0 .. 3
+            const auto y_of = [&](int r, int t) {
+                at_f4 y;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float z = w.acc[rt][t + i][r];
+                    if constexpr (Wave::QUANT) {
+                        const float h = KIND == BSP_INT4 && (i & 1) ? up * 0.0625f : up;
+                        z = fmaf(w.sig, fmaf(z, h, -ps), os);
+                    }
+                    y[i] = z;
+                }
+                return y;
+            };
+            __syncthreads();                             // the LDS area's last readers
+            if (w.grp == 0) s_m[wave * 16 + w.col] = m, s_l[wave * 16 + w.col] = l;
             float *o = s_acc + (wave * 16 + w.col) * LD;
 #pragma unroll
             for (int r = 0; r < 4; ++r)
 #pragma unroll
-                for (int t = 0; t < Sh::NT; t += 4) {
-                    at_f4 y;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        float z = w.acc[rt][t + i][r];
-                        if constexpr (Wave::QUANT) {
-                            const float h = KIND == BSP_INT4 && (i & 1) ? up * 0.0625f : up;
-                            z = fmaf(w.sig, fmaf(z, h, -ps), os);
-                        }
-                        y[i] = z;
-                    }
-                    *reinterpret_cast<at_f4 *>(o + (4 * w.grp + r) * Sh::NT + t) = y;
-                }
+                for (int t = 0; t < Sh::NT; t += 4) *reinterpret_cast<at_f4 *>(o + (4 * w.grp + r) * Sh::NT + t) = y_of(r, t);
             __syncthreads();
-            for (int i = threadIdx.x; i < WR * 16 * (D / 8); i += 64 * AT_WAVES) {
+            for (int i = threadIdx.x; i < wr_n * 16 * (D / 8); i += 64 * AT_WAVES) {
                 const int d = (i % (D / 8)) * 8, row = i / (D / 8) % 16, g = i / (D / 8) / 16;   // g: the row group
-                const int rl = g * 16 * RT + 16 * rt + row, ri = rb * ROWS + rl;
-                if (ri >= rows) continue;
-                float mx = s_m[g * 16 + row];
-#pragma unroll
-                for (int k = 1; k < WT; ++k) mx = fmaxf(mx, s_m[(k * WR + g) * 16 + row]);
-                at_f4 y0 = {0.f, 0.f, 0.f, 0.f}, y1 = y0;
-                float lt = 0.f;
-#pragma unroll
-                for (int k = 0; k < WT; ++k) {
-                    const int at = (k * WR + g) * 16 + row;
-                    const float f = __builtin_amdgcn_exp2f(s_m[at] - mx);
-                    lt = fmaf(s_l[at], f, lt);
+                const int rl = g * 16 * RT + 16 * rt + row;
+                if (rl >= rows_here) continue;
+                AtSum sum;
+                for (int k = 0; k < w.wt_n; ++k) {
+                    const int at = (k * wr_n + g) * 16 + row;
                     const at_f4 *src = reinterpret_cast<const at_f4 *>(s_acc + at * LD + d);
-                    const at_f4 z0 = src[0], z1 = src[1];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) y0[e] = fmaf(z0[e], f, y0[e]), y1[e] = fmaf(z1[e], f, y1[e]);
+                    sum.add(src[0], src[1], s_m[at], s_l[at]);
                 }
-                if (split) {
-                    const int64_t slot = (2 * (int64_t)ch + (ch == c0)) * heads + head;
-                    const __amdgpu_buffer_rsrc_t rs = bsp_rsrc(ap->part + slot * slot_floats, slot_floats * 4);
-                    const uint32_t at = ((uint32_t)rl * D + d) * 4u;
-                    at_ws_store(rs, at, y0), at_ws_store(rs, at + 16, y1);
-                    if (d == 0) at_ws_store(rs, (uint32_t)(ROWS * D + 4 * rl) * 4u, at_f4{mx, lt, 0.f, 0.f});
-                } else {
-                    at_write(ap, q0, w.kvh, G, ri, d, D, y0, y1, lt == 0.f ? 0.f : 1.0f / lt);
-                }
+                put(rl, d, sum.y0, sum.y1, sum.m, sum.l);
             }
         }
         if (!split || ap->join) continue;
@@ -758,9 +789,9 @@ __global__ __launch_bounds__(64 * AT_WAVES, D == 256 ? 1 : 2) void k_at(const At
             *s_flag = (int)__hip_atomic_fetch_add(&ap->counters[unit], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         __syncthreads();
         if (*s_flag != count - 1) continue;
-        for (int i = threadIdx.x; i < min(ROWS, rows - rb * ROWS) * (D / 8); i += 64 * AT_WAVES) {
+        for (int i = threadIdx.x; i < rows_here * (D / 8); i += 64 * AT_WAVES) {
             const int row = i / (D / 8), d = (i % (D / 8)) * 8;
-            const uint32_t at = ((uint32_t)row * D + d) * 4u, at_ml = (uint32_t)(ROWS * D + 4 * row) * 4u;
+            const uint32_t at = ((uint32_t)row * D + d) * 4u, at_ml = (uint32_t)(ap->slot_rows * D + 4 * row) * 4u;
             AtSum sum;
             for (int s = 0; s < count; ++s)        // in chunk order
                 sum.add(ap->part + ((2 * (int64_t)(c0 + s) + (s == 0)) * heads + head) * slot_floats, slot_floats * 4, at, at_ml);
@@ -772,9 +803,9 @@ __global__ __launch_bounds__(64 * AT_WAVES, D == 256 ? 1 : 2) void k_at(const At
 
 // Joins the posted parts of split sequences: a workgroup takes 4 rows of a
 // (sequence, kv head), its wavefronts every fourth chunk; their sums meet in
-// LDS, in wavefront order. ROWS: rows of a row block.
+// LDS, in wavefront order.
 template <int D>
-__global__ __launch_bounds__(64 * AT_WAVES) void k_at_join(const AtArgs a, int ROWS) {
+__global__ __launch_bounds__(64 * AT_WAVES) void k_at_join(const AtArgs a, int block_rows) {
     constexpr int P = D / 8, RW = 64 / P;          // 8-channel pieces of a row; rows of a wavefront's 64 lanes
     __shared__ __attribute__((aligned(16))) float s_y[AT_WAVES][64][8];
     __shared__ float s_ml[AT_WAVES][64][2];
@@ -795,14 +826,18 @@ __global__ __launch_bounds__(64 * AT_WAVES) void k_at_join(const AtArgs a, int R
     const int per = max(a.min_per, (total + a.chunks - 1) / a.chunks);
     const int c0 = begin / per, count = work == 0 ? 0 : (begin + work - 1) / per - c0 + 1;
     if (count <= 1 || (int)blockIdx.x * RW >= rows) return;
-    const int64_t heads = (int64_t)a.hkv * a.row_blocks, head = (int64_t)kvh * a.row_blocks + row / ROWS;
-    const uint32_t slot_floats = (uint32_t)ROWS * (D + 4), rl = (uint32_t)(row % ROWS);
+    const int64_t heads = (int64_t)a.hkv * a.row_blocks, head = (int64_t)kvh * a.row_blocks + row / block_rows;
+    const uint32_t slot_floats = (uint32_t)a.slot_rows * (D + 4), rl = (uint32_t)(row % block_rows);
     AtSum sum;
     if (row < rows) {
+        // (a kernel of its own: plain loads)
 #pragma unroll 4
-        for (int s = wave; s < count; s += AT_WAVES)
-            sum.add(a.part + ((2 * (int64_t)(c0 + s) + (s == 0)) * heads + head) * slot_floats, slot_floats * 4,
-                    (rl * D + d) * 4u, (ROWS * D + 4 * rl) * 4u);
+        for (int s = wave; s < count; s += AT_WAVES) {
+            const float *place = a.part + ((2 * (int64_t)(c0 + s) + (s == 0)) * heads + head) * slot_floats;
+            const float2 ml = *reinterpret_cast<const float2 *>(place + a.slot_rows * D + 4 * rl);
+            const at_f4 *z = reinterpret_cast<const at_f4 *>(place + rl * D + d);
+            sum.add(z[0], z[1], ml.x, ml.y);
+        }
     }
 #pragma unroll
     for (int e = 0; e < 4; ++e) s_y[wave][lane][e] = sum.y0[e], s_y[wave][lane][4 + e] = sum.y1[e];
@@ -819,10 +854,10 @@ __global__ __launch_bounds__(64 * AT_WAVES) void k_at_join(const AtArgs a, int R
     at_write(at_late(), q0, kvh, G, row, d, D, sum.y0, sum.y1, sum.l == 0.f ? 0.f : 1.0f / sum.l);
 }
 
-// The plan of a call: row tiles per wavefront, wavefronts side by side, row
-// blocks, and how many chunks the tiles of all sequences are cut into.
+// The plan of a call: row tiles per wavefront, rows of a row block and of its
+// partial sums, row blocks, and how many chunks the work is cut into.
 struct AtPlan {
-    int rt, wr, row_blocks, chunks, min_per, max_chunks, join;
+    int rt, block_rows, slot_rows, row_blocks, chunks, min_per, max_chunks, join;
     int64_t ws_bytes;
 };
 
@@ -831,51 +866,46 @@ struct AtPlan {
 AtPlan at_plan(const bsp_kv_cache *c, int64_t table_width, int64_t B, int64_t max_q, int64_t hq, bool split) {
     AtPlan p{};
     const int64_t rows = max_q * (hq / c->kv_heads);
-    p.rt = rows <= 16 || c->head_dim == 256 ? 1 : 2;
-    p.wr = rows <= 16 * p.rt ? 1 : rows <= 32 * p.rt ? 2 : 4;
-    p.row_blocks = (int)((rows + 16 * p.rt * p.wr - 1) / (16 * p.rt * p.wr));
+    const int64_t D = c->head_dim;
+    p.rt = rows <= 16 || D == 256 ? 1 : 2;
+    p.block_rows = (int)(p.rt == 1 ? AT_ROWS(1) : AT_ROWS(2));
+    p.row_blocks = (int)((rows + p.block_rows - 1) / p.block_rows);
+    p.slot_rows = (int)std::min<int64_t>(p.block_rows, rows);
     p.max_chunks = (int)B;
-    p.min_per = AT_MINPER;
+    p.min_per = 2 * AT_WAVES;                // two tiles per wavefront at least
     const int64_t heads = c->kv_heads * p.row_blocks;
     const int64_t tiles = (table_width * c->page_size + AT_TILE - 1) / AT_TILE;      // of the longest sequence
     if (split && B * heads <= AT_WS_COUNTERS) {
         const int64_t want = std::max<int64_t>(1, AT_GROUPS / heads);
-        const int64_t most = B * std::max<int64_t>(1, (tiles + p.min_per - 1) / p.min_per);
+        const int64_t side = p.slot_rows <= 16 * p.rt ? 1 : p.slot_rows <= 32 * p.rt ? 2 : 4;
+        const int64_t most = B * std::max<int64_t>(1, (tiles * side + p.min_per - 1) / p.min_per);
         p.chunks = p.max_chunks = (int)std::min(want, most);
         p.join = p.chunks > B && (rows > 16 || p.chunks > 8 * B);
-        p.ws_bytes = AT_WS_COUNTERS * 4 + 2 * p.chunks * heads * 16 * p.rt * p.wr * (c->head_dim + 4) * 4;
+        p.ws_bytes = AT_WS_COUNTERS * 4 + 2 * p.chunks * heads * p.slot_rows * (D + 4) * 4;
     }
     return p;
 }
 
-template <int KIND, int D, int RT, int WR>
+template <int KIND, int D, int RT>
 void at_launch_t(const AtArgs &a, hipStream_t stream) {
-    static_assert(sizeof(AtArgs) <= 512, "the kernels read their arguments in place");
     const size_t lds = (size_t)(AT_WAVES * 16 * (D + 4) + 2 * AT_WAVES * 16 + 4) * 4;
     const int64_t pieces = ((int64_t)a.max_chunks * a.hkv + 7) / 8 * 8;
     if (lds > 65536)
-        (void)hipFuncSetAttribute((const void *)k_at<KIND, D, RT, WR>, hipFuncAttributeMaxDynamicSharedMemorySize,
-                                  (int)lds);
-    hipLaunchKernelGGL((k_at<KIND, D, RT, WR>), dim3((unsigned)(pieces * a.row_blocks)), dim3(64 * AT_WAVES), lds,
-                       stream, a);
+        (void)hipFuncSetAttribute((const void *)k_at<KIND, D, RT>, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+    hipLaunchKernelGGL((k_at<KIND, D, RT>), dim3((unsigned)(pieces * a.row_blocks)), dim3(64 * AT_WAVES), lds, stream, a);
     if (a.join) {
         const int rw = 64 / (D / 8), rows = a.max_q * (a.hq / a.hkv);
         hipLaunchKernelGGL((k_at_join<D>), dim3((rows + rw - 1) / rw, a.hkv, a.B), dim3(64 * AT_WAVES), 0, stream, a,
-                           16 * RT * WR);
+                           AT_ROWS(RT));
     }
 }
 
 template <int KIND, int D>
 void at_launch_r(const AtArgs &a, const AtPlan &p, hipStream_t stream) {
-    constexpr int RT = D == 256 ? 1 : 2;           // row tiles of a wavefront past one
-    if (p.wr == 4)
-        at_launch_t<KIND, D, RT, 4>(a, stream);
-    else if (p.wr == 2)
-        at_launch_t<KIND, D, RT, 2>(a, stream);
-    else if (p.rt == 1)
-        at_launch_t<KIND, D, 1, 1>(a, stream);
-    else
-        at_launch_t<KIND, D, RT, 1>(a, stream);
+    if (p.rt == 1)
+        at_launch_t<KIND, D, 1>(a, stream);
+    else if constexpr (D != 256)
+        at_launch_t<KIND, D, 2>(a, stream);
 }
 
 template <int KIND>
@@ -895,6 +925,7 @@ int at_check(const bsp_kv_cache *c, int64_t table_width, int64_t B, int64_t max_
     if (table_width < 0 || B < 0 || max_q < 0 || max_q > BSP_TREE_MAX || hq < 0) return BSP_E_ARG;
     if (hq > 0 && (c->kv_heads == 0 || hq % c->kv_heads != 0)) return BSP_E_ARG;
     if (B > 65535 || hq > 65535) return BSP_E_OVERFLOW;
+    if (hq > 0 && hq / c->kv_heads > 16384) return BSP_E_UNSUPPORTED;
     if (table_width > INT32_MAX / c->page_size) return BSP_E_OVERFLOW;
     return BSP_OK;
 }
@@ -939,10 +970,11 @@ extern "C" int attention_tree_f16(const uint16_t *Q, int64_t q_stride, const bsp
     a.num_pages = (int)cache->num_pages;
     a.page_shift = __builtin_ctzll((unsigned long long)cache->page_size);
     a.scale = scale;
+    a.inv_group = 1.0f / (float)(q_heads / cache->kv_heads);
     a.B = (int)B;
     a.q_vec = ((uintptr_t)Q & 15u) == 0 && (q_stride & 7) == 0;
     a.o_vec = ((uintptr_t)O & 15u) == 0 && (o_stride & 7) == 0;
-    a.row_blocks = p.row_blocks, a.chunks = p.chunks, a.min_per = p.min_per, a.max_chunks = p.max_chunks, a.join = p.join;
+    a.unit_rows = 16 * p.rt, a.row_blocks = p.row_blocks, a.slot_rows = p.slot_rows, a.chunks = p.chunks, a.min_per = p.min_per, a.max_chunks = p.max_chunks, a.join = p.join;
     a.counters = (uint32_t *)workspace;
     a.part = p.ws_bytes > 0 ? (float *)((uint8_t *)workspace + AT_WS_COUNTERS * 4) : nullptr;
     if (cache->dtype == BSP_FP16)
