@@ -872,7 +872,7 @@ AtPlan at_plan(const bsp_kv_cache *c, int64_t table_width, int64_t B, int64_t ma
     p.row_blocks = (int)((rows + p.block_rows - 1) / p.block_rows);
     p.slot_rows = (int)std::min<int64_t>(p.block_rows, rows);
     p.max_chunks = (int)B;
-    p.min_per = 2 * AT_WAVES;                // two tiles per wavefront at least
+    p.min_per = 4 * AT_WAVES;                // four tiles per wavefront at least
     const int64_t heads = c->kv_heads * p.row_blocks;
     const int64_t tiles = (table_width * c->page_size + AT_TILE - 1) / AT_TILE;      // of the longest sequence
     if (split && B * heads <= AT_WS_COUNTERS) {

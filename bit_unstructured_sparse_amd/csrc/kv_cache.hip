@@ -33,27 +33,28 @@ struct KvArgs {
 };
 
 #define KV_BLOCK 256
+#define KV_MANY 65536      // (token, head) rows
 
-// The (token, head, K or V) of this lane's row; lanes of a row agree.
+// Rows of one lane: U token groups of a (head, K / V), so that a lane has U
+// independent chains of loads (slot, row, codes) in flight. Items run over (run
+// of groups, head, K / V), K / V fastest; a group is the rows a wavefront holds,
+// consecutive tokens.
 struct KvItem {
-    int64_t token;
+    int64_t token;     // of the first group
     int head;
     bool is_v;
-    int ch;        // the lane's first channel
+    int ch;            // the lane's first channel
 };
 
-// Items run over (token group, head, K / V), K / V fastest: a group is the
-// rows a wavefront holds, consecutive tokens.
-template <int D>
-__device__ __forceinline__ KvItem kv_item(const KvArgs &a, int64_t item) {
+template <int D, int U>
+__device__ __forceinline__ KvItem kv_item(const KvArgs &a, uint32_t item) {
     constexpr int LPR = D / 8, RPW = 64 / LPR;
     const int lane = threadIdx.x & 63;
-    const int64_t th = item >> 1;
-    const int64_t group = th / a.hkv;
+    const uint32_t th = item >> 1, run = th / (uint32_t)a.hkv;
     KvItem it;
     it.is_v = (item & 1) != 0;
-    it.head = (int)(th - group * a.hkv);
-    it.token = group * RPW + lane / LPR;
+    it.head = (int)(th - run * (uint32_t)a.hkv);
+    it.token = (int64_t)run * (RPW * U) + lane / LPR;
     it.ch = (lane % LPR) * 8;
     return it;
 }
@@ -139,86 +140,130 @@ __device__ __forceinline__ uint32_t kv_value(float s, float o, uint32_t u) {
     return bsp_f2h(v > 65504.0f ? 65504.0f : v);
 }
 
-template <int KIND, int D, bool VEC>
-__global__ __launch_bounds__(KV_BLOCK) void k_kv_append(const KvArgs a, int64_t items) {
-    const int64_t item = (int64_t)blockIdx.x * (KV_BLOCK / 64) + (threadIdx.x >> 6);
+template <int KIND, int D, bool VEC, int U>
+__global__ __launch_bounds__(KV_BLOCK) void k_kv_append(const KvArgs a, uint32_t items) {
+    constexpr int RPW = 64 / (D / 8);
+    const uint32_t item = blockIdx.x * (KV_BLOCK / 64) + (threadIdx.x >> 6);
     if (item >= items) return;
-    const KvItem it = kv_item<D>(a, item);
-    const bool in = it.token < a.n;
-    const int64_t slot = in ? a.slots[it.token] : -1;
-    // skipped rows are read as row 0 of the call, so that every lane of the
-    // shuffles holds a value
-    const int64_t t = in ? it.token : 0;
-    const uint16_t *src = (it.is_v ? a.V + t * a.vs : a.K + t * a.ks) + (int64_t)it.head * D + it.ch;
-    const kv_u4 raw = kv_load8<VEC>(src);
-    const bool ok = slot >= 0 && slot < a.nslots;
-    const int64_t row = kv_row(a, ok ? slot : 0, it.head);
+    const KvItem it = kv_item<D, U>(a, item);
+    kv_u4 raw[U];
+    int64_t slot[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+        // rows past the end are read as row 0 of the call, so that every lane
+        // of the shuffles holds a value
+        const int64_t token = it.token + i * RPW;
+        const bool in = token < a.n;
+        slot[i] = in ? a.slots[token] : -1;
+        const int64_t t = in ? token : 0;
+        raw[i] = kv_load8<VEC>((it.is_v ? a.V + t * a.vs : a.K + t * a.ks) + (int64_t)it.head * D + it.ch);
+    }
     uint8_t *codes = it.is_v ? a.vc : a.kc;
-    if constexpr (KIND == BSP_FP16) {
-        if (ok) *reinterpret_cast<kv_u4 *>(codes + row * (2 * D) + 2 * it.ch) = raw;
-    } else {
-        uint32_t u[8], word;
-        kv_quantise<D / 8>(raw, KIND == BSP_INT8 ? 255.0f : 15.0f, u, word);
-        if (!ok) return;
-        if constexpr (KIND == BSP_INT8) {
-            kv_u2 c;
-            c.x = u[0] | (u[1] << 8) | (u[2] << 16) | (u[3] << 24);
-            c.y = u[4] | (u[5] << 8) | (u[6] << 16) | (u[7] << 24);
-            *reinterpret_cast<kv_u2 *>(codes + row * D + it.ch) = c;
-        } else {
-            uint32_t c = 0;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) c |= u[i] << (4 * i);
-            *reinterpret_cast<uint32_t *>(codes + row * (D / 2) + it.ch / 2) = c;
-        }
-        if (it.ch == 0) (it.is_v ? a.vw : a.kw)[row] = word;
-    }
-}
-
-template <int KIND, int D, bool VEC>
-__global__ __launch_bounds__(KV_BLOCK) void k_kv_gather(const KvArgs a, int64_t items) {
-    const int64_t item = (int64_t)blockIdx.x * (KV_BLOCK / 64) + (threadIdx.x >> 6);
-    if (item >= items) return;
-    const KvItem it = kv_item<D>(a, item);
-    if (it.token >= a.n) return;
-    const int64_t slot = a.slots[it.token];
-    uint16_t *dst = (it.is_v ? a.Vo + it.token * a.vs : a.Ko + it.token * a.ks) + (int64_t)it.head * D + it.ch;
-    kv_u4 out = kv_u4{0u, 0u, 0u, 0u};
-    if (slot >= 0 && slot < a.nslots) {
-        const int64_t row = kv_row(a, slot, it.head);
-        const uint8_t *codes = it.is_v ? a.vc : a.kc;
+    for (int i = 0; i < U; ++i) {
+        const bool ok = slot[i] >= 0 && slot[i] < a.nslots;
+        const int64_t row = kv_row(a, ok ? slot[i] : 0, it.head);
         if constexpr (KIND == BSP_FP16) {
-            out = *reinterpret_cast<const kv_u4 *>(codes + row * (2 * D) + 2 * it.ch);
+            if (ok) *reinterpret_cast<kv_u4 *>(codes + row * (2 * D) + 2 * it.ch) = raw[i];
         } else {
-            const uint32_t w = (it.is_v ? a.vw : a.kw)[row];
-            const float s = kv_word_step(w), o = kv_word_offset(w);
-            uint32_t u[8];
+            uint32_t u[8], word;
+            kv_quantise<D / 8>(raw[i], KIND == BSP_INT8 ? 255.0f : 15.0f, u, word);
+            if (!ok) continue;
             if constexpr (KIND == BSP_INT8) {
-                const kv_u2 c = *reinterpret_cast<const kv_u2 *>(codes + row * D + it.ch);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) u[i] = (c[i >> 2] >> (8 * (i & 3))) & 255u;
+                kv_u2 c;
+                c.x = u[0] | (u[1] << 8) | (u[2] << 16) | (u[3] << 24);
+                c.y = u[4] | (u[5] << 8) | (u[6] << 16) | (u[7] << 24);
+                *reinterpret_cast<kv_u2 *>(codes + row * D + it.ch) = c;
             } else {
-                const uint32_t c = *reinterpret_cast<const uint32_t *>(codes + row * (D / 2) + it.ch / 2);
+                uint32_t c = 0;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) u[i] = (c >> (4 * i)) & 15u;
+                for (int e = 0; e < 8; ++e) c |= u[e] << (4 * e);
+                *reinterpret_cast<uint32_t *>(codes + row * (D / 2) + it.ch / 2) = c;
             }
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                out[i] = kv_value(s, o, u[2 * i]) | (kv_value(s, o, u[2 * i + 1]) << 16);
+            if (it.ch == 0) (it.is_v ? a.vw : a.kw)[row] = word;
         }
     }
-    kv_store8<VEC>(dst, out);
 }
 
+template <int KIND, int D, bool VEC, int U>
+__global__ __launch_bounds__(KV_BLOCK) void k_kv_gather(const KvArgs a, uint32_t items) {
+    constexpr int RPW = 64 / (D / 8);
+    constexpr int CW = KIND == BSP_FP16 ? 4 : KIND == BSP_INT8 ? 2 : 1;      // dwords of a lane's codes
+    const uint32_t item = blockIdx.x * (KV_BLOCK / 64) + (threadIdx.x >> 6);
+    if (item >= items) return;
+    const KvItem it = kv_item<D, U>(a, item);
+    const uint8_t *codes = it.is_v ? a.vc : a.kc;
+    const uint32_t *words = it.is_v ? a.vw : a.kw;
+    int64_t slot[U];
+    uint32_t c[U][CW], w[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+        const int64_t token = it.token + i * RPW;
+        slot[i] = token < a.n ? a.slots[token] : -1;
+    }
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+        const bool ok = slot[i] >= 0 && slot[i] < a.nslots;
+        w[i] = 0;
+#pragma unroll
+        for (int j = 0; j < CW; ++j) c[i][j] = 0;
+        if (ok) {
+            const int64_t row = kv_row(a, slot[i], it.head);
+            const uint32_t *p = reinterpret_cast<const uint32_t *>(codes + (row * D + it.ch) * CW / 2);
+            if constexpr (CW == 4) {
+                const kv_u4 v = *reinterpret_cast<const kv_u4 *>(p);
+                c[i][0] = v.x, c[i][1] = v.y, c[i][2] = v.z, c[i][3] = v.w;
+            } else if constexpr (CW == 2) {
+                const kv_u2 v = *reinterpret_cast<const kv_u2 *>(p);
+                c[i][0] = v.x, c[i][1] = v.y;
+            } else {
+                c[i][0] = *p;
+            }
+            if constexpr (KIND != BSP_FP16) w[i] = words[row];
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+        const int64_t token = it.token + i * RPW;
+        if (token >= a.n) continue;
+        kv_u4 out;
+        if constexpr (KIND == BSP_FP16) {
+            out = kv_u4{c[i][0], c[i][1], c[i][2], c[i][3]};
+        } else {
+            // (a slot outside the cache: word and codes 0, value 0)
+            const float s = kv_word_step(w[i]), o = kv_word_offset(w[i]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                uint32_t u0, u1;
+                if constexpr (KIND == BSP_INT8)
+                    u0 = (c[i][e >> 1] >> (16 * (e & 1))) & 255u, u1 = (c[i][e >> 1] >> (16 * (e & 1) + 8)) & 255u;
+                else
+                    u0 = (c[i][0] >> (8 * e)) & 15u, u1 = (c[i][0] >> (8 * e + 4)) & 15u;
+                out[e] = kv_value(s, o, u0) | (kv_value(s, o, u1) << 16);
+            }
+        }
+        kv_store8<VEC>((it.is_v ? a.Vo + token * a.vs : a.Ko + token * a.ks) + (int64_t)it.head * D + it.ch, out);
+    }
+}
+
+template <int KIND, int D, bool VEC, int U>
+void kv_launch_u(const KvArgs &a, bool append, hipStream_t stream) {
+    constexpr int RUN = 64 / (D / 8) * U;
+    const uint32_t items = (uint32_t)((a.n + RUN - 1) / RUN * a.hkv * 2);
+    const unsigned grid = (items + KV_BLOCK / 64 - 1) / (KV_BLOCK / 64);
+    if (append)
+        hipLaunchKernelGGL((k_kv_append<KIND, D, VEC, U>), dim3(grid), dim3(KV_BLOCK), 0, stream, a, items);
+    else
+        hipLaunchKernelGGL((k_kv_gather<KIND, D, VEC, U>), dim3(grid), dim3(KV_BLOCK), 0, stream, a, items);
+}
+
+// Four groups a lane once that leaves enough wavefronts to fill the card.
 template <int KIND, int D, bool VEC>
 void kv_launch(const KvArgs &a, bool append, hipStream_t stream) {
-    constexpr int RPW = 64 / (D / 8);
-    const int64_t items = (a.n + RPW - 1) / RPW * a.hkv * 2;
-    const unsigned grid = (unsigned)((items + KV_BLOCK / 64 - 1) / (KV_BLOCK / 64));
-    if (append)
-        hipLaunchKernelGGL((k_kv_append<KIND, D, VEC>), dim3(grid), dim3(KV_BLOCK), 0, stream, a, items);
+    if (a.n * a.hkv >= KV_MANY)
+        kv_launch_u<KIND, D, VEC, 4>(a, append, stream);
     else
-        hipLaunchKernelGGL((k_kv_gather<KIND, D, VEC>), dim3(grid), dim3(KV_BLOCK), 0, stream, a, items);
+        kv_launch_u<KIND, D, VEC, 1>(a, append, stream);
 }
 
 template <int KIND, bool VEC>
@@ -246,7 +291,7 @@ int kv_common(const bsp_kv_cache *c, const uint16_t *K, int64_t ks, const uint16
     const int rc = kv_check_cache(c);
     if (rc != BSP_OK) return rc;
     if (n < 0) return BSP_E_ARG;
-    if (n >= INT32_MAX / std::max<int64_t>(c->kv_heads, 1)) return BSP_E_OVERFLOW;    // the grid
+    if (n >= INT32_MAX / std::max<int64_t>(c->kv_heads, 1)) return BSP_E_OVERFLOW;    // 32-bit item numbers
     if (n == 0 || c->kv_heads == 0) return BSP_OK;
     if (K == nullptr || V == nullptr || slots == nullptr) return BSP_E_ARG;
     if (ks < c->kv_heads * c->head_dim || vs < c->kv_heads * c->head_dim) return BSP_E_ARG;
