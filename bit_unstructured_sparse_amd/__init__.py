@@ -782,7 +782,7 @@ def kv_gather(cache: KVCache, slots, K=None, V=None, stream=None):
     n = slots.numel()
     at = _flat(slots, "slots", torch.int64, n, index)
     K = torch.empty((n, heads, dim), dtype=torch.float16, device=cache.device) if K is None else K
-    V = torch.empty((n, heads, dim), dtype=torch.float16, device=cache.device) if V is None else V
+    V = torch.empty_like(K) if V is None else V
     ks, vs = _rows(K, "K", n, heads, dim, index), _rows(V, "V", n, heads, dim, index)
     rc = load_library().kv_cache_gather(cache._ref, at, n, K.data_ptr(), ks, V.data_ptr(), vs,
                                         _stream_of(stream, index))

@@ -169,6 +169,27 @@ __device__ __forceinline__ void bt_store_y1(int32_t *Y, const BtEpi &e, int M, i
         Y[at] = v;
 }
 
+// The epilogue with adapters: fp16(dequantised sum + the adapter's part).
+struct BtLoraEpi {
+    uint16_t *Yh;
+    const float *sw;
+    const float *sx;
+    LoraAdd add;
+};
+
+__device__ __forceinline__ void bt_store_y4(int32_t *, const BtLoraEpi &e, int M, int n, int m, bt_v4i v) {
+    const int32_t a[4] = {v.x, v.y, v.z, v.w};
+    const float sx = e.sx[n];
+    float s[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) s[k] = m + k < M ? (float)a[k] * e.sw[m + k] * sx : 0.f;
+    e.add.rows<4, 2>(s, n, m, M);
+    const int64_t at = (int64_t)n * M + m;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        if (m + k < M) e.Yh[at + k] = bsp_f2h(s[k]);
+}
+
 // Rows m .. m+3 of column n (those below M).
 __device__ __forceinline__ void bt_store_y4(int32_t *Y, const BtEpi &e, int M, int n, int m, bt_v4i v) {
     const int64_t at = (int64_t)n * M + m;
@@ -773,12 +794,12 @@ __device__ __forceinline__ void bt_make_b(const uint32_t (&xw)[NB][TPL][8], bt_v
 // The work of one workgroup; gid is its index among the workgroups of its
 // matrix (the plain kernel's block index, or its place in a grouped launch).
 // WB: width of a stored weight value (4: int4; 2: int2, the W2A4 variant).
-template <int NB, int D, bool XU, int NBLK = BTS_NBLK, int WB = 4>
+template <int NB, int D, bool XU, int NBLK = BTS_NBLK, int WB = 4, class Epi>
 __device__ __forceinline__ void bts_body(
         int gid, const uint32_t *__restrict__ offsets, int M, int K, int bq, int br,
         const uint64_t *__restrict__ bitmaps, const uint8_t *__restrict__ X, int N,
         const uint8_t *__restrict__ payload, uint32_t payload_bytes, int32_t *__restrict__ Y, uint32_t stagger,
-        uint32_t area_kb, const BtEpi epi) {
+        uint32_t area_kb, const Epi epi) {
     constexpr int TPL = 2, WC = 8;
     extern __shared__ __attribute__((aligned(16))) uint8_t bt_smem[];
     const int nwaves = blockDim.x >> 6;
@@ -1273,6 +1294,36 @@ static void launch_bt64_t(const BtPlan &p, const uint64_t *bitmaps, const uint32
         launch_bt64_s<NB, TPL, XU, true>(p, bitmaps, offsets, payload, payload_bytes, M, K, X, N, Y, e, stream);
     else
         launch_bt64_s<NB, TPL, XU, false>(p, bitmaps, offsets, payload, payload_bytes, M, K, X, N, Y, e, stream);
+}
+
+// The streaming kernel with adapters in its final write.
+template <int NB, int D, bool XU>
+__global__ __launch_bounds__(512) void k_bt64s_lora(
+        const uint32_t *__restrict__ offsets, int M, int K, int bq, int br, const uint64_t *__restrict__ bitmaps,
+        const uint8_t *__restrict__ X, int N, const uint8_t *__restrict__ payload, uint32_t payload_bytes,
+        uint32_t stagger, uint32_t area_kb, const BtLoraEpi epi) {
+    bts_body<NB, D, XU>((int)blockIdx.x, offsets, M, K, bq, br, bitmaps, X, N, payload, payload_bytes,
+                        (int32_t *)nullptr, stagger, area_kb, epi);
+}
+
+template <bool XU>
+static void launch_bt64s_lora(const BtPlan &p, const uint64_t *bitmaps, const uint32_t *offsets,
+                              const uint8_t *payload, uint32_t payload_bytes, int M, int K, const uint8_t *X, int N,
+                              const BtLoraEpi &e, hipStream_t stream) {
+#define BTL_LAUNCH(NB, D)                                                                                             \
+    do {                                                                                                              \
+        (void)hipFuncSetAttribute((const void *)k_bt64s_lora<NB, D, XU>, hipFuncAttributeMaxDynamicSharedMemorySize, \
+                                  (int)p.lds);                                                                        \
+        hipLaunchKernelGGL((k_bt64s_lora<NB, D, XU>), dim3(p.grid), dim3(64 * p.nwaves), p.lds, stream, offsets, M, K, \
+                           p.bq, p.br, bitmaps, X, N, payload, payload_bytes, (uint32_t)p.stagger,                    \
+                           (uint32_t)p.area_kb, e);                                                                   \
+    } while (0)
+    if (p.nb == 1) {
+        if (p.streaming == 2) BTL_LAUNCH(1, 2); else if (p.streaming == 3) BTL_LAUNCH(1, 3); else BTL_LAUNCH(1, 4);
+    } else {
+        if (p.streaming == 2) BTL_LAUNCH(2, 2); else if (p.streaming == 3) BTL_LAUNCH(2, 3); else BTL_LAUNCH(2, 4);
+    }
+#undef BTL_LAUNCH
 }
 
 template <bool XU>

@@ -33,27 +33,53 @@ __device__ __forceinline__ int lora_of(const LoraArgs &a, int n, int *rank) {
 typedef _Float16 lora_h8 __attribute__((ext_vector_type(8)));
 typedef float lora_f4 __attribute__((ext_vector_type(4)));
 
-// s + B_a[m] t_n, 8 rank positions at a time; what lies past the rank (any
-// bits) is replaced by zero.
+// s[i] + B_a[m + i] t_n, 8 rank positions a load; what lies past the rank (any
+// bits) is replaced by zero. The loads of PIECES positions are issued before
+// the first is used: the tail of the sparse kernels has too few wavefronts to
+// hide one load after the other.
 struct LoraAdd {
     LoraArgs a;
-    __device__ __forceinline__ float to(float s, int n, int m, int M) const {
+
+    template <int ROWS, int PIECES>
+    __device__ __forceinline__ void rows(float (&s)[ROWS], int n, int m, int M) const {
         int rank;
         const int i = lora_of(a, n, &rank);
-        if (i < 0) return s;
+        if (i < 0) return;
         const uint16_t *row = a.B + ((int64_t)i * M + m) * a.R;
         const float *t = a.t + (int64_t)n * a.R;
-        float u = 0.f;
-        for (int r = 0; r < rank; r += 8) {
-            const lora_h8 b = *reinterpret_cast<const lora_h8 *>(row + r);
-            const lora_f4 t0 = *reinterpret_cast<const lora_f4 *>(t + r), t1 = *reinterpret_cast<const lora_f4 *>(t + r + 4);
+        float u[ROWS];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float bj = r + j < rank ? (float)b[j] : 0.f;
-                u = fmaf(bj, j < 4 ? t0[j & 3] : t1[j & 3], u);
+        for (int k = 0; k < ROWS; ++k) u[k] = 0.f;
+        for (int r0 = 0; r0 < rank; r0 += 8 * PIECES) {
+            lora_h8 b[PIECES][ROWS];
+            lora_f4 v[PIECES][2];
+#pragma unroll
+            for (int p = 0; p < PIECES; ++p) {
+                // (past the rank: the piece at r0 again)
+                const int r = r0 + 8 * p < rank ? r0 + 8 * p : r0;
+                v[p][0] = *reinterpret_cast<const lora_f4 *>(t + r);
+                v[p][1] = *reinterpret_cast<const lora_f4 *>(t + r + 4);
+#pragma unroll
+                for (int k = 0; k < ROWS; ++k)
+                    b[p][k] = *reinterpret_cast<const lora_h8 *>(row + (int64_t)(m + k < M ? k : 0) * a.R + r);
             }
+#pragma unroll
+            for (int p = 0; p < PIECES; ++p)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const bool in = r0 + 8 * p + j < rank;
+#pragma unroll
+                    for (int k = 0; k < ROWS; ++k) u[k] = fmaf(in ? (float)b[p][k][j] : 0.f, v[p][j >> 2][j & 3], u[k]);
+                }
         }
-        return s + u;
+#pragma unroll
+        for (int k = 0; k < ROWS; ++k) s[k] += u[k];
+    }
+
+    __device__ __forceinline__ float to(float s, int n, int m, int M) const {
+        float v[1] = {s};
+        rows<1, 4>(v, n, m, M);
+        return v[0];
     }
 };
 
@@ -96,7 +122,8 @@ __global__ __launch_bounds__(64 * LORA_WAVES) void k_lora_down(const LoraArgs a,
     }
 }
 
-// The dequantised int32 sums with the adapters' part, rounded once.
+// The dequantised int32 sums with the adapters' part, rounded once (for the
+// int4 kernels whose final write does not do it: K past 4096).
 __global__ __launch_bounds__(256) void k_lora_dq(const LoraAdd add, const int32_t *__restrict__ Y32, int M,
                                                  const float *__restrict__ sw, const float *__restrict__ sx,
                                                  uint16_t *__restrict__ Yh) {

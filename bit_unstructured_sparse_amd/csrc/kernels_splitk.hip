@@ -776,7 +776,8 @@ static int64_t sk_ws_counters_bytes() { return (int64_t)SK_WS_COUNTERS * 4; }
 // or 4; then the set holds as many blocks, so that a workgroup decodes one
 // block's worth of weights with 1 / splits of X). Returns false if the shape
 // is outside (N > 32, K >= 2^25, or an LDS plan that does not fit).
-static bool sk_plan(int dtype, int64_t M, int64_t K, int64_t N, int64_t payload_bytes, int splits, SkPlan *p) {
+static bool sk_plan(int dtype, int64_t M, int64_t K, int64_t N, int64_t payload_bytes, int splits, SkPlan *p,
+                    int most_waves = 16) {
     if (M <= 0 || K <= 0 || N < 1 || N > 32 || splits < 1 || splits > SK_NBS_MAX) return false;
     const int64_t T = (K + 63) / 64, blocks = (M + 15) / 16;
     if (splits > 1 && T < 2 * splits) return false;               // at least two tiles per split
@@ -795,7 +796,7 @@ static bool sk_plan(int dtype, int64_t M, int64_t K, int64_t N, int64_t payload_
     p->nsets = (int)((blocks + p->nbs - 1) / p->nbs);
     p->tps = (int)((T + splits - 1) / splits);
     const int per_wave = dtype == BSP_INT4 ? 8 : 4;                 // tiles per wavefront and chunk
-    const int max_waves = dtype == BSP_INT4 ? 8 : 16;
+    const int max_waves = dtype == BSP_INT4 ? 8 : most_waves;
     // wavefronts: enough for the split's tiles, fewer (shorter chunks, smaller
     // slots) when the slots of a dense set would not fit the LDS
     int nw = (int)std::min<int64_t>(max_waves, (std::min<int64_t>(p->tps, (int64_t)per_wave * max_waves) + per_wave - 1) / per_wave);

@@ -260,32 +260,12 @@ bool workspace_usable(const void *ws, int64_t bytes) {
     return ws != nullptr && bytes > 0 && ((uintptr_t)ws & 255u) == 0;
 }
 
-// The product of one call; `add` (fp16 only) is what the kernels add to each
-// sum before rounding it.
+// Launches a plan; `add` (fp16 only) is what the kernels add to each sum
+// before rounding it.
 template <class Add = NoAdd>
-int spmm_common(int dtype, const uint64_t *bitmaps, const uint32_t *offsets, const void *payload,
+int launch_plan(int dtype, const Plan &p, const uint64_t *bitmaps, const uint32_t *offsets, const void *payload,
                 int64_t payload_bytes, int64_t M, int64_t K, const void *X, int64_t N, void *Y, void *workspace,
-                int64_t workspace_bytes, int algo, hipStream_t stream, const Add &add = Add{}) {
-    Shape s;
-    int rc = check_args(bitmaps, offsets, payload, payload_bytes, M, K, X, N, Y, algo, &s);
-    if (rc != BSP_OK || M == 0 || N == 0) return rc;
-    if (workspace_bytes < 0 || (workspace == nullptr && workspace_bytes != 0)) return BSP_E_ARG;
-    if (workspace != nullptr && ((uintptr_t)workspace & 255u) != 0) return BSP_E_ARG;
-    const bool have_ws = workspace_usable(workspace, workspace_bytes);
-    Plan p;
-    rc = choose_plan(dtype, s, payload_bytes, algo, have_ws, &p);
-    if (rc != BSP_OK) return rc;
-    // The int4 MFMA and split-K kernels read X in whole dwords from its start
-    // (the last one may reach up to 3 bytes past N * ceil(K/2), inside the
-    // same page only when X starts on a 4-byte boundary); fp16 ones read
-    // 16-byte pieces. An X off the boundary takes the plain kernel (automatic
-    // choice) or is refused (forced).
-    const bool x_aligned = ((uintptr_t)X & (dtype == BSP_INT4 ? 3u : 15u)) == 0;
-    if (p.kind != PK_ROWWAVE && !x_aligned) {
-        if (algo != BSP_ALGO_AUTO) return BSP_E_UNSUPPORTED;
-        p = Plan{};
-    }
-    if (p.ws_bytes() > workspace_bytes) return BSP_E_CAPACITY;
+                hipStream_t stream, const Add &add = Add{}) {
     const uint32_t pb = (uint32_t)payload_bytes;
     switch (p.kind) {
         case PK_BT64:
@@ -314,6 +294,32 @@ int spmm_common(int dtype, const uint64_t *bitmaps, const uint32_t *offsets, con
             break;
     }
     return launch_status();
+}
+
+int spmm_common(int dtype, const uint64_t *bitmaps, const uint32_t *offsets, const void *payload,
+                int64_t payload_bytes, int64_t M, int64_t K, const void *X, int64_t N, void *Y, void *workspace,
+                int64_t workspace_bytes, int algo, hipStream_t stream) {
+    Shape s;
+    int rc = check_args(bitmaps, offsets, payload, payload_bytes, M, K, X, N, Y, algo, &s);
+    if (rc != BSP_OK || M == 0 || N == 0) return rc;
+    if (workspace_bytes < 0 || (workspace == nullptr && workspace_bytes != 0)) return BSP_E_ARG;
+    if (workspace != nullptr && ((uintptr_t)workspace & 255u) != 0) return BSP_E_ARG;
+    const bool have_ws = workspace_usable(workspace, workspace_bytes);
+    Plan p;
+    rc = choose_plan(dtype, s, payload_bytes, algo, have_ws, &p);
+    if (rc != BSP_OK) return rc;
+    // The int4 MFMA and split-K kernels read X in whole dwords from its start
+    // (the last one may reach up to 3 bytes past N * ceil(K/2), inside the
+    // same page only when X starts on a 4-byte boundary); fp16 ones read
+    // 16-byte pieces. An X off the boundary takes the plain kernel (automatic
+    // choice) or is refused (forced).
+    const bool x_aligned = ((uintptr_t)X & (dtype == BSP_INT4 ? 3u : 15u)) == 0;
+    if (p.kind != PK_ROWWAVE && !x_aligned) {
+        if (algo != BSP_ALGO_AUTO) return BSP_E_UNSUPPORTED;
+        p = Plan{};
+    }
+    if (p.ws_bytes() > workspace_bytes) return BSP_E_CAPACITY;
+    return launch_plan(dtype, p, bitmaps, offsets, payload, payload_bytes, M, K, X, N, Y, workspace, stream);
 }
 
 }  // namespace
@@ -786,12 +792,20 @@ extern "C" int spmm_bitmap_f16_lora(const uint64_t *bitmaps, const uint32_t *off
     Plan p;
     rc = choose_plan(BSP_FP16, s, payload_bytes, BSP_ALGO_AUTO, true, &p);
     if (rc != BSP_OK) return rc;
+    if (p.kind != PK_ROWWAVE && ((uintptr_t)X & 15u) != 0) p = Plan{};     // fp16 kernels read 16-byte pieces of X
+    // Split plans that count on two workgroups a CU: at 120 registers a lane
+    // two of 16 wavefronts do not fit (4096 x 11008 at density 0.3, N = 8:
+    // 39 us, with 8 wavefronts 23).
+    if (p.kind == PK_BSK && p.sk.S > 1 && p.sk.grid > BT_CUS && p.sk.nwaves > 8) {
+        SkPlan q;
+        if (sk_plan(BSP_FP16, M, K, N, payload_bytes, p.sk.S, &q, 8)) p.sk = q;
+    }
     const LoraSpace sp = lora_space(BSP_FP16, p.ws_bytes(), M, N, lora->rank);
     if (workspace == nullptr || workspace_bytes < sp.bytes) return BSP_E_CAPACITY;
     const LoraArgs a = lora_args(lora, (uint8_t *)workspace + sp.t);
     launch_lora_down(a, X, N, K, stream);
-    return spmm_common(BSP_FP16, bitmaps, offsets, payload, payload_bytes, M, K, X, N, Y, workspace, sp.t, BSP_ALGO_AUTO,
-                       stream, LoraAdd{a});
+    return launch_plan(BSP_FP16, p, bitmaps, offsets, payload, payload_bytes, M, K, X, N, Y, workspace, stream,
+                       LoraAdd{a});
 }
 
 extern "C" int spmm_bitmap_w4a4_dq_lora(const uint64_t *bitmaps, const uint32_t *offsets, const uint8_t *payload,
@@ -813,6 +827,16 @@ extern "C" int spmm_bitmap_w4a4_dq_lora(const uint64_t *bitmaps, const uint32_t 
     const LoraArgs a = lora_args(lora, (uint8_t *)workspace + sp.t);
     int32_t *Y32 = (int32_t *)((uint8_t *)workspace + sp.y32);
     launch_lora_down(a, X16, N, K, stream);
+    if (p.kind == PK_BT64 && p.bt.streaming && ((uintptr_t)X & 3u) == 0) {
+        const BtLoraEpi e{Yh, scale_w, scale_x, LoraAdd{a}};
+        if (K % 8 == 0)
+            launch_bt64s_lora<false>(p.bt, bitmaps, offsets, payload, (uint32_t)payload_bytes, (int)M, (int)K, X, (int)N,
+                                     e, stream);
+        else
+            launch_bt64s_lora<true>(p.bt, bitmaps, offsets, payload, (uint32_t)payload_bytes, (int)M, (int)K, X, (int)N,
+                                    e, stream);
+        return launch_status();
+    }
     rc = spmm_common(BSP_INT4, bitmaps, offsets, payload, payload_bytes, M, K, X, N, Y32, workspace, sp.t, BSP_ALGO_AUTO,
                      stream);
     if (rc != BSP_OK) return rc;
