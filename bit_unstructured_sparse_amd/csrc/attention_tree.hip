@@ -1,5 +1,50 @@
 // attention_tree.hip -- attention of drafted token trees over the paged
 // key/value cache, for gfx950.
+//
+// Mathematics. For one kv head, with query rows r (drafted token, query head)
+// and cached tokens j, x_rj = scale log2(e) q_r.k_j and
+//     O_r = sum_j 2^(x_rj - m_r) v_j / sum_j 2^(x_rj - m_r)
+// over the tokens r sees, in one pass over the cache: m_r is a running maximum,
+// and sums made before it moved are scaled by 2^(old - new). A quantised row
+// is s u + o (u unsigned codes), so
+//     q.k_j = s_j (q.u_j) + o_j sum(q),
+//     sum_j w_j v_j = sum_j (w_j s_j) u_j + sum_j w_j o_j :
+// the codes go through the products as they are, and steps and offsets are
+// applied to scores and weights, per token and not per channel.
+//
+// Both products are v_mfma_f32_16x16x32_f16. Scores are computed transposed (A =
+// 16 cached tokens, B = 16 query rows), so that a lane ends with the scores of
+// 8 neighbouring tokens for one query row: exactly its part of the second
+// product's B operand (32 tokens x 16 rows), whose A operand is V transposed, put
+// together in registers by byte permutes. No score, weight or V passes through
+// LDS. Codes enter as fp16 subnormals (u 2^-24: the code in the low byte of a
+// 16-bit lane), which the MFMA multiplies exactly; int4 codes with odd channel
+// stay in the high nibble (16 u 2^-24).
+//
+// Numbers. Weights are scaled by 2^6 and the maximum is moved only when a score
+// passes it by 2^8, so they stay below 2^14 and are normal fp16 numbers down to
+// 2^-20 of the maximum; their 11 bits are the one rounding between the products,
+// independent from token to token. For quantised values the step enters the
+// weight relative to a common power of two, and the sum of the rounded weights
+// times the middle code is taken off again: what is rounded counts from the
+// middle of the codes, not from their end. Sums, maxima and normalisations are fp32.
+//
+// What bounds it. With few query rows, the cache's bytes: 131072 tokens x 8 kv
+// heads, one token, fp16 122 us (4.4 TB/s; a copy reaches 4.7 counting both ways),
+// int8 63 (4.4 TB/s). Past 32 query rows per kv head the vector unit: per 32 tokens
+// and 32 rows about 300 VALU instructions (half of them the decoding of codes,
+// masks and addresses, done by each wavefront of the rows) beside 32 MFMAs; 65536
+// int8 tokens, 128 rows, 89 us (384 TFLOP/s; counters: vector unit 51 % busy,
+// matrix cores 18 %). Short calls are bound by latency: launch, lengths, block
+// table, first tile, join, about 6 us for 16 tokens.
+//
+// Taken and dropped, measured at the same sizes: 4 row tiles per wavefront (one
+// wavefront per SIMD: trees of 16 at 8192 tokens 169 us against 112), 3 wavefronts
+// per SIMD for 16 rows (spills: 10.4 against 9.8 for one token, 28.7 against 29.9
+// for a batch of 32), the last workgroup of a sequence joining all parts of 64 rows
+// (218 us against 128 with a kernel of its own), masks as comparisons (16 pairs of
+// scalar registers in flight, spilled), rows written from registers without LDS
+// (16-byte pieces at 512-byte strides: trees 87 us against 63).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -71,23 +116,24 @@ __device__ __forceinline__ void at_write(AtLate ap, int q0, int kvh, int G, int 
 typedef _Float16 at_h8 __attribute__((ext_vector_type(8)));
 typedef _Float16 at_h2 __attribute__((ext_vector_type(2)));
 
-#ifndef AT_GROUPS
-#define AT_GROUPS 512
-#endif
 #define AT_WAVES 4
+// Workgroups aimed at: the two per CU that fit (their registers allow 2
+// wavefronts per SIMD), in one round. 448: trees 65.8 us against 63.4, long fp16
+// 135 against 124; 768: 75 and 132.
+#define AT_GROUPS 512
 #define AT_TILE 32                 // cached tokens per wavefront and step
 #define AT_BOOST 6.0f              // log2: the weights' scale, 2^6 at the running maximum
 #define AT_SLACK 8.0f              // log2: how far a score may pass the running maximum before it is moved
 // Query rows of a row block: 16 where a call has no more, else four wavefronts of 16 RT.
 #define AT_ROWS(RT) ((RT) == 1 ? (D == 256 ? 64 : 16) : 64 * (RT))
 #define AT_LOW -1e30f              // stands for the maximum of no scores when sums are joined
-#define AT_NONE -3e38f
+#define AT_NONE -3e38f             // `limit` of a row without a score yet
 
 // What a lane reads of a K row and of a V row. A K row goes to the four lanes
 // of its A row in pieces of PIECE bytes in turn, so that one load instruction
-// takes whole 64-byte stretches of 16 rows (a contiguous quarter of the row
-// per lane instead touched every line of the rows with each of its loads:
-// 131072 fp16 tokens 224 -> NEW us). A V row goes to 16 lanes, a sixteenth each.
+// takes whole 64-byte stretches of 16 rows (with a contiguous quarter of the
+// row per lane each of its loads touches every line of the rows: 131072 fp16
+// tokens 224 us against 218). A V row goes to 16 lanes, a sixteenth each.
 template <int KIND, int D>
 struct AtShape {
     static constexpr int ROW = KIND == BSP_FP16 ? 2 * D : KIND == BSP_INT8 ? D : D / 2;
@@ -872,14 +918,20 @@ AtPlan at_plan(const bsp_kv_cache *c, int64_t table_width, int64_t B, int64_t ma
     p.row_blocks = (int)((rows + p.block_rows - 1) / p.block_rows);
     p.slot_rows = (int)std::min<int64_t>(p.block_rows, rows);
     p.max_chunks = (int)B;
-    p.min_per = 4 * AT_WAVES;                // four tiles per wavefront at least
+    // four tiles per wavefront at least (two: one token at 500 cached 9.8 us
+    // against 9.3; longer calls alike)
+    p.min_per = 4 * AT_WAVES;
     const int64_t heads = c->kv_heads * p.row_blocks;
     const int64_t tiles = (table_width * c->page_size + AT_TILE - 1) / AT_TILE;      // of the longest sequence
-    if (split && B * heads <= AT_WS_COUNTERS) {
+    // (all work in 32 bits: sequences may share pages, so B * tiles is not bounded by the cache)
+    if (split && B * heads <= AT_WS_COUNTERS && B * tiles <= INT32_MAX / 4 - B) {
         const int64_t want = std::max<int64_t>(1, AT_GROUPS / heads);
         const int64_t side = p.slot_rows <= 16 * p.rt ? 1 : p.slot_rows <= 32 * p.rt ? 2 : 4;
         const int64_t most = B * std::max<int64_t>(1, (tiles * side + p.min_per - 1) / p.min_per);
         p.chunks = p.max_chunks = (int)std::min(want, most);
+        // Few parts of few rows are joined by the last of them to arrive, others
+        // by a kernel of their own: joining is 3 loads a part and 8 channels, one
+        // part after another, on one workgroup per row block.
         p.join = p.chunks > B && (rows > 16 || p.chunks > 8 * B);
         p.ws_bytes = AT_WS_COUNTERS * 4 + 2 * p.chunks * heads * p.slot_rows * (D + 4) * 4;
     }
@@ -958,6 +1010,8 @@ extern "C" int attention_tree_f16(const uint16_t *Q, int64_t q_stride, const bsp
     if (q_stride < q_heads * cache->head_dim || o_stride < q_heads * cache->head_dim) return BSP_E_ARG;
     if ((((uintptr_t)Q | (uintptr_t)O) & 1u) != 0 || ((uintptr_t)tree_mask & 7u) != 0) return BSP_E_ARG;
     const AtPlan p = at_plan(cache, table_width, B, max_q, q_heads, workspace != nullptr);
+    // a launch holds fewer than 2^32 threads
+    if (((int64_t)p.max_chunks * cache->kv_heads + 7) * p.row_blocks >= (int64_t)1 << 24) return BSP_E_OVERFLOW;
     if (p.ws_bytes > workspace_bytes) return BSP_E_CAPACITY;
     AtArgs a{};
     a.Q = Q, a.q_stride = q_stride;

@@ -507,7 +507,8 @@ typedef struct bsp_kv_cache {
  *             output will do. Strides >= kv_heads * head_dim.
  *   slots     DEVICE int64 [n]. A slot outside [0, num_pages * page_size) is
  *             skipped; two tokens of one call must not share a slot.
- * n == 0 or kv_heads == 0 launches nothing.
+ * n == 0 or kv_heads == 0 launches nothing; n * kv_heads >= 2^28 is refused
+ * (BSP_E_OVERFLOW), here and in kv_cache_gather.
  */
 int kv_cache_append(const bsp_kv_cache *cache, const uint16_t *K, int64_t k_stride, const uint16_t *V,
                     int64_t v_stride, const int64_t *slots, int64_t n, hipStream_t stream);
@@ -564,6 +565,8 @@ int attention_tree_workspace_bytes(const bsp_kv_cache *cache, int64_t table_widt
  *   max_q        most drafted tokens of a sequence, 0..BSP_TREE_MAX; rows past it are
  *                not computed.
  *   tree_mask    DEVICE uint64 [total_q], or NULL for chains.
+ *   q_heads      a multiple of kv_heads, at most 16384 of them per kv head
+ *                (BSP_E_UNSUPPORTED past that).
  *   scale        finite.
  *   O            DEVICE fp16, token row r at element r * o_stride. Must not overlap Q.
  *   workspace    DEVICE, NULL (one workgroup walks all of a sequence) or

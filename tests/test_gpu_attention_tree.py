@@ -292,3 +292,41 @@ def test_offsets_past_32_bits(dev):
     for h in range(hkv):
         want, spread = serving.attend(Q[:, h:h + 1], K[:, h].astype(np.float64), V[:, h].astype(np.float64), D ** -0.5)
         assert (np.abs(O[:, h:h + 1].cpu().numpy() - want) <= 2.0 ** -10 * spread + 1e-4).all()
+
+
+def test_python_refusals(dev):
+    c = Case(12, [(2, 20)], 4, 2, 64, "int8", 16, dev)
+    Q, cache = torch.from_numpy(c.Q).to(dev), c.cache
+    table = torch.from_numpy(c.table).to(dev)
+    one = torch.tensor([20], dtype=torch.int32, device=dev)
+    qs = torch.tensor([0, 2], dtype=torch.int32, device=dev)
+    ok = (Q, cache, table, one, qs, 2)
+    assert bsp.attention_tree(*ok).shape == (2, 4, 64)
+
+    def bad(exc, i, value, **kw):
+        with pytest.raises(exc):
+            bsp.attention_tree(*(value if i == j else a for j, a in enumerate(ok)), **kw)
+
+    bad(TypeError, 0, Q.float())
+    bad(TypeError, 0, Q.cpu())
+    bad(ValueError, 0, Q[..., :32])
+    bad(ValueError, 0, Q.transpose(0, 1))
+    bad(bsp.BspError, 0, torch.cat([Q, Q[:, :1]], 1))          # 5 query heads over 2 kv heads
+    bad(TypeError, 2, table.long())
+    bad(ValueError, 2, table[0])
+    bad(ValueError, 3, torch.zeros(2, dtype=torch.int32, device=dev))
+    bad(ValueError, 4, one)
+    bad(bsp.BspError, 5, 65)
+    bad(TypeError, 9, None, tree_mask=torch.zeros(2, dtype=torch.int32, device=dev))
+    bad(ValueError, 9, None, tree_mask=torch.zeros(3, dtype=torch.int64, device=dev))
+    bad(ValueError, 9, None, O=torch.empty(3, 4, 64, dtype=torch.float16, device=dev))
+    bad(bsp.BspError, 9, None, scale=float("nan"))
+    bad(bsp.BspError, 9, None, workspace=torch.zeros(256, dtype=torch.uint8, device=dev))
+    with pytest.raises(ValueError):
+        bsp.kv_append(cache, Q[:, :2], Q[:1, :2], torch.zeros(2, dtype=torch.int64, device=dev))
+    with pytest.raises(TypeError):
+        bsp.kv_append(cache, Q[:, :2], Q[:, :2], torch.zeros(2, dtype=torch.int32, device=dev))
+    with pytest.raises(ValueError):
+        bsp.KVCache(bsp.INT8, cache.k, cache.v, cache.k_scale[:1], cache.v_scale)
+    with pytest.raises(ValueError):
+        bsp.KVCache(bsp.FP16, cache.k.half(), cache.v.half(), cache.k_scale, None)
