@@ -18,8 +18,7 @@
 // product's B operand (32 tokens x 16 rows), whose A operand is V transposed, put
 // together in registers by byte permutes. No score, weight or V passes through
 // LDS. Codes enter as fp16 subnormals (u 2^-24: the code in the low byte of a
-// 16-bit lane), which the MFMA multiplies exactly; int4 codes with odd channel
-// stay in the high nibble (16 u 2^-24).
+// 16-bit lane; int4 16 u 2^-24), which the MFMA multiplies exactly.
 //
 // Numbers. Weights are scaled by 2^6 and the maximum is moved only when a score
 // passes it by 2^8, so they stay below 2^14 and are normal fp16 numbers down to
@@ -39,9 +38,7 @@
 // table, first tile, join, about 6 us for 16 tokens.
 //
 // Taken and dropped, measured at the same sizes: 4 row tiles per wavefront (one
-// wavefront per SIMD: trees of 16 at 8192 tokens 169 us against 112), 3 wavefronts
-// per SIMD for 16 rows (spills: 10.4 against 9.8 for one token, 28.7 against 29.9
-// for a batch of 32), the last workgroup of a sequence joining all parts of 64 rows
+// wavefront per SIMD: trees of 16 at 8192 tokens 169 us against 112), the last workgroup of a sequence joining all parts of 64 rows
 // (218 us against 128 with a kernel of its own), masks as comparisons (16 pairs of
 // scalar registers in flight, spilled), rows written from registers without LDS
 // (16-byte pieces at 512-byte strides: trees 87 us against 63).
@@ -117,10 +114,7 @@ typedef _Float16 at_h8 __attribute__((ext_vector_type(8)));
 typedef _Float16 at_h2 __attribute__((ext_vector_type(2)));
 
 #define AT_WAVES 4
-// Workgroups aimed at: the two per CU that fit (their registers allow 2
-// wavefronts per SIMD), in one round. 448: trees 65.8 us against 63.4, long fp16
-// 135 against 124; 768: 75 and 132.
-#define AT_GROUPS 512
+#define AT_CUS 256
 #define AT_TILE 32                 // cached tokens per wavefront and step
 #define AT_BOOST 6.0f              // log2: the weights' scale, 2^6 at the running maximum
 #define AT_SLACK 8.0f              // log2: how far a score may pass the running maximum before it is moved
@@ -128,6 +122,15 @@ typedef _Float16 at_h2 __attribute__((ext_vector_type(2)));
 #define AT_ROWS(RT) ((RT) == 1 ? (D == 256 ? 64 : 16) : 64 * (RT))
 #define AT_LOW -1e30f              // stands for the maximum of no scores when sums are joined
 #define AT_NONE -3e38f             // `limit` of a row without a score yet
+
+// Workgroups per CU that the kernels are compiled for and the work is cut to
+// (their registers; a wavefront each per SIMD): one round, no workgroup waits
+// for another. D = 128: aiming at 448 workgroups, trees 65.8 us against 63.4
+// and long fp16 135 against 124; at 768, 75 and 132; int4 with few rows fits
+// three, and 768 then took 28.0 against 30.2 for the batch of uneven lengths but
+// 39.8 against 34.8 for 32 sequences of 4096. D = 256, 512 against 256: int8
+// 30,000 tokens x 2 44.3 us against 38.3.
+constexpr int at_per_cu(int dim) { return dim == 256 ? 1 : 2; }
 
 // What a lane reads of a K row and of a V row. A K row goes to the four lanes
 // of its A row in pieces of PIECE bytes in turn, so that one load instruction
@@ -145,6 +148,7 @@ struct AtShape {
     static constexpr int VW = VB < 4 ? 1 : VB / 4;
     static constexpr int NT = D / 16;                        // 16-channel blocks of the output
     static constexpr int STEPS = D / 32;                     // MFMAs along the channels
+    static constexpr float UNIT = KIND == BSP_INT8 ? 0x1p24f : 0x1p20f;      // a code over what stands for it
 };
 
 // Agent-scope 16-byte stores and loads of the partial sums: they go to the
@@ -195,14 +199,18 @@ __device__ __forceinline__ void at_load(const uint8_t *p, uint32_t (&r)[N]) {
 }
 
 // Bytes 2k, 2k + 1 of a dword, or byte k of two dwords, as the low bytes of
-// two 16-bit lanes: fp16 subnormals u * 2^-24, which the MFMA takes exactly.
+// two 16-bit lanes: fp16 subnormals u * 2^-24. The MFMA multiplies them exactly,
+// and lines products up by the exponents of their factors, so a subnormal's
+// leading zeros are bits its sums lose: int4 codes sit in bits 4 .. 7 for that
+// (as 16 u; in bits 0 .. 3, 606409 int4 tokens came out 7.8e-4 off in norm, half
+// of it a bias, against 2.6e-4).
 __device__ __forceinline__ uint32_t at_bytes(uint32_t hi, uint32_t lo, uint32_t sel) {
     return __builtin_amdgcn_perm(hi, lo, sel);
 }
 
 // The A operand of step `s` of the scores: 8 channels of this lane's K row.
-// int4: even steps hold the even channels of 16, odd steps the odd ones times
-// 16 (the codes stay where they are in their bytes).
+// int4: even steps hold the even channels of 16, odd steps the odd ones, all
+// times 16.
 template <int KIND>
 __device__ __forceinline__ at_h8 at_k_frag(const uint32_t *k, int s) {
     at_u4 f;
@@ -214,8 +222,9 @@ __device__ __forceinline__ at_h8 at_k_frag(const uint32_t *k, int s) {
                   at_bytes(b, b, 0x0C030C02u)};
     } else {
         const uint32_t a = k[s & ~1], b = k[s | 1];
-        const uint32_t m = (s & 1) ? 0x00F000F0u : 0x000F000Fu;
-        f = at_u4{a & m, (a >> 8) & m, b & m, (b >> 8) & m};
+        constexpr uint32_t m = 0x00F000F0u;
+        f = (s & 1) ? at_u4{a & m, (a >> 8) & m, b & m, (b >> 8) & m}
+                    : at_u4{(a << 4) & m, (a >> 4) & m, (b << 4) & m, (b >> 4) & m};
     }
     return __builtin_bit_cast(at_h8, f);
 }
@@ -249,7 +258,7 @@ __device__ __forceinline__ at_h8 at_v_frag(const uint32_t (&v)[8][VW], int t) {
             f[p] = at_bytes(v[2 * p + 1][t >> 2], v[2 * p][t >> 2], 0x0C040C00u + 0x00010001u * (t & 3));
         } else {
             const uint32_t b = at_bytes(v[2 * p + 1][t >> 3], v[2 * p][t >> 3], 0x0C040C00u + 0x00010001u * ((t >> 1) & 3));
-            f[p] = b & ((t & 1) ? 0x00F000F0u : 0x000F000Fu);
+            f[p] = ((t & 1) ? b : b << 4) & 0x00F000F0u;
         }
     }
     return __builtin_bit_cast(at_h8, f);
@@ -376,44 +385,21 @@ struct AtWave {
         at_f4 x[RT][2];
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) x[rt][0] = x[rt][1] = at_f4{0.f, 0.f, 0.f, 0.f};
-        if constexpr (KIND == BSP_INT4) {
-            at_f4 hi[RT][2];
 #pragma unroll
-            for (int rt = 0; rt < RT; ++rt) hi[rt][0] = hi[rt][1] = at_f4{0.f, 0.f, 0.f, 0.f};
+        for (int s = 0; s < Sh::STEPS; ++s) {
+            const at_h8 f = at_k_frag<KIND>(k[0], s), g = at_k_frag<KIND>(k[1], s);
 #pragma unroll
-            for (int s = 0; s < Sh::STEPS; s += 2) {
-                const at_h8 f0 = at_k_frag<KIND>(k[0], s), f1 = at_k_frag<KIND>(k[0], s + 1);
-                const at_h8 g0 = at_k_frag<KIND>(k[1], s), g1 = at_k_frag<KIND>(k[1], s + 1);
-#pragma unroll
-                for (int rt = 0; rt < RT; ++rt) {
-                    const at_h8 q0 = q_frag(rt, s), q1 = q_frag(rt, s + 1);
-                    x[rt][0] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f0, q0, x[rt][0], 0, 0, 0);
-                    x[rt][1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(g0, q0, x[rt][1], 0, 0, 0);
-                    hi[rt][0] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f1, q1, hi[rt][0], 0, 0, 0);
-                    hi[rt][1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(g1, q1, hi[rt][1], 0, 0, 0);
-                }
-            }
-#pragma unroll
-            for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) x[rt][e >> 2][e & 3] = fmaf(hi[rt][e >> 2][e & 3], 0.0625f, x[rt][e >> 2][e & 3]);
-        } else {
-#pragma unroll
-            for (int s = 0; s < Sh::STEPS; ++s) {
-                const at_h8 f = at_k_frag<KIND>(k[0], s), g = at_k_frag<KIND>(k[1], s);
-#pragma unroll
-                for (int rt = 0; rt < RT; ++rt) {
-                    const at_h8 qs = q_frag(rt, s);
-                    x[rt][0] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f, qs, x[rt][0], 0, 0, 0);
-                    x[rt][1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(g, qs, x[rt][1], 0, 0, 0);
-                }
+            for (int rt = 0; rt < RT; ++rt) {
+                const at_h8 qs = q_frag(rt, s);
+                x[rt][0] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f, qs, x[rt][0], 0, 0, 0);
+                x[rt][1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(g, qs, x[rt][1], 0, 0, 0);
             }
         }
         __builtin_amdgcn_sched_barrier(0);
         // scores in log2 units, less the running maximum (mb):
-        // scale * log2(e) * (s u.q 2^-24 2^24 + o sum(q)) - mb
+        // scale * log2(e) * (s u.q + o sum(q)) - mb
         float top[RT];
-        const float cc = c * 16777216.0f;
+        const float cc = c * Sh::UNIT;
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) top[rt] = -INFINITY;
 #pragma unroll
@@ -441,14 +427,15 @@ struct AtWave {
             // pairs of scalar registers at a time.)
             const int n = min(max(len - (j0 + 8 * grp), 0), 8);     // tokens there are
             const uint32_t in = (1u << n) - 1u;
+            uint32_t ok[RT];
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt) {
-                const uint32_t ok = visible(j0 + 8 * grp - past, seen[rt]) & in;
+                ok[rt] = visible(j0 + 8 * grp - past, seen[rt]) & in;
                 top[rt] = -INFINITY;
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     const float x0 = x[rt][e >> 2][e & 3];
-                    const uint32_t m = at_spread(ok, e), y = __builtin_bit_cast(uint32_t, x0);
+                    const uint32_t m = at_spread(ok[rt], e), y = __builtin_bit_cast(uint32_t, x0);
                     const float z = __builtin_bit_cast(float, (m & y) | (~m & 0xFF800000u));
                     x[rt][e >> 2][e & 3] = z;
                     top[rt] = fmaxf(top[rt], z);
@@ -480,10 +467,7 @@ struct AtWave {
 #pragma unroll
                 for (int d = 1; d < 16; d <<= 1) odd |= (uint32_t)__shfl_xor((int)odd, d, 64);
 #pragma unroll
-                for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        if ((odd >> e & 1u) != 0u && x[rt][e >> 2][e & 3] != -INFINITY) l[rt] = __builtin_nanf("");
+                for (int rt = 0; rt < RT; ++rt) l[rt] = (ok[rt] & odd) != 0u ? __builtin_nanf("") : l[rt];
             }
         }
         // the largest value step (positive floats order as integers)
@@ -505,10 +489,12 @@ struct AtWave {
         if (moved) {
             float fs = 1.f;
             if constexpr (QUANT) {
-                float sm = 0.f;            // the largest finite step
+                // the largest finite step (an exponent below all ones borrows)
+                uint32_t big = 0;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) sm = fmaxf(sm, vw[e] < 0x7F800000u ? kv_word_step(vw[e]) : 0.f);
-                sm = fmaxf(at_group_max(sm), sig);
+                for (int e = 0; e < 8; ++e)
+                    big = max(big, vw[e] & (uint32_t)((int32_t)((vw[e] & 0x7F800000u) - 0x7F800000u) >> 31));
+                const float sm = fmaxf(at_group_max(kv_word_step(big)), sig);
                 const uint32_t b = (__builtin_bit_cast(uint32_t, sm) + 0x7FFFFFu) & 0x7F800000u;
                 fs = sig * __builtin_bit_cast(float, 0x7F000000u - b);
                 sig = __builtin_bit_cast(float, b);
@@ -616,7 +602,7 @@ struct AtSeqs {
 // same tiles (their reads of the cache meet in the CU's L1); the sets so
 // formed take the tiles in turn. RT 1 is for calls of at most 16 rows.
 template <int KIND, int D, int RT>
-__global__ __launch_bounds__(64 * AT_WAVES, D == 256 ? 1 : 2) void k_at(const AtArgs a) {
+__global__ __launch_bounds__(64 * AT_WAVES, at_per_cu(D)) void k_at(const AtArgs a) {
     using Sh = AtShape<KIND, D>;
     using Wave = AtWave<KIND, D, RT>;
     extern __shared__ __attribute__((aligned(16))) float at_smem[];
@@ -786,11 +772,10 @@ __global__ __launch_bounds__(64 * AT_WAVES, D == 256 ? 1 : 2) void k_at(const At
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
             const float l = at_group_sum(w.l[rt]), m = w.limit[rt] == AT_NONE ? AT_LOW : w.mb[rt];
-            float os = 0.f, ps = 0.f, up = 1.f;
+            float os = 0.f, ps = 0.f;
             if constexpr (Wave::QUANT) {
                 os = at_group_sum(w.osum[rt]);
                 ps = at_group_sum(w.psum[rt]) * (KIND == BSP_INT8 ? 128.0f : 8.0f);
-                up = 16777216.0f;
             }
             // the lane's channels: NT from (4 grp + r) NT on, for r = 0 .. 3
             const auto y_of = [&](int r, int t) {
@@ -798,10 +783,7 @@ __global__ __launch_bounds__(64 * AT_WAVES, D == 256 ? 1 : 2) void k_at(const At
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     float z = w.acc[rt][t + i][r];
-                    if constexpr (Wave::QUANT) {
-                        const float h = KIND == BSP_INT4 && (i & 1) ? up * 0.0625f : up;
-                        z = fmaf(w.sig, fmaf(z, h, -ps), os);
-                    }
+                    if constexpr (Wave::QUANT) z = fmaf(w.sig, fmaf(z, Sh::UNIT, -ps), os);
                     y[i] = z;
                 }
                 return y;
@@ -925,7 +907,7 @@ AtPlan at_plan(const bsp_kv_cache *c, int64_t table_width, int64_t B, int64_t ma
     const int64_t tiles = (table_width * c->page_size + AT_TILE - 1) / AT_TILE;      // of the longest sequence
     // (all work in 32 bits: sequences may share pages, so B * tiles is not bounded by the cache)
     if (split && B * heads <= AT_WS_COUNTERS && B * tiles <= INT32_MAX / 4 - B) {
-        const int64_t want = std::max<int64_t>(1, AT_GROUPS / heads);
+        const int64_t want = std::max<int64_t>(1, (int64_t)AT_CUS * at_per_cu((int)D) / heads);
         const int64_t side = p.slot_rows <= 16 * p.rt ? 1 : p.slot_rows <= 32 * p.rt ? 2 : 4;
         const int64_t most = B * std::max<int64_t>(1, (tiles * side + p.min_per - 1) / p.min_per);
         p.chunks = p.max_chunks = (int)std::min(want, most);
