@@ -29,8 +29,8 @@
 // middle of the codes, not from their end. Sums, maxima and normalisations are fp32.
 //
 // What bounds it. With few query rows, the cache's bytes: 131072 tokens x 8 kv
-// heads, one token, fp16 122 us (4.4 TB/s; a copy reaches 4.7 counting both ways),
-// int8 63 (4.4 TB/s). Past 32 query rows per kv head the vector unit: per 32 tokens
+// heads, one token, fp16 103 us (5.2 TB/s; a copy reaches 4.7 counting both ways),
+// int8 63 (4.4 TB/s), int4 41 (3.5 TB/s). Past 32 query rows per kv head the vector unit: per 32 tokens
 // and 32 rows about 300 VALU instructions (half of them the decoding of codes,
 // masks and addresses, done by each wavefront of the rows) beside 32 MFMAs; 65536
 // int8 tokens, 128 rows, 89 us (384 TFLOP/s; counters: vector unit 51 % busy,
@@ -38,10 +38,11 @@
 // table, first tile, join, about 6 us for 16 tokens.
 //
 // Taken and dropped, measured at the same sizes: 4 row tiles per wavefront (one
-// wavefront per SIMD: trees of 16 at 8192 tokens 169 us against 112), the last workgroup of a sequence joining all parts of 64 rows
-// (218 us against 128 with a kernel of its own), masks as comparisons (16 pairs of
-// scalar registers in flight, spilled), rows written from registers without LDS
-// (16-byte pieces at 512-byte strides: trees 87 us against 63).
+// wavefront per SIMD: trees of 16 at 8192 tokens 169 us against 112), the last
+// workgroup of a sequence joining all parts of 64 rows (218 us against 128 with a
+// kernel of its own), masks as comparisons (16 pairs of scalar registers in
+// flight, spilled), rows written from registers without LDS (16-byte pieces at
+// 512-byte strides: trees 87 us against 63).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
