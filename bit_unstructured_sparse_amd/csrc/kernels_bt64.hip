@@ -149,6 +149,7 @@ struct BtEpi {
     uint16_t *Yh;
     const float *sw;
     const float *sx;
+    NoAdd add;
 };
 
 __device__ __forceinline__ uint16_t bt_dequant(int32_t v, float sw, float sx) {
@@ -177,17 +178,26 @@ struct BtLoraEpi {
     LoraAdd add;
 };
 
-__device__ __forceinline__ void bt_store_y4(int32_t *, const BtLoraEpi &e, int M, int n, int m, bt_v4i v) {
+template <class Item>
+__device__ __forceinline__ void bt_store_item(int32_t *, const BtLoraEpi &e, Item &item, int M, int n, int m, bt_v4i v) {
     const int32_t a[4] = {v.x, v.y, v.z, v.w};
     const float sx = e.sx[n];
     float s[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) s[k] = m + k < M ? (float)a[k] * e.sw[m + k] * sx : 0.f;
-    e.add.rows<4, 2>(s, n, m, M);
+    e.add.close(item, s, m, M);
     const int64_t at = (int64_t)n * M + m;
 #pragma unroll
     for (int k = 0; k < 4; ++k)
         if (m + k < M) e.Yh[at + k] = bsp_f2h(s[k]);
+}
+
+__device__ __forceinline__ void bt_store_y4(int32_t *Y, const BtLoraEpi &e, int M, int n, int m, bt_v4i v) {
+    LoraAdd::Item<4, 2> item;
+    e.add.open(item, n, true);
+    e.add.fetch(item, m, M);
+    e.add.reduce(item);
+    bt_store_item(Y, e, item, M, n, m, v);
 }
 
 // Rows m .. m+3 of column n (those below M).
@@ -213,6 +223,10 @@ __device__ __forceinline__ void bt_store_y4(int32_t *Y, const BtEpi &e, int M, i
         const int32_t a[4] = {v.x, v.y, v.z, v.w};
         for (int k = 0; k < 4 && m + k < M; ++k) Y[at + k] = a[k];
     }
+}
+template <class Item>
+__device__ __forceinline__ void bt_store_item(int32_t *Y, const BtEpi &e, Item &, int M, int n, int m, bt_v4i v) {
+    bt_store_y4(Y, e, M, n, m, v);
 }
 
 // 16 bytes of X at byte offset off. X rows start on a 4-byte boundary when
@@ -836,6 +850,12 @@ __device__ __forceinline__ void bts_body(
     constexpr int PS = WB == 4 ? 8 : 10;                           // log2 of the A x B operand scale
     const uint32_t tmul = stagger ? VPB * 16u * BTS_OVL : 0u;    // values added per run
     const __amdgpu_buffer_rsrc_t prs = bt_rsrc(payload, payload_bytes);
+    // this thread's first item (below): what the epilogue adds to it is loaded
+    // with the last block
+    typename decltype(Epi::add)::template Item<4, 2> item;
+    const int item_ln = (int)threadIdx.x & 63, item_nb = (int)(threadIdx.x >> 6) % NB, item_i = (int)threadIdx.x / (NB * 64);
+    const int item_n = (item_ln & 15) + 16 * item_nb, item_m = (b_begin + item_i) * BT_ROWS + 4 * (item_ln >> 4);
+    epi.add.open(item, item_n, item_i < nblk && item_n < N && item_m < M);
 
     uint32_t nib[NBLK + 1];
 #pragma unroll
@@ -910,7 +930,9 @@ __device__ __forceinline__ void bts_body(
     };
     // one block in flight: the memory system serves it before any later
     // block, which is issued only once block i has landed
+    epi.add.opened(item);
     issue(0);
+    if (nblk == 1) epi.add.fetch(item, item_m, M);
     {
         __attribute__((address_space(3))) uint64_t *lut_lds =
                 (__attribute__((address_space(3))) uint64_t *)(uintptr_t)bt_lds_addr(bt_smem);
@@ -943,9 +965,11 @@ __device__ __forceinline__ void bts_body(
         int32_t *wti = wt + i * BT_ROWS * WC;
         if (q == 3) wti[r * WC + wave] = (int32_t)incl;
         bt_wait_vm(0);   // this wavefront's share of block i landed (nothing later is in flight)
+        if (i == nblk - 1) epi.add.reduce(item);
         if (i + 1 < nblk) {
             load_words(i + 1);   // ahead of its payload: block i + 1's row totals need no wait for it
             issue(i + 1);
+            if (i == nblk - 2) epi.add.fetch(item, item_m, M);
         }
         if (i == 0) {
             // X landed with block 0 (waited above)
@@ -1010,7 +1034,10 @@ __device__ __forceinline__ void bts_body(
         bt_v4i s = bt_v4i{0, 0, 0, 0};
         for (int w = 0; w < nwaves; ++w)
             s += *(bt_lds_v4i *)(uintptr_t)bt_lds_addr(part + ((i * nwaves + w) * NB + nb) * 256 + ln * 4);
-        bt_store_y4(Y, epi, M, n, m, s);
+        if (o == (int)threadIdx.x)
+            bt_store_item(Y, epi, item, M, n, m, s);
+        else
+            bt_store_y4(Y, epi, M, n, m, s);
     }
 }
 

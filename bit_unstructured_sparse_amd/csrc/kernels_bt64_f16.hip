@@ -480,6 +480,11 @@ __global__ __launch_bounds__(512) void k_bt8_f16(
     const uint32_t lut = bt_lds_addr(lut_lds);
     const __amdgpu_buffer_rsrc_t prs = bt_rsrc(payload, payload_bytes);
 
+    // this thread's first item (all steps summed at the end): what `add` needs
+    // for it is loaded with the last step
+    typename Add::template Item<1, 2> item;
+    const int item_n = (int)(threadIdx.x & 7), item_m = (s_begin + (int)(threadIdx.x >> 6)) * 8 + (int)((threadIdx.x >> 3) & 7);
+    if (!RING) add.open(item, item_n, item_n < N && item_m < M && (int)threadIdx.x < nstep * 64);
     // step boundaries (wave-uniform scalar loads), ahead of everything
     uint32_t eb[NSTEP + 1];
 #pragma unroll
@@ -553,7 +558,9 @@ __global__ __launch_bounds__(512) void k_bt8_f16(
         }
         Y[(int64_t)n * M + m] = __builtin_bit_cast(uint16_t, (_Float16)add.to(sum, n, m, M));
     };
+    if (!RING) add.opened(item);
     issue(0);
+    if (!RING && nstep == 1) add.fetch(item, item_m, M);
     bf_h8 xb[1][8];   // X of this lane's tile, loaded behind the first DMA (below)
     bt_v4i xg[1][8];  // the same in runs of the rows, before the transpose (XR: N > 4)
     constexpr bool x_runs = XR;
@@ -606,7 +613,9 @@ __global__ __launch_bounds__(512) void k_bt8_f16(
         }
         bt_wait_vm(0);   // this wavefront's share of step i landed (nothing later in flight)
         if (i + 1 < nstep) issue(i + 1);
+        if (!RING && i == nstep - 2) add.fetch(item, item_m, M);
         bt_barrier_lds();   // everyone's share, every half-row total of step i, step i - 1's partials
+        if (!RING && i == nstep - 1) add.reduce(item);
         if (RING && i > 0) write_step(i - 1);
 
         const BtRange g = bf_range(eb[i], eb[i + 1]);
@@ -654,7 +663,8 @@ __global__ __launch_bounds__(512) void k_bt8_f16(
                 sum += pw[l1];
                 sum += pw[l2];
             }
-            Y[(int64_t)n * M + m] = __builtin_bit_cast(uint16_t, (_Float16)add.to(sum, n, m, M));
+            sum = o == (int)threadIdx.x ? add.close(item, sum, m, M) : add.to(sum, n, m, M);
+            Y[(int64_t)n * M + m] = __builtin_bit_cast(uint16_t, (_Float16)sum);
         }
     }
 }
