@@ -872,15 +872,16 @@ class LoraAdapters:
             _flat(self.scale, "scale", torch.float32, n, index)
         if self.rank is not None:
             _flat(self.rank, "rank", torch.int32, n, index)
-        for name, value in (("adapters", n), ("R", R), ("K", K), ("M", int(self.B.shape[1])), ("_index", index)):
+        fixed = (n, R, _dptr(self.A), _dptr(self.B), _dptr(self.scale), _dptr(self.rank))
+        for name, value in (("adapters", n), ("R", R), ("K", K), ("M", int(self.B.shape[1])), ("_index", index),
+                            ("_fixed", fixed)):
             object.__setattr__(self, name, value)
 
     def _desc(self, W, index, N) -> _LoraDesc:
         import torch
         if self.K != W.K or self.M != W.M:
             raise ValueError(f"the adapters are for a {self.M} x {self.K} projection, not {W.M} x {W.K}")
-        return _LoraDesc(self.adapters, self.R, _dptr(self.A), _dptr(self.B), _dptr(self.scale), _dptr(self.rank),
-                         _flat(index, "index", torch.int32, N, self._index))
+        return _LoraDesc(*self._fixed, _flat(index, "index", torch.int32, N, self._index))
 
 
 def lora_workspace_bytes(dtype: int, M: int, K: int, N: int, rank: int, nnz: int = -1) -> int:
