@@ -760,6 +760,32 @@ def _stream_of(stream, index: int) -> int:
     return torch._C._cuda_getCurrentRawStream(index)
 
 
+def _new_output(shape, dtype, device, stream):
+    """A tensor for a call to write on `stream`. It is taken from that stream's
+    memory: a block of the current stream's may still be in use by what was
+    queued there. The current stream, where the caller will read it, is noted
+    for the time it is freed."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
+def _call_workspace(n: int, device, stream):
+    """A zero-filled workspace for one call on `stream`: cleared on that stream,
+    ahead of the call, and free for that stream's later work once dropped."""
+    import torch
+    if n == 0:
+        return None
+    if stream is None:
+        return torch.zeros(n, dtype=torch.uint8, device=device)
+    with torch.cuda.stream(stream):
+        return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
 def kv_append(cache: KVCache, K, V, slots, stream=None) -> None:
     """Quantise the rows K, V (float16 [n][kv_heads][head_dim], a token's heads
     contiguous) into cache slots (int64 [n], page * page_size + offset; a slot
@@ -781,8 +807,8 @@ def kv_gather(cache: KVCache, slots, K=None, V=None, stream=None):
     heads, dim, index = cache.kv_heads, cache.head_dim, cache._index
     n = slots.numel()
     at = _flat(slots, "slots", torch.int64, n, index)
-    K = torch.empty((n, heads, dim), dtype=torch.float16, device=cache.device) if K is None else K
-    V = torch.empty_like(K) if V is None else V
+    K = _new_output((n, heads, dim), torch.float16, cache.device, stream) if K is None else K
+    V = _new_output((n, heads, dim), torch.float16, cache.device, stream) if V is None else V
     ks, vs = _rows(K, "K", n, heads, dim, index), _rows(V, "V", n, heads, dim, index)
     rc = load_library().kv_cache_gather(cache._ref, at, n, K.data_ptr(), ks, V.data_ptr(), vs,
                                         _stream_of(stream, index))
@@ -801,7 +827,8 @@ def attention_workspace_bytes(cache: KVCache, B: int, max_q: int, q_heads: int, 
 
 
 def new_attention_workspace(cache: KVCache, B: int, max_q: int, q_heads: int, table_width: int, device="cuda"):
-    """A zero-filled workspace for attention_tree (None if none is used)."""
+    """A zero-filled workspace for attention_tree (None if none is used).
+    It is cleared on the current stream: calls on another one wait for that."""
     import torch
     n = attention_workspace_bytes(cache, B, max_q, q_heads, table_width)
     return torch.zeros(n, dtype=torch.uint8, device=device) if n else None
@@ -827,7 +854,7 @@ def attention_tree(Q, cache: KVCache, block_table, kv_lens, q_start, max_q: int,
     B, width = block_table.shape
     qs = _rows(Q, "Q", None, hq, dim, index)
     if O is None:
-        O = torch.empty((rows, hq, dim), dtype=torch.float16, device=cache.device)
+        O = _new_output((rows, hq, dim), torch.float16, cache.device, stream)
     os_ = _rows(O, "O", rows, hq, dim, index)
     wp, wb = _ws_args(workspace)
     i32 = torch.int32
@@ -891,17 +918,22 @@ def lora_workspace_bytes(dtype: int, M: int, K: int, N: int, rank: int, nnz: int
     return int(out.value)
 
 
+def _lora_bytes(W: DeviceMatrix, N: int, adapters: LoraAdapters) -> int:
+    return lora_workspace_bytes(W.dtype, W.M, W.K, N, adapters.R, W.nnz)
+
+
 def new_lora_workspace(W: DeviceMatrix, N: int, adapters: LoraAdapters, device="cuda"):
-    """A zero-filled workspace for the adapter entry points (None if empty)."""
+    """A zero-filled workspace for the adapter entry points (None if empty).
+    It is cleared on the current stream: calls on another one wait for that."""
     import torch
-    n = lora_workspace_bytes(W.dtype, W.M, W.K, N, adapters.R, W.nnz)
+    n = _lora_bytes(W, N, adapters)
     return torch.zeros(n, dtype=torch.uint8, device=device) if n else None
 
 
 def spmm_f16_lora(W: DeviceMatrix, X, adapters: LoraAdapters, index, Y=None, workspace=None, stream=None):
     """fp16 Y [N][M] = W x_n + scale[a] B_a (A_a x_n), a = index[n] (int32 [N];
     negative: no adapter). X: float16 [N][K]. workspace: new_lora_workspace(...)
-    (one is made for the call when not given)."""
+    (one is made for the call, on its stream, when not given)."""
     import torch
     if W.dtype != FP16:
         raise TypeError("spmm_f16_lora needs an fp16 DeviceMatrix")
@@ -911,10 +943,10 @@ def spmm_f16_lora(W: DeviceMatrix, X, adapters: LoraAdapters, index, Y=None, wor
     x = _flat(X, "X", torch.float16, N * W.K, dev)
     d = adapters._desc(W, index, N)
     if Y is None:
-        Y = torch.empty((N, W.M), dtype=torch.float16, device=X.device)
+        Y = _new_output((N, W.M), torch.float16, X.device, stream)
     y = _flat(Y, "Y", torch.float16, N * W.M, dev)
     if workspace is None:
-        workspace = new_lora_workspace(W, N, adapters, device=X.device)
+        workspace = _call_workspace(_lora_bytes(W, N, adapters), X.device, stream)
     wp, wb = _ws_args(workspace)
     rc = load_library().spmm_bitmap_f16_lora(
         _dptr(W.bitmaps), _dptr(W.offsets), _dptr(W.payload), W.payload.numel(), W.M, W.K, x, N, ctypes.byref(d), y,
@@ -940,10 +972,10 @@ def spmm_w4a4_dq_lora(W: DeviceMatrix, X, X16, scale_w, scale_x, adapters: LoraA
     sw, sx = _flat(scale_w, "scale_w", torch.float32, W.M, dev), _flat(scale_x, "scale_x", torch.float32, N, dev)
     d = adapters._desc(W, index, N)
     if Yh is None:
-        Yh = torch.empty((N, W.M), dtype=torch.float16, device=X16.device)
+        Yh = _new_output((N, W.M), torch.float16, X16.device, stream)
     y = _flat(Yh, "Yh", torch.float16, N * W.M, dev)
     if workspace is None:
-        workspace = new_lora_workspace(W, N, adapters, device=X16.device)
+        workspace = _call_workspace(_lora_bytes(W, N, adapters), X16.device, stream)
     wp, wb = _ws_args(workspace)
     rc = load_library().spmm_bitmap_w4a4_dq_lora(
         _dptr(W.bitmaps), _dptr(W.offsets), _dptr(W.payload), W.payload.numel(), W.M, W.K, x, x16, N, sw, sx,
