@@ -124,6 +124,7 @@ typedef _Float16 at_h2 __attribute__((ext_vector_type(2)));
 #define AT_WAVES 4
 #define AT_CUS 256
 #define AT_TILE 32                 // cached tokens per wavefront and step
+#define AT_AHEAD (32 * AT_WAVES * AT_TILE)   // tokens past the end that indexes may reach
 #define AT_BOOST 6.0f              // log2: the weights' scale, 2^6 at the running maximum
 #define AT_SLACK 8.0f              // log2: how far a score may pass the running maximum before it is moved
 // Query rows of a row block: 16 where a call has no more, else four wavefronts of 16 RT.
@@ -968,7 +969,9 @@ int at_check(const bsp_kv_cache *c, int64_t table_width, int64_t B, int64_t max_
     if (hq > 0 && (c->kv_heads == 0 || hq % c->kv_heads != 0)) return BSP_E_ARG;
     if (B > 65535 || hq > 65535) return BSP_E_OVERFLOW;
     if (hq > 0 && hq / c->kv_heads > 16384) return BSP_E_UNSUPPORTED;
-    if (table_width > INT32_MAX / c->page_size) return BSP_E_OVERFLOW;
+    // token indexes are 32 bits wide, and a wavefront looks pages up to 32 of its
+    // tiles ahead: 4 x 31 tiles and one more past the last token
+    if (table_width > (INT32_MAX - AT_AHEAD) / c->page_size) return BSP_E_OVERFLOW;
     return BSP_OK;
 }
 

@@ -559,6 +559,7 @@ int attention_tree_workspace_bytes(const bsp_kv_cache *cache, int64_t table_widt
  *   cache        HOST descriptor (read during the call only).
  *   block_table  DEVICE int32 [B][table_width]: page of tokens p * page_size ...
  *                of sequence b at [b][p]. Entries outside the cache are read as page 0.
+ *                table_width * page_size is below 2^31 - 4096 (BSP_E_OVERFLOW past that).
  *   kv_lens      DEVICE int32 [B], at most table_width * page_size (clamped to it).
  *   q_start      DEVICE int32 [B+1], non-decreasing, q_start[B] <= total_q. Rows
  *                of Q no sequence owns leave O as it is.
