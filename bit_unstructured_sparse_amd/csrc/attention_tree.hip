@@ -914,8 +914,11 @@ AtPlan at_plan(const bsp_kv_cache *c, int64_t table_width, int64_t B, int64_t ma
     p.min_per = 4 * AT_WAVES;
     const int64_t heads = c->kv_heads * p.row_blocks;
     const int64_t tiles = (table_width * c->page_size + AT_TILE - 1) / AT_TILE;      // of the longest sequence
-    // (all work in 32 bits: sequences may share pages, so B * tiles is not bounded by the cache)
-    if (split && B * heads <= AT_WS_COUNTERS && B * tiles <= INT32_MAX / 4 - B) {
+    // all work in 32 bits (sequences may share pages, so B * tiles is not bounded by
+    // the cache): up to 4 wavefronts side by side per tile, or for a sequence of
+    // none, and what rounding it up to whole chunks adds (at most 2 AT_CUS of them)
+    const int64_t most_work = 4 * B * std::max<int64_t>(1, tiles);
+    if (split && B * heads <= AT_WS_COUNTERS && most_work <= INT32_MAX - 2 * AT_CUS * p.min_per) {
         const int64_t want = std::max<int64_t>(1, (int64_t)AT_CUS * at_per_cu((int)D) / heads);
         const int64_t side = p.slot_rows <= 16 * p.rt ? 1 : p.slot_rows <= 32 * p.rt ? 2 : 4;
         const int64_t most = B * std::max<int64_t>(1, (tiles * side + p.min_per - 1) / p.min_per);

@@ -32,3 +32,20 @@ def test_tokens_a_table_can_hold(page):
     for width, status in ((most, bsp.OK), (most + 1, bsp.E_OVERFLOW), ((2 ** 31 - 1) // page, bsp.E_OVERFLOW)):
         assert attend(cache(page), width) == status
         assert workspace(cache(page), width, 1, 1, 1)[0] == status
+
+
+def test_work_of_all_sequences_fits_32_bits():
+    # 4 wavefronts side by side per tile of 32 tokens, and up to 512 chunks of
+    # which the last is rounded up: past that a call is not split
+    def work(width, B):
+        return 4 * B * -(-width * 16 // 32)
+
+    c = cache(16)
+    for B in (9, 33, 512):
+        most = (2 ** 31 - 1 - 512 * 16) // (4 * B) * 2
+        for width, split in ((most, True), (most + 2, False)):
+            assert (work(width, B) + 512 * 16 < 2 ** 31) == split
+            rc, n = workspace(c, width, B, 64, 8)
+            assert rc == bsp.OK and (n > 0) == split, (B, width, n)
+    # sizes of calls are far from it
+    assert workspace(c, 131072 // 16, 512, 64, 8)[1] > 0
