@@ -23,10 +23,14 @@
 // Numbers. Weights are scaled by 2^6 and the maximum is moved only when a score
 // passes it by 2^8, so they stay below 2^14 and are normal fp16 numbers down to
 // 2^-20 of the maximum; their 11 bits are the one rounding between the products,
-// independent from token to token. For quantised values the step enters the
-// weight relative to a common power of two, and the sum of the rounded weights
-// times the middle code is taken off again: what is rounded counts from the
-// middle of the codes, not from their end. Sums, maxima and normalisations are fp32.
+// independent from token to token. For quantised values weight times step is
+// what enters, and its maximum over the tokens a row sees is the running one (a
+// maximum of the scores, with one scale for the steps beside it, lets a single
+// large step, of a negligible weight or not seen at all, push the others' weights
+// below the normal numbers: 500 int8 tokens of size 1e-3 beside one unseen row of
+// 3e4 came out 2.8e-3 off in norm, against 3.3e-4). The sum of the rounded weights
+// times the middle code is taken off again: what is rounded counts from the middle
+// of the codes, not from their end. Sums, maxima and normalisations are fp32.
 //
 // What bounds it. With few query rows, the cache's bytes: 131072 tokens x 8 kv
 // heads, one token, fp16 103 us (5.2 TB/s; a copy reaches 4.7 counting both ways),
@@ -131,6 +135,10 @@ typedef _Float16 at_h2 __attribute__((ext_vector_type(2)));
 #define AT_ROWS(RT) ((RT) == 1 ? (D == 256 ? 64 : 16) : 64 * (RT))
 #define AT_LOW -1e30f              // stands for the maximum of no scores when sums are joined
 #define AT_NONE -3e38f             // `limit` of a row without a score yet
+// Bits of the least value step the maximum counts, 2^-40 (a row of equal
+// values has step 0; the least other step is 2^-24 / 255): weights relative to
+// a maximum with steps this small stay in range.
+#define AT_STEP_LOW 0x2B800000u
 
 // Workgroups per CU that the kernels are compiled for and the work is cut to
 // (their registers; a wavefront each per SIMD): one round, no workgroup waits
@@ -314,11 +322,11 @@ struct AtWave {
     const at_h8 *q_lds;
     float qc[RT];                  // sum of the row's q, times the score factor
     uint64_t seen[RT];
-    // the running maximum less AT_BOOST, and the sums of the weights 2^(x - mb)
+    // the running maximum less AT_BOOST (of scores, or of scores + log2(value
+    // step)), and the sums of the weights 2^(x - mb)
     float mb[RT], l[RT], osum[RT], psum[RT];
     float limit[RT];               // a score past it moves the maximum (AT_NONE: the row has none yet)
     at_f4 acc[RT][Sh::NT];
-    float sig, rsig;               // the value steps' common power of two, and 1 / it
     float c;                       // score factor: scale * log2(e)
     // the tile in flight
     uint32_t k[2][Sh::KW], v[8][Sh::VW], kw[8], vw[8];
@@ -479,50 +487,51 @@ struct AtWave {
                 for (int rt = 0; rt < RT; ++rt) l[rt] = (ok[rt] & odd) != 0u ? __builtin_nanf("") : l[rt];
             }
         }
-        // the largest value step (positive floats order as integers)
-        uint32_t smax = 0;
+        // Move the running maximum only when a score passes it by more than
+        // the slack (the weights stay fp16: 2^(6 + 8) at most). What enters the
+        // second product of a quantised cache is weight times step, so there
+        // the maximum is that of score + log2(step), over the tokens the row
+        // sees: a large step counts with its weight alone. The largest step of
+        // the lane's tokens and the largest score bound it from above.
+        float lg = 0.f;
         if constexpr (QUANT) {
+            uint32_t smax = AT_STEP_LOW;                   // (positive floats order as integers)
 #pragma unroll
             for (int e = 0; e < 8; ++e) smax = max(smax, vw[e]);
+            lg = __builtin_amdgcn_logf(__builtin_bit_cast(float, smax));
         }
-        // Move the running maximum only when a score passes it by more than
-        // the slack (the weights stay fp16: 2^(6 + 8) at most), and the value
-        // steps' scale when a step passes it.
-        bool move = QUANT && (smax & 0xFFFF0000u) > __builtin_bit_cast(uint32_t, sig);
+        bool move = false;
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt) move |= top[rt] > limit[rt];
+        for (int rt = 0; rt < RT; ++rt) move |= (QUANT ? top[rt] + lg : top[rt]) > limit[rt];
         float f[RT];
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) f[rt] = 1.f;
         const bool moved = __ballot(move) != 0;
         if (moved) {
-            float fs = 1.f;
             if constexpr (QUANT) {
-                // the largest finite step (an exponent below all ones borrows)
-                uint32_t big = 0;
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    big = max(big, vw[e] & (uint32_t)((int32_t)((vw[e] & 0x7F800000u) - 0x7F800000u) >> 31));
-                const float sm = fmaxf(at_group_max(kv_word_step(big)), sig);
-                const uint32_t b = (__builtin_bit_cast(uint32_t, sm) + 0x7FFFFFu) & 0x7F800000u;
-                fs = sig * __builtin_bit_cast(float, 0x7F000000u - b);
-                sig = __builtin_bit_cast(float, b);
-                rsig = __builtin_bit_cast(float, 0x7F000000u - b);
+                for (int rt = 0; rt < RT; ++rt) top[rt] = -INFINITY;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float le = __builtin_amdgcn_logf(kv_word_step(max(vw[e], AT_STEP_LOW)));
+#pragma unroll
+                    for (int rt = 0; rt < RT; ++rt) top[rt] = fmaxf(top[rt], x[rt][e >> 2][e & 3] + le);
+                }
             }
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt) {
-                // how far it moves: up only, but for the row's first scores
+                // how far it moves: up only, but for the row's first scores, and
+                // by what the row itself sees
                 const float most = at_group_max(top[rt]);
-                const bool first = limit[rt] == AT_NONE && most > AT_NONE;
-                const float up = first ? most - AT_BOOST : fmaxf(0.f, most - AT_BOOST);
-                const float g = first ? 1.f : __builtin_amdgcn_exp2f(-up);
-                limit[rt] = first ? AT_BOOST + AT_SLACK : limit[rt];
+                const bool over = most > limit[rt], first = limit[rt] == AT_NONE;
+                const float up = over ? most - AT_BOOST : 0.f;
+                const float g = over && !first ? __builtin_amdgcn_exp2f(-up) : 1.f;
+                limit[rt] = over ? AT_BOOST + AT_SLACK : limit[rt];
                 mb[rt] += up;
 #pragma unroll
                 for (int e = 0; e < 8; ++e) x[rt][e >> 2][e & 3] -= up;
-                l[rt] *= g, osum[rt] *= g;
-                f[rt] = g * fs;
-                psum[rt] *= f[rt];
+                l[rt] *= g, osum[rt] *= g, psum[rt] *= g;
+                f[rt] = g;
             }
         }
         __builtin_amdgcn_sched_barrier(0);
@@ -536,10 +545,10 @@ struct AtWave {
         const at_h2 one = {(_Float16)1.f, (_Float16)1.f};
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            float vs, vo;
+            float st, vo;
             if constexpr (QUANT) {
-                const float st = kv_word_step(vw[e]);
-                vs = st * rsig, vo = fmaf(KIND == BSP_INT8 ? 128.0f : 8.0f, st, kv_word_offset(vw[e]));
+                st = kv_word_step(vw[e]);
+                vo = fmaf(KIND == BSP_INT8 ? 128.0f : 8.0f, st, kv_word_offset(vw[e]));
             }
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt) {
@@ -547,7 +556,7 @@ struct AtWave {
                 if constexpr (QUANT) {
                     l[rt] += w;
                     osum[rt] = fmaf(w, vo, osum[rt]);
-                    w *= vs;
+                    w *= st;
                 }
                 p[rt][e] = (_Float16)w;          // nearest even: errors of 11 bits that average out over the tokens
             }
@@ -701,7 +710,6 @@ __global__ __launch_bounds__(64 * AT_WAVES, at_per_cu(D)) void k_at(const AtArgs
             w.load_k();
             w.load_v();
         }
-        w.sig = 0x1p-100f, w.rsig = 0x1p100f;
         if constexpr (Wave::Q_LDS) __syncthreads();      // the LDS area's last readers
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
@@ -792,7 +800,7 @@ __global__ __launch_bounds__(64 * AT_WAVES, at_per_cu(D)) void k_at(const AtArgs
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     float z = w.acc[rt][t + i][r];
-                    if constexpr (Wave::QUANT) z = fmaf(w.sig, fmaf(z, Sh::UNIT, -ps), os);
+                    if constexpr (Wave::QUANT) z = fmaf(z, Sh::UNIT, -ps) + os;
                     y[i] = z;
                 }
                 return y;

@@ -536,9 +536,10 @@ int kv_cache_gather(const bsp_kv_cache *cache, const int64_t *slots, int64_t n, 
  *   the cache at tokens a row does not see, NaN included, has no effect on it.
  *   A seen drafted token whose v row holds an infinity or a NaN makes the whole
  *   output row NaN.
- * Scores, softmax statistics and sums are fp32, the exponentials enter the
- * second product as fp16 (their scale chosen so that they stay normal numbers
- * down to 2^-20 of the largest), one rounding to fp16 at the end. Partial sums
+ * Scores, softmax statistics and sums are fp32, the exponentials (times the
+ * value row's step, where it is quantised) enter the second product as fp16
+ * (their scale chosen so that they stay normal numbers down to 2^-20 of the
+ * largest the row sees), one rounding to fp16 at the end. Partial sums
  * are joined in a fixed order: results do not depend on timing.
  * --------------------------------------------------------------------------- */
 
