@@ -305,6 +305,10 @@ __device__ __forceinline__ int at_uniform(int v) { return __builtin_amdgcn_readf
 // All ones where bit e of m is set, else zero.
 __device__ __forceinline__ uint32_t at_spread(uint32_t m, int e) { return (uint32_t)((int32_t)(m << (31 - e)) >> 31); }
 
+// 1 in each half of a dword of two fp16 numbers that is an infinity or a NaN:
+// an exponent of all ones carries into the bit above it.
+__device__ __forceinline__ uint32_t at_odd(uint32_t h) { return (((h & 0x7C007C00u) + 0x04000400u) >> 15) & 0x00010001u; }
+
 // One wavefront's share: 16 RT query rows, every wt_n-th tile.
 template <int KIND, int D, int RT>
 struct AtWave {
@@ -396,6 +400,43 @@ struct AtWave {
         return (m << b) | ((1u << b) - 1u);
     }
 
+    // Values that are not finite: how many infinities (a NaN is one of each
+    // sign) a row sees per channel is a product of ones; they are added to the
+    // sums, and taken out of v.
+    __device__ __forceinline__ void add_odd(const uint32_t (&ok)[RT]) {
+#pragma unroll
+        for (int t = 0; t < Sh::NT; ++t) {
+            const at_u4 f = __builtin_bit_cast(at_u4, at_v_frag<KIND>(v, t));
+            at_u4 pos, neg;
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+                const uint32_t nf = at_odd(f[p]), sign = f[p] >> 15;
+                const uint32_t nan = ((f[p] & 0x03FF03FFu) + 0x03FF03FFu) >> 10;
+                pos[p] = (nf & (~sign | nan)) * 0x3C00u, neg[p] = (nf & (sign | nan)) * 0x3C00u;
+            }
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {
+                at_u4 see;
+#pragma unroll
+                for (int p = 0; p < 4; ++p)
+                    see[p] = ((at_spread(ok[rt], 2 * p) & 0xFFFFu) | (at_spread(ok[rt], 2 * p + 1) << 16)) & 0x3C003C00u;
+                const at_f4 none = {0.f, 0.f, 0.f, 0.f};
+                const at_h8 b = __builtin_bit_cast(at_h8, see);
+                const at_f4 up = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(at_h8, pos), b, none, 0, 0, 0);
+                const at_f4 dn = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(at_h8, neg), b, none, 0, 0, 0);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    acc[rt][t][i] += up[i] > 0.f ? INFINITY : 0.f;
+                    acc[rt][t][i] -= dn[i] > 0.f ? INFINITY : 0.f;
+                }
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+#pragma unroll
+            for (int i = 0; i < Sh::VW; ++i) v[e][i] &= ~(at_odd(v[e][i]) * 0xFFFFu);
+    }
+
     // One tile: scores, running maximum, weights, output. The next tile's loads
     // (base0, base1: set_tile) are issued as the registers they fill fall free.
     __device__ __forceinline__ void tile(int j0) {
@@ -438,10 +479,11 @@ struct AtWave {
         if (j0 + AT_TILE > past) {
             // Drafted tokens or the end of the sequence: what a row does not
             // see scores -inf; rows past the end hold anything, NaN too, and
-            // count as zeros. A value row (or its word) that is not finite
-            // counts as zero too, and makes the query rows that see it NaN.
-            // (Masks are spread over registers: comparisons would hold 16
-            // pairs of scalar registers at a time.)
+            // count as zeros. A value that is not finite counts as zero in the
+            // product, where a weight of zero would not keep it out, and is
+            // added for the query rows that see it; a quantised row whose word
+            // is not finite makes them NaN. (Masks are spread over registers:
+            // comparisons would hold 16 pairs of scalar registers at a time.)
             const int n = min(max(len - (j0 + 8 * grp), 0), 8);     // tokens there are
             const uint32_t in = (1u << n) - 1u;
             uint32_t ok[RT];
@@ -458,7 +500,7 @@ struct AtWave {
                     top[rt] = fmaxf(top[rt], z);
                 }
             }
-            uint32_t odd = 0;              // bit e: token e's row is not finite
+            uint32_t odd = 0;              // quantised: bit e: token e's word is not finite; else any value of the lane's
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const uint32_t m = at_spread(in, e);
@@ -472,19 +514,19 @@ struct AtWave {
                     uint32_t any = 0;
 #pragma unroll
                     for (int i = 0; i < Sh::VW; ++i) {
-                        const uint32_t h = v[e][i] & m, nf = (((h & 0x7C007C00u) + 0x04000400u) >> 15) & 0x00010001u;
-                        v[e][i] = h & ~(nf * 0xFFFFu);
-                        any |= nf;
+                        v[e][i] &= m;
+                        any |= at_odd(v[e][i]);
                     }
-                    odd |= any != 0u ? 1u << e : 0u;
+                    odd |= any;
                 }
             }
             if (__ballot(odd != 0) != 0) {
-                // a row's 16 lanes hold pieces of it
+                if constexpr (QUANT) {
 #pragma unroll
-                for (int d = 1; d < 16; d <<= 1) odd |= (uint32_t)__shfl_xor((int)odd, d, 64);
-#pragma unroll
-                for (int rt = 0; rt < RT; ++rt) l[rt] = (ok[rt] & odd) != 0u ? __builtin_nanf("") : l[rt];
+                    for (int rt = 0; rt < RT; ++rt) l[rt] = (ok[rt] & odd) != 0u ? __builtin_nanf("") : l[rt];
+                } else {
+                    add_odd(ok);
+                }
             }
         }
         // Move the running maximum only when a score passes it by more than

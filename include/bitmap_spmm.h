@@ -534,8 +534,9 @@ int kv_cache_gather(const bsp_kv_cache *cache, const int64_t *slots, int64_t n, 
  *   tokens j, k_j and v_j the rows of kv head h / (q_heads / kv_heads) as the
  *   cache stands for them. A row that sees no token gives zeros. What lies in
  *   the cache at tokens a row does not see, NaN included, has no effect on it.
- *   A seen drafted token whose v row holds an infinity or a NaN makes the whole
- *   output row NaN.
+ *   An infinity or a NaN in a v row that a row sees makes that channel of its
+ *   output infinite or NaN (a quantised row that held one stands for NaN in
+ *   every channel), one in a k row makes scores, and all of its output, so.
  * Scores, softmax statistics and sums are fp32, the exponentials (times the
  * value row's step, where it is quantised) enter the second product as fp16
  * (their scale chosen so that they stay normal numbers down to 2^-20 of the
