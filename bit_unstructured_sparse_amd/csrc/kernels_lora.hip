@@ -46,7 +46,7 @@ typedef _Float16 lora_h8 __attribute__((ext_vector_type(8)));
 typedef float lora_f4 __attribute__((ext_vector_type(4)));
 
 // s[k] + B_a[m + k] t_n, 8 rank positions a load; what lies past the rank (any
-// bits) is replaced by zero. Index, rank and rows are loads one after the other
+// bits of B, and t read again where a piece repeats) is left out. Index, rank and rows are loads one after the other
 // that the tail of a sparse kernel has too few wavefronts to hide. Where
 // registers allow it (N <= 8, and int4) a thread's first item is therefore taken
 // in steps beside the kernel's own: its index with the first loads (open), its
@@ -95,8 +95,10 @@ struct LoraAdd {
             for (int j = 0; j < 8; ++j) {
                 const bool in = r0 + 8 * p + j < e.rank;
 #pragma unroll
-                for (int k = 0; k < ROWS; ++k)
-                    e.u[k] = fmaf(in ? (float)e.b[p][k][j] : 0.f, e.v[p][j >> 2][j & 3], e.u[k]);
+                for (int k = 0; k < ROWS; ++k) {
+                    const float u = fmaf((float)e.b[p][k][j], e.v[p][j >> 2][j & 3], e.u[k]);
+                    e.u[k] = in ? u : e.u[k];
+                }
             }
     }
     // (the first positions are there whatever the rank: R is at least 8; past R the first again)
