@@ -285,12 +285,14 @@ def _check_dev(t, name, dtype, numel=None):
         raise ValueError(f"{name} has {t.numel()} elements, expected {numel}")
 
 
-def _ws_args(workspace):
+def _ws_args(workspace, index=None):
     if workspace is None:
         return None, 0
     import torch
     if not isinstance(workspace, torch.Tensor) or not workspace.is_cuda or not workspace.is_contiguous():
         raise TypeError("workspace must be a contiguous CUDA (HIP) tensor")
+    if index is not None and workspace.get_device() != index:
+        raise ValueError(f"workspace must be on device {index}")
     return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
@@ -755,9 +757,27 @@ def _stream_of(stream, index: int) -> int:
     """The handle of a stream, by default the device's current one (its
     handle alone: the Stream object around it costs as much as a launch)."""
     if stream is not None:
+        if stream.device_index != index:
+            raise ValueError(f"the stream must be one of device {index}")
         return stream.cuda_stream
     import torch
     return torch._C._cuda_getCurrentRawStream(index)
+
+
+def _launch(fn, index: int, *args) -> int:
+    """Calls an entry point with the tensors' device as the current one: kernels
+    go to the current device, and its default stream has the same handle as
+    every other device's."""
+    import torch
+    if torch._C._cuda_getDevice() == index:
+        return fn(*args)
+    with torch.cuda.device(index):
+        return fn(*args)
+
+
+def _weights_on(W: DeviceMatrix, index: int) -> None:
+    if not W.bitmaps.get_device() == W.offsets.get_device() == W.payload.get_device() == index:
+        raise ValueError(f"the projection must be on device {index}")
 
 
 def _new_output(shape, dtype, device, stream):
@@ -795,8 +815,8 @@ def kv_append(cache: KVCache, K, V, slots, stream=None) -> None:
     ks = _rows(K, "K", None, heads, dim, index)
     n = K.shape[0]
     vs = _rows(V, "V", n, heads, dim, index)
-    rc = load_library().kv_cache_append(cache._ref, K.data_ptr(), ks, V.data_ptr(), vs,
-                                        _flat(slots, "slots", torch.int64, n, index), n, _stream_of(stream, index))
+    rc = _launch(load_library().kv_cache_append, index, cache._ref, K.data_ptr(), ks, V.data_ptr(), vs,
+                 _flat(slots, "slots", torch.int64, n, index), n, _stream_of(stream, index))
     _check(rc, "kv_cache_append")
 
 
@@ -810,8 +830,8 @@ def kv_gather(cache: KVCache, slots, K=None, V=None, stream=None):
     K = _new_output((n, heads, dim), torch.float16, cache.device, stream) if K is None else K
     V = _new_output((n, heads, dim), torch.float16, cache.device, stream) if V is None else V
     ks, vs = _rows(K, "K", n, heads, dim, index), _rows(V, "V", n, heads, dim, index)
-    rc = load_library().kv_cache_gather(cache._ref, at, n, K.data_ptr(), ks, V.data_ptr(), vs,
-                                        _stream_of(stream, index))
+    rc = _launch(load_library().kv_cache_gather, index, cache._ref, at, n, K.data_ptr(), ks, V.data_ptr(), vs,
+                 _stream_of(stream, index))
     _check(rc, "kv_cache_gather")
     return K, V
 
@@ -856,9 +876,10 @@ def attention_tree(Q, cache: KVCache, block_table, kv_lens, q_start, max_q: int,
     if O is None:
         O = _new_output((rows, hq, dim), torch.float16, cache.device, stream)
     os_ = _rows(O, "O", rows, hq, dim, index)
-    wp, wb = _ws_args(workspace)
+    wp, wb = _ws_args(workspace, index)
     i32 = torch.int32
-    rc = load_library().attention_tree_f16(
+    rc = _launch(
+        load_library().attention_tree_f16, index,
         Q.data_ptr(), qs, cache._ref, _flat(block_table, "block_table", i32, B * width, index), width,
         _flat(kv_lens, "kv_lens", i32, B, index), _flat(q_start, "q_start", i32, B + 1, index), B, rows, max_q, hq,
         None if tree_mask is None else _flat(tree_mask, "tree_mask", torch.int64, rows, index),
@@ -940,6 +961,7 @@ def spmm_f16_lora(W: DeviceMatrix, X, adapters: LoraAdapters, index, Y=None, wor
     if X.dim() != 2 or X.shape[1] != W.K:
         raise ValueError("X must be [N][K]")
     N, dev = X.shape[0], adapters._index
+    _weights_on(W, dev)
     x = _flat(X, "X", torch.float16, N * W.K, dev)
     d = adapters._desc(W, index, N)
     if Y is None:
@@ -947,8 +969,9 @@ def spmm_f16_lora(W: DeviceMatrix, X, adapters: LoraAdapters, index, Y=None, wor
     y = _flat(Y, "Y", torch.float16, N * W.M, dev)
     if workspace is None:
         workspace = _call_workspace(_lora_bytes(W, N, adapters), X.device, stream)
-    wp, wb = _ws_args(workspace)
-    rc = load_library().spmm_bitmap_f16_lora(
+    wp, wb = _ws_args(workspace, dev)
+    rc = _launch(
+        load_library().spmm_bitmap_f16_lora, dev,
         _dptr(W.bitmaps), _dptr(W.offsets), _dptr(W.payload), W.payload.numel(), W.M, W.K, x, N, ctypes.byref(d), y,
         wp, wb, _stream_of(stream, dev))
     _check(rc, "spmm_bitmap_f16_lora")
@@ -967,6 +990,7 @@ def spmm_w4a4_dq_lora(W: DeviceMatrix, X, X16, scale_w, scale_x, adapters: LoraA
     if X16.dim() != 2 or X16.shape[1] != W.K:
         raise ValueError("X16 must be [N][K]")
     N, dev = X16.shape[0], adapters._index
+    _weights_on(W, dev)
     x16 = _flat(X16, "X16", torch.float16, N * W.K, dev)
     x = _flat(X, "X", torch.uint8, N * ((W.K + 1) // 2), dev)
     sw, sx = _flat(scale_w, "scale_w", torch.float32, W.M, dev), _flat(scale_x, "scale_x", torch.float32, N, dev)
@@ -976,8 +1000,9 @@ def spmm_w4a4_dq_lora(W: DeviceMatrix, X, X16, scale_w, scale_x, adapters: LoraA
     y = _flat(Yh, "Yh", torch.float16, N * W.M, dev)
     if workspace is None:
         workspace = _call_workspace(_lora_bytes(W, N, adapters), X16.device, stream)
-    wp, wb = _ws_args(workspace)
-    rc = load_library().spmm_bitmap_w4a4_dq_lora(
+    wp, wb = _ws_args(workspace, dev)
+    rc = _launch(
+        load_library().spmm_bitmap_w4a4_dq_lora, dev,
         _dptr(W.bitmaps), _dptr(W.offsets), _dptr(W.payload), W.payload.numel(), W.M, W.K, x, x16, N, sw, sx,
         ctypes.byref(d), y, wp, wb, _stream_of(stream, dev))
     _check(rc, "spmm_bitmap_w4a4_dq_lora")
