@@ -753,26 +753,22 @@ def _flat(t, name, dtype, numel, index) -> int:
     raise ValueError(f"{name} must be on device {index}")
 
 
-def _stream_of(stream, index: int) -> int:
-    """The handle of a stream, by default the device's current one (its
-    handle alone: the Stream object around it costs as much as a launch)."""
-    if stream is not None:
-        if stream.device_index != index:
-            raise ValueError(f"the stream must be one of device {index}")
-        return stream.cuda_stream
+def _launch(fn, index: int, stream, *args) -> int:
+    """Calls an entry point on a stream, by default the device's current one (by
+    its handle alone: the Stream object around it costs as much as a launch),
+    with the tensors' device as the current one: kernels go to the current
+    device, and its default stream has the same handle as every other device's."""
     import torch
-    return torch._C._cuda_getCurrentRawStream(index)
-
-
-def _launch(fn, index: int, *args) -> int:
-    """Calls an entry point with the tensors' device as the current one: kernels
-    go to the current device, and its default stream has the same handle as
-    every other device's."""
-    import torch
+    if stream is None:
+        handle = torch._C._cuda_getCurrentRawStream(index)
+    elif stream.device_index == index:
+        handle = stream.cuda_stream
+    else:
+        raise ValueError(f"the stream must be one of device {index}")
     if torch._C._cuda_getDevice() == index:
-        return fn(*args)
+        return fn(*args, handle)
     with torch.cuda.device(index):
-        return fn(*args)
+        return fn(*args, handle)
 
 
 def _weights_on(W: DeviceMatrix, index: int) -> None:
@@ -815,8 +811,8 @@ def kv_append(cache: KVCache, K, V, slots, stream=None) -> None:
     ks = _rows(K, "K", None, heads, dim, index)
     n = K.shape[0]
     vs = _rows(V, "V", n, heads, dim, index)
-    rc = _launch(load_library().kv_cache_append, index, cache._ref, K.data_ptr(), ks, V.data_ptr(), vs,
-                 _flat(slots, "slots", torch.int64, n, index), n, _stream_of(stream, index))
+    rc = _launch(load_library().kv_cache_append, index, stream, cache._ref, K.data_ptr(), ks, V.data_ptr(), vs,
+                 _flat(slots, "slots", torch.int64, n, index), n)
     _check(rc, "kv_cache_append")
 
 
@@ -830,8 +826,7 @@ def kv_gather(cache: KVCache, slots, K=None, V=None, stream=None):
     K = _new_output((n, heads, dim), torch.float16, cache.device, stream) if K is None else K
     V = _new_output((n, heads, dim), torch.float16, cache.device, stream) if V is None else V
     ks, vs = _rows(K, "K", n, heads, dim, index), _rows(V, "V", n, heads, dim, index)
-    rc = _launch(load_library().kv_cache_gather, index, cache._ref, at, n, K.data_ptr(), ks, V.data_ptr(), vs,
-                 _stream_of(stream, index))
+    rc = _launch(load_library().kv_cache_gather, index, stream, cache._ref, at, n, K.data_ptr(), ks, V.data_ptr(), vs)
     _check(rc, "kv_cache_gather")
     return K, V
 
@@ -879,11 +874,11 @@ def attention_tree(Q, cache: KVCache, block_table, kv_lens, q_start, max_q: int,
     wp, wb = _ws_args(workspace, index)
     i32 = torch.int32
     rc = _launch(
-        load_library().attention_tree_f16, index,
+        load_library().attention_tree_f16, index, stream,
         Q.data_ptr(), qs, cache._ref, _flat(block_table, "block_table", i32, B * width, index), width,
         _flat(kv_lens, "kv_lens", i32, B, index), _flat(q_start, "q_start", i32, B + 1, index), B, rows, max_q, hq,
         None if tree_mask is None else _flat(tree_mask, "tree_mask", torch.int64, rows, index),
-        dim ** -0.5 if scale is None else scale, O.data_ptr(), os_, wp, wb, _stream_of(stream, index))
+        dim ** -0.5 if scale is None else scale, O.data_ptr(), os_, wp, wb)
     _check(rc, "attention_tree_f16")
     return O
 
@@ -971,9 +966,9 @@ def spmm_f16_lora(W: DeviceMatrix, X, adapters: LoraAdapters, index, Y=None, wor
         workspace = _call_workspace(_lora_bytes(W, N, adapters), X.device, stream)
     wp, wb = _ws_args(workspace, dev)
     rc = _launch(
-        load_library().spmm_bitmap_f16_lora, dev,
+        load_library().spmm_bitmap_f16_lora, dev, stream,
         _dptr(W.bitmaps), _dptr(W.offsets), _dptr(W.payload), W.payload.numel(), W.M, W.K, x, N, ctypes.byref(d), y,
-        wp, wb, _stream_of(stream, dev))
+        wp, wb)
     _check(rc, "spmm_bitmap_f16_lora")
     return Y
 
@@ -1002,8 +997,8 @@ def spmm_w4a4_dq_lora(W: DeviceMatrix, X, X16, scale_w, scale_x, adapters: LoraA
         workspace = _call_workspace(_lora_bytes(W, N, adapters), X16.device, stream)
     wp, wb = _ws_args(workspace, dev)
     rc = _launch(
-        load_library().spmm_bitmap_w4a4_dq_lora, dev,
+        load_library().spmm_bitmap_w4a4_dq_lora, dev, stream,
         _dptr(W.bitmaps), _dptr(W.offsets), _dptr(W.payload), W.payload.numel(), W.M, W.K, x, x16, N, sw, sx,
-        ctypes.byref(d), y, wp, wb, _stream_of(stream, dev))
+        ctypes.byref(d), y, wp, wb)
     _check(rc, "spmm_bitmap_w4a4_dq_lora")
     return Yh
