@@ -896,7 +896,8 @@ class _LoraDesc(ctypes.Structure):
 class LoraAdapters:
     """The adapters of one projection: A float16 [adapters][R][K], B float16
     [adapters][M][R] (R a multiple of 8, at most 256); scale float32 [adapters]
-    (None: 1); rank int32 [adapters], the rows of A in use (None: R)."""
+    (None: 1); rank int32 [adapters], the rows of A in use (None: R). A tensor
+    given another storage is taken up, and checked, by the next call."""
     A: "object"
     B: "object"
     scale: "object" = None
@@ -922,6 +923,8 @@ class LoraAdapters:
 
     def _desc(self, W, index, N) -> _LoraDesc:
         import torch
+        if (self.A.data_ptr(), self.B.data_ptr(), _dptr(self.scale), _dptr(self.rank)) != self._fixed[2:]:
+            self.__post_init__()
         if self.K != W.K or self.M != W.M:
             raise ValueError(f"the adapters are for a {self.M} x {self.K} projection, not {W.M} x {W.K}")
         return _LoraDesc(*self._fixed, _flat(index, "index", torch.int32, N, self._index))
