@@ -417,14 +417,20 @@ extern "C" int bsp_workspace_bytes(int dtype, int64_t M, int64_t K, int64_t N, i
     if (M < 0 || K < 0 || N < 0 || N > BSP_MAX_N || bytes == nullptr) return BSP_E_ARG;
     if (K >= BSP_MAX_K || M > INT32_MAX || M * ((K + 63) / 64) >= INT32_MAX) return BSP_E_OVERFLOW;
     const Shape s{M, K, N, (K + 63) / 64, M * ((K + 63) / 64)};
-    const int64_t nz = nnz >= 0 ? nnz : M * K;
-    Plan p;
-    choose_plan(dtype, s, dtype == BSP_INT4 ? (nz + 1) / 2 : 2 * nz, BSP_ALGO_AUTO, true, &p);
-    // the forced split-K plan may want more than the automatic one
-    Plan q;
-    int64_t need = p.ws_bytes();
-    if (choose_plan(dtype, s, dtype == BSP_INT4 ? (nz + 1) / 2 : 2 * nz, BSP_ALGO_SPLITK, true, &q) == BSP_OK)
-        need = std::max(need, q.ws_bytes());
+    // An unknown nnz: the most of a dense and of an empty W. A split plan's
+    // need depends on the payload only by the blocks of its sets (the last set
+    // is rounded up to them), and those by whether a slot holds one KB or two,
+    // or none fits: an empty W has the first, a dense one the last of these its
+    // shape can come to.
+    int64_t need = 0;
+    for (const int64_t nz : {nnz >= 0 ? nnz : M * K, nnz >= 0 ? nnz : 0}) {
+        const int64_t pbytes = dtype == BSP_INT4 ? (nz + 1) / 2 : 2 * nz;
+        // the forced split-K plan may want more than the automatic one
+        for (const int algo : {BSP_ALGO_AUTO, BSP_ALGO_SPLITK}) {
+            Plan p;
+            if (choose_plan(dtype, s, pbytes, algo, true, &p) == BSP_OK) need = std::max(need, p.ws_bytes());
+        }
+    }
     *bytes = need;
     return BSP_OK;
 }
