@@ -823,8 +823,10 @@ def kv_gather(cache: KVCache, slots, K=None, V=None, stream=None):
     heads, dim, index = cache.kv_heads, cache.head_dim, cache._index
     n = slots.numel()
     at = _flat(slots, "slots", torch.int64, n, index)
-    K = _new_output((n, heads, dim), torch.float16, cache.device, stream) if K is None else K
-    V = _new_output((n, heads, dim), torch.float16, cache.device, stream) if V is None else V
+    if K is None:
+        K = _new_output((n, heads, dim), torch.float16, cache.device, stream)
+    if V is None:
+        V = torch.empty_like(K) if stream is None else _new_output((n, heads, dim), torch.float16, cache.device, stream)
     ks, vs = _rows(K, "K", n, heads, dim, index), _rows(V, "V", n, heads, dim, index)
     rc = _launch(load_library().kv_cache_gather, index, stream, cache._ref, at, n, K.data_ptr(), ks, V.data_ptr(), vs)
     _check(rc, "kv_cache_gather")
@@ -916,14 +918,16 @@ class LoraAdapters:
             _flat(self.scale, "scale", torch.float32, n, index)
         if self.rank is not None:
             _flat(self.rank, "rank", torch.int32, n, index)
-        fixed = (n, R, _dptr(self.A), _dptr(self.B), _dptr(self.scale), _dptr(self.rank))
+        at = (_dptr(self.A), _dptr(self.B), _dptr(self.scale), _dptr(self.rank))
         for name, value in (("adapters", n), ("R", R), ("K", K), ("M", int(self.B.shape[1])), ("_index", index),
-                            ("_fixed", fixed)):
+                            ("_at", at), ("_fixed", (n, R) + at)):
             object.__setattr__(self, name, value)
 
     def _desc(self, W, index, N) -> _LoraDesc:
         import torch
-        if (self.A.data_ptr(), self.B.data_ptr(), _dptr(self.scale), _dptr(self.rank)) != self._fixed[2:]:
+        scale, rank = self.scale, self.rank
+        if (self.A.data_ptr(), self.B.data_ptr(), None if scale is None else scale.data_ptr(),
+                None if rank is None else rank.data_ptr()) != self._at:
             self.__post_init__()
         if self.K != W.K or self.M != W.M:
             raise ValueError(f"the adapters are for a {self.M} x {self.K} projection, not {W.M} x {W.K}")
@@ -970,8 +974,8 @@ def spmm_f16_lora(W: DeviceMatrix, X, adapters: LoraAdapters, index, Y=None, wor
     wp, wb = _ws_args(workspace, dev)
     rc = _launch(
         load_library().spmm_bitmap_f16_lora, dev, stream,
-        _dptr(W.bitmaps), _dptr(W.offsets), _dptr(W.payload), W.payload.numel(), W.M, W.K, x, N, ctypes.byref(d), y,
-        wp, wb)
+        W.bitmaps.data_ptr(), W.offsets.data_ptr(), W.payload.data_ptr(), W.payload.numel(), W.M, W.K, x, N,
+        ctypes.byref(d), y, wp, wb)
     _check(rc, "spmm_bitmap_f16_lora")
     return Y
 
@@ -1001,7 +1005,7 @@ def spmm_w4a4_dq_lora(W: DeviceMatrix, X, X16, scale_w, scale_x, adapters: LoraA
     wp, wb = _ws_args(workspace, dev)
     rc = _launch(
         load_library().spmm_bitmap_w4a4_dq_lora, dev, stream,
-        _dptr(W.bitmaps), _dptr(W.offsets), _dptr(W.payload), W.payload.numel(), W.M, W.K, x, x16, N, sw, sx,
+        W.bitmaps.data_ptr(), W.offsets.data_ptr(), W.payload.data_ptr(), W.payload.numel(), W.M, W.K, x, x16, N, sw, sx,
         ctypes.byref(d), y, wp, wb)
     _check(rc, "spmm_bitmap_w4a4_dq_lora")
     return Yh
