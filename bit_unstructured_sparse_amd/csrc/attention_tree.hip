@@ -33,26 +33,26 @@
 // of the codes, not from their end. Sums, maxima and normalisations are fp32.
 //
 // What bounds it. With few query rows, the cache's bytes: 131072 tokens x 8 kv
-// heads, one token, fp16 103 us (5.2 TB/s; a copy reaches 4.7 counting both ways),
-// int8 63 (4.4 TB/s), int4 41 (3.5 TB/s). Past 32 query rows per kv head the vector
-// unit: per 32 tokens and 32 rows about 300 VALU instructions (half of them the
-// decoding of codes, masks and addresses, done by each wavefront of the rows)
-// beside 32 MFMAs; 65536 int8 tokens, 128 rows, 89 us (384 TFLOP/s; counters:
-// vector unit 51 % busy, matrix cores 18 %; with every load of the cache left out,
-// 82 us; partial sums, their joining and the start take about 15 of them). Short
-// calls are bound by latency: launch, lengths, block table, first tile, join,
-// about 6 us for 16 tokens.
+// heads, one token, on caches not used before, fp16 105 us (5.1 TB/s; a copy
+// reaches 5.3 counting both ways), int8 63 (4.4 TB/s), int4 40 (3.5 TB/s). Past 32
+// query rows per kv head instructions and their latency, at two wavefronts per
+// SIMD: per 32 tokens and 32 rows 321 VALU instructions (half of them the decoding
+// of codes, masks and addresses, done by each wavefront of the rows) beside 32
+// MFMAs; 65536 int8 tokens, 128 rows, 83 us (414 TFLOP/s; counters: vector unit
+// about half of the time busy, matrix cores 18 %, so a good part of it neither;
+// partial sums, their joining and the start take about 15 us). Short calls are bound by
+// latency: launch, lengths, block table, first tile, join, about 6 us for 16 tokens.
 //
 // Taken and dropped, measured at the same sizes: 4 row tiles per wavefront (one
 // wavefront per SIMD: trees of 16 at 8192 tokens 169 us against 112), the last
 // workgroup of a sequence joining all parts of 64 rows (218 us against 128 with a
 // kernel of its own), masks as comparisons (16 pairs of scalar registers in
 // flight, spilled), rows written from registers without LDS (16-byte pieces at
-// 512-byte strides: trees 87 us against 63), quantised tiles moved to LDS by DMA and
-// shared by the wavefronts side by side (trees 61.5 us against 62.7, but a batch of
+// 512-byte strides: trees 87 us against 63), tiles of codes moved to LDS by DMA and
+// read there by the wavefronts side by side, each of which still decodes them (trees 61.5 us against 62.7, but a batch of
 // 32 31.5 against 30.0 and trees of 61 42.8 against 40.0; the same with one tile's
-// output beside the next one's scores 61.9, 35.5 and 44.3), workgroups of 8
-// wavefronts for 32 rows each (half the partial sums: 131072 fp16 tokens 119 us
+// output beside the next one's scores 61.9, 35.5 and 44.3; decoding a tile once for
+// all of them has not been built), workgroups of 8 wavefronts for 32 rows each (half the partial sums: 131072 fp16 tokens 119 us
 // against 124, but 4 x 2000 30 against 25).
 #include <hip/hip_runtime.h>
 

@@ -54,7 +54,8 @@ typedef float lora_f4 __attribute__((ext_vector_type(4)));
 // that payload has landed (reduce), the rest in the final write (close): fp16
 // 4096 x 4096, N = 1, rank 8 11.3 us against 11.9, int4 12288 x 4096, N = 8, rank
 // 16 12.9 against 13.2. (The 1024-thread kernels have 128 registers and spill it:
-// fp16 N = 32 29.9 against 24.7; they take all of it at the end.)
+// fp16 N = 32 29.9 against 24.7. They take all of it at the end, where the one for
+// two column blocks still spills 22 registers, with its plain form at 126.)
 struct LoraAdd {
     LoraArgs a;
 
@@ -200,8 +201,10 @@ __global__ __launch_bounds__(64 * LORA_WAVES) void k_lora_down(const LoraArgs a,
     }
 }
 
-// The dequantised int32 sums with the adapters' part, rounded once (for the
-// int4 kernels whose final write does not do it: K past 4096).
+// The dequantised int32 sums with the adapters' part, rounded once (for every
+// int4 plan but the streaming one: K past 4096, more than three 16-row blocks per
+// workgroup, an X off a 4-byte boundary; 16384 x 2048, N = 8, rank 16 14.5 us for
+// its three kernels).
 __global__ __launch_bounds__(256) void k_lora_dq(const LoraAdd add, const int32_t *__restrict__ Y32, int M,
                                                  const float *__restrict__ sw, const float *__restrict__ sx,
                                                  uint16_t *__restrict__ Yh) {

@@ -536,7 +536,7 @@ int kv_cache_gather(const bsp_kv_cache *cache, const int64_t *slots, int64_t n, 
  *   the cache at tokens a row does not see, NaN included, has no effect on it.
  *   An infinity or a NaN in a v row that a row sees makes that channel of its
  *   output infinite or NaN (a quantised row that held one stands for NaN in
- *   every channel), one in a k row makes scores, and all of its output, so.
+ *   every channel), one in a k row the score of that token.
  * Scores, softmax statistics and sums are fp32, the exponentials (times the
  * value row's step, where it is quantised) enter the second product as fp16
  * (their scale chosen so that they stay normal numbers down to 2^-20 of the
