@@ -17,7 +17,7 @@ from __future__ import annotations
 import ctypes
 import os
 from dataclasses import dataclass
-from typing import Optional
+from typing import NamedTuple, Optional
 
 import numpy as np
 
@@ -26,13 +26,16 @@ __all__ = ["load_library", "encode", "pack_int4", "Encoded", "DeviceMatrix", "sp
            "ALGO_SPLITK",
            "INT4", "FP16", "INT8", "PAYLOAD_ALIGN", "MAX_N", "library_path", "KVCache", "new_kv_cache", "kv_append",
            "kv_gather", "attention_tree", "attention_workspace_bytes", "new_attention_workspace", "LoraAdapters",
-           "spmm_f16_lora", "spmm_w4a4_dq_lora", "lora_workspace_bytes", "new_lora_workspace"]
+           "spmm_f16_lora", "spmm_w4a4_dq_lora", "lora_workspace_bytes", "new_lora_workspace", "KVPages", "new_kv_pages",
+           "KVStep", "kv_step", "rope_frequencies", "qk_norm_rope", "qk_norm_rope_append", "Tokens", "quantize_tokens",
+           "dequantize_tokens", "EncodedInt8", "DenseInt8", "encode_int8", "gemm_workspace_bytes",
+           "new_gemm_workspace", "gemm_w8a8"]
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 library_path = os.path.join(HERE, "libbitmap_spmm.so")
 
 OK, E_ARG, E_RANGE, E_CAPACITY, E_OVERFLOW, E_HIP, E_UNSUPPORTED = 0, 1, 2, 3, 4, 5, 6
-INT4, FP16, INT2, INT8 = 0, 1, 2, 3      # INT8: a cache type only
+INT4, FP16, INT2, INT8 = 0, 1, 2, 3      # INT8: caches, tokens and the dense product only
 ALGO_AUTO, ALGO_ROWWAVE, ALGO_MFMA, ALGO_SPLITK = 0, 1, 2, 3
 PAYLOAD_ALIGN = 16
 MAX_N = 32
@@ -46,7 +49,10 @@ EXPORTS = ["encode_bitmap_tiles", "pack_int4_activations", "spmm_bitmap_w4a4", "
            "spmm_bitmap_w4a4_dq", "spmm_bitmap_w4a4_grouped", "spmm_bitmap_w2a4", "spmm_bitmap_w2a4_algo",
            "cbc_gtile_count", "encode_cbc_f16", "spmspv_cbc_workspace_bytes", "spmspv_cbc_f16",
            "kv_cache_append", "kv_cache_gather", "attention_tree_workspace_bytes", "attention_tree_f16",
-           "lora_workspace_bytes", "spmm_bitmap_f16_lora", "spmm_bitmap_w4a4_dq_lora"]
+           "lora_workspace_bytes", "spmm_bitmap_f16_lora", "spmm_bitmap_w4a4_dq_lora",
+           "kv_pages_step", "qk_norm_rope_f16", "qk_norm_rope_append_f16", "quantize_tokens_f16",
+           "dequantize_tokens_f16", "int8_tiles_bytes", "encode_int8_tiles", "gemm_w8a8_workspace_bytes",
+           "gemm_w8a8_dq"]
 
 
 class BspError(RuntimeError):
@@ -127,6 +133,18 @@ def load_library():
         L.spmm_bitmap_f16_lora.restype = I32
         L.spmm_bitmap_w4a4_dq_lora.argtypes = [P, P, P, I64, I64, I64, P, P, I64, P, P, P, P, P, I64, P]
         L.spmm_bitmap_w4a4_dq_lora.restype = I32
+        L.kv_pages_step.argtypes, L.kv_pages_step.restype = [P, P, P, P, I64, P, P, P, P, P, P], I32
+        L.qk_norm_rope_f16.argtypes = [P, I64, P, I64, I64, I64, I64, I64, P, P, I64, P, I64, P]
+        L.qk_norm_rope_f16.restype = I32
+        L.qk_norm_rope_append_f16.argtypes = [P, I64, P, I64, P, I64, I64, I64, P, P, P, P, I64, P]
+        L.qk_norm_rope_append_f16.restype = I32
+        L.quantize_tokens_f16.argtypes, L.quantize_tokens_f16.restype = [P, I32, P, I64, P], I32
+        L.dequantize_tokens_f16.argtypes, L.dequantize_tokens_f16.restype = [P, I64, I32, P, I64, I64, P, I64, P], I32
+        L.int8_tiles_bytes.argtypes, L.int8_tiles_bytes.restype = [I64, I64], I64
+        L.encode_int8_tiles.argtypes, L.encode_int8_tiles.restype = [P, I64, I64, I64, P], I32
+        L.gemm_w8a8_workspace_bytes.argtypes, L.gemm_w8a8_workspace_bytes.restype = [I64, I64, I64, P], I32
+        L.gemm_w8a8_dq.argtypes = [P, I64, I64, P, I64, I64, P, P, P, I64, P, I64, P]
+        L.gemm_w8a8_dq.restype = I32
         _lib = L
     return _lib
 
@@ -642,6 +660,7 @@ def new_workspace(dtype: int, M: int, K: int, N: int, nnz: int = -1, device="cud
 # ---- paged key/value cache, quantised as it is written ----
 
 TREE_MAX = 64
+PAGES_MAX_SEQUENCES = 8192
 
 
 class _KVCacheDesc(ctypes.Structure):
@@ -1009,3 +1028,369 @@ def spmm_w4a4_dq_lora(W: DeviceMatrix, X, X16, scale_w, scale_x, adapters: LoraA
         ctypes.byref(d), y, wp, wb)
     _check(rc, "spmm_bitmap_w4a4_dq_lora")
     return Yh
+
+
+# ---- pages, slots and positions of a step, made on the GPU ----
+
+class _KVPagesDesc(ctypes.Structure):
+    """bsp_kv_pages of include/bitmap_spmm.h."""
+    _fields_ = [("sequences", ctypes.c_int64), ("table_width", ctypes.c_int64), ("page_size", ctypes.c_int64),
+                ("pool", ctypes.c_int64), ("block_table", ctypes.c_void_p), ("lens", ctypes.c_void_p),
+                ("held", ctypes.c_void_p), ("free_pages", ctypes.c_void_p)]
+
+
+@dataclass(frozen=True)
+class KVPages:
+    """Which pages of a cache each sequence holds, in device memory and updated
+    there by kv_step (the tensors' contents change, the tensors do not): block_table int32 [B][width] (as attention_tree takes it), lens
+    int32 [B] tokens cached, held int32 [B] pages held, free int32 [2 + pool]: the number of
+    free pages, a counter of the call's own (0), the free pages (the next to be
+    taken last)."""
+    block_table: "object"
+    lens: "object"
+    held: "object"
+    free: "object"
+    page_size: int
+
+    def __post_init__(self):
+        import torch
+        if self.block_table.dim() != 2:
+            raise ValueError("block_table must be [B][width]")
+        B, width = (int(x) for x in self.block_table.shape)
+        _check_dev(self.block_table, "block_table", torch.int32)
+        index = self.block_table.get_device()
+        for n in ("lens", "held"):
+            _flat(getattr(self, n), n, torch.int32, B, index)
+        if self.free.dim() != 1 or self.free.numel() < 2:
+            raise ValueError("free must be [2 + pool]")
+        _flat(self.free, "free", torch.int32, self.free.numel(), index)
+        desc = _KVPagesDesc(B, width, self.page_size, self.free.numel() - 2, _dptr(self.block_table), _dptr(self.lens),
+                            _dptr(self.held), _dptr(self.free))
+        for name, value in (("sequences", B), ("width", width), ("device", self.block_table.device),
+                            ("_index", index), ("_desc", desc), ("_ref", ctypes.byref(desc))):
+            object.__setattr__(self, name, value)
+
+
+def new_kv_pages(sequences: int, width: int, num_pages: int, page_size: int, device="cuda") -> KVPages:
+    """Empty sequences, and all of a cache's num_pages pages free (page 0 is taken first)."""
+    import torch
+
+    def zeros(*shape):
+        return torch.zeros(shape, dtype=torch.int32, device=device)
+
+    free = zeros(2 + num_pages)
+    free[0] = num_pages
+    free[2:] = torch.arange(num_pages - 1, -1, -1, dtype=torch.int32, device=device)
+    return KVPages(zeros(sequences, width), zeros(sequences), zeros(sequences), free, page_size)
+
+
+class KVStep(NamedTuple):
+    """What a step's calls take: slots int64 [rows] (kv_append, qk_norm_rope_append), positions int32 [rows],
+    sequences int32 [rows] (-1: no sequence's), q_start int32 [B + 1] and kv_lens int32 [B] (attention_tree)."""
+    slots: "object"
+    positions: "object"
+    sequences: "object"
+    q_start: "object"
+    kv_lens: "object"
+
+
+def kv_step(pages: KVPages, keep, new_tokens, rows: int, tree_mask=None, out: Optional[KVStep] = None,
+            stream=None) -> KVStep:
+    """One step of all sequences, on the GPU: sequence b keeps the first keep[b] of its tokens (int32 [B]; None: all
+    of them) and appends new_tokens[b] (int32 [B]), in rows q_start[b] up to q_start[b + 1] of the step's `rows` token
+    rows. Pages that are no longer needed go back, those needed are taken; block_table, lens, held and free are
+    updated in place. tree_mask: int64 [rows], attention_tree's: positions follow the depth in the tree. A sequence
+    whose pages (or rows) do not fit waits: its slots are -1 and its kv_lens 0, and it keeps its kept tokens. Rows behind
+    the last sequence get slot -1, position 0, sequence -1."""
+    import torch
+    index, B = pages._index, pages.sequences
+    i32 = torch.int32
+    if out is None:
+        shapes = ((rows, torch.int64), (rows, i32), (rows, i32), (B + 1, i32), (B, i32))
+        out = KVStep(*(_new_output((n,), t, pages.device, stream) for n, t in shapes))
+    rc = _launch(
+        load_library().kv_pages_step, index, stream, pages._ref,
+        None if keep is None else _flat(keep, "keep", i32, B, index), _flat(new_tokens, "new_tokens", i32, B, index),
+        None if tree_mask is None else _flat(tree_mask, "tree_mask", torch.int64, rows, index), rows,
+        _flat(out.slots, "slots", torch.int64, rows, index), _flat(out.positions, "positions", i32, rows, index),
+        _flat(out.sequences, "sequences", i32, rows, index), _flat(out.q_start, "q_start", i32, B + 1, index),
+        _flat(out.kv_lens, "kv_lens", i32, B, index))
+    _check(rc, "kv_pages_step")
+    return out
+
+
+# ---- query and key heads normed, rotated, and written to the cache ----
+
+class _RotationDesc(ctypes.Structure):
+    """bsp_rotation of include/bitmap_spmm.h."""
+    _fields_ = [("rot", ctypes.c_int64), ("interleaved", ctypes.c_int), ("freq", ctypes.c_void_p),
+                ("positions", ctypes.c_void_p), ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p),
+                ("eps", ctypes.c_float)]
+
+
+def rope_frequencies(rot: int, base: float = 10000.0, angles=None, device="cuda"):
+    """int64 [rot / 2]: the turn of each pair per position, as a fraction of 2^64 of a whole one. angles: radians per
+    position (float64 [rot / 2], for scaled forms); default base ** (-2 i / rot)."""
+    import torch
+    if angles is None:
+        angles = float(base) ** (-2.0 * np.arange(rot // 2) / max(rot, 1))
+    angles = np.asarray(angles, np.float64)
+    if angles.shape != (rot // 2,) or not np.isfinite(angles).all():
+        raise ValueError("angles must be rot / 2 finite radians per position")
+    turns = np.mod(angles / (2.0 * np.pi), 1.0)
+    # 2^64 turns in two 32-bit halves, each an exact product
+    hi = np.floor(turns * 2.0 ** 32)
+    lo = np.floor((turns * 2.0 ** 32 - hi) * 2.0 ** 32)
+    words = (hi.astype(np.uint64) << np.uint64(32)) | lo.astype(np.uint64)
+    return torch.from_numpy(words.view(np.int64)).to(device)
+
+
+def _rotation(positions, freq, q_weight, k_weight, eps, interleaved, n, dim, index) -> _RotationDesc:
+    import torch
+    rot = 0 if freq is None else 2 * freq.numel()
+    f16 = torch.float16
+    return _RotationDesc(
+        rot, 1 if interleaved else 0, None if freq is None else _flat(freq, "freq", torch.int64, rot // 2, index),
+        None if freq is None else _flat(positions, "positions", torch.int32, n, index),
+        None if q_weight is None else _flat(q_weight, "q_weight", f16, dim, index),
+        None if k_weight is None else _flat(k_weight, "k_weight", f16, dim, index), eps)
+
+
+def _heads(t, name):
+    if t.dim() != 3 or not t.is_cuda:
+        raise ValueError(f"{name} must be [tokens][heads][head_dim] on the device")
+    return t.shape
+
+
+def qk_norm_rope(Q, K, positions, freq, q_weight=None, k_weight=None, eps: float = 1e-6, interleaved: bool = False,
+                 Qo=None, Ko=None, stream=None):
+    """Queries and keys normed head by head (x / sqrt(mean(x^2) + eps) * weight; no weight: not normed) and rotated to
+    their positions (int32 [n]): Q float16 [n][q_heads][head_dim], K [n][kv_heads][head_dim], a token's heads contiguous.
+    freq: rope_frequencies(rot), rot <= head_dim a multiple of 16 (None: no rotation). Qo, Ko: the results (may be
+    Q, K)."""
+    import torch
+    n, hq, dim = _heads(Q, "Q")
+    hkv = _heads(K, "K")[1]
+    index = Q.get_device()
+    qs, ks = _rows(Q, "Q", n, hq, dim, index), _rows(K, "K", n, hkv, dim, index)
+    if Qo is None:
+        Qo = _new_output((n, hq, dim), torch.float16, Q.device, stream)
+    if Ko is None:
+        Ko = _new_output((n, hkv, dim), torch.float16, Q.device, stream)
+    qo, ko = _rows(Qo, "Qo", n, hq, dim, index), _rows(Ko, "Ko", n, hkv, dim, index)
+    d = _rotation(positions, freq, q_weight, k_weight, eps, interleaved, n, dim, index)
+    rc = _launch(load_library().qk_norm_rope_f16, index, stream, Q.data_ptr(), qs, K.data_ptr(), ks, n, hq, hkv, dim,
+                 ctypes.byref(d), Qo.data_ptr(), qo, Ko.data_ptr(), ko)
+    _check(rc, "qk_norm_rope_f16")
+    return Qo, Ko
+
+
+def qk_norm_rope_append(Q, K, V, positions, freq, cache: KVCache, slots, q_weight=None, k_weight=None,
+                        eps: float = 1e-6, interleaved: bool = False, Qo=None, stream=None):
+    """qk_norm_rope with the keys and the values V written to the cache's slots (int64 [n]) in the same pass: what
+    qk_norm_rope and kv_append leave there, bit for bit. Returns the queries."""
+    import torch
+    n, hq, _ = _heads(Q, "Q")
+    hkv, dim, index = cache.kv_heads, cache.head_dim, cache._index
+    qs, ks, vs = _rows(Q, "Q", n, hq, dim, index), _rows(K, "K", n, hkv, dim, index), _rows(V, "V", n, hkv, dim, index)
+    if Qo is None:
+        Qo = _new_output((n, hq, dim), torch.float16, cache.device, stream)
+    qo = _rows(Qo, "Qo", n, hq, dim, index)
+    d = _rotation(positions, freq, q_weight, k_weight, eps, interleaved, n, dim, index)
+    rc = _launch(load_library().qk_norm_rope_append_f16, index, stream, Q.data_ptr(), qs, K.data_ptr(), ks,
+                 V.data_ptr(), vs, n, hq, ctypes.byref(d), cache._ref, _flat(slots, "slots", torch.int64, n, index),
+                 Qo.data_ptr(), qo)
+    _check(rc, "qk_norm_rope_append_f16")
+    return Qo
+
+
+# ---- hidden states quantised token by token ----
+
+class _TokensDesc(ctypes.Structure):
+    """bsp_tokens of include/bitmap_spmm.h."""
+    _fields_ = [("n", ctypes.c_int64), ("K", ctypes.c_int64), ("X", ctypes.c_void_p), ("x_stride", ctypes.c_int64),
+                ("residual", ctypes.c_void_p), ("residual_stride", ctypes.c_int64), ("weight", ctypes.c_void_p),
+                ("eps", ctypes.c_float), ("hidden", ctypes.c_void_p), ("hidden_stride", ctypes.c_int64),
+                ("x16", ctypes.c_void_p), ("x16_stride", ctypes.c_int64), ("scale", ctypes.c_void_p)]
+
+
+class Tokens(NamedTuple):
+    """Quantised tokens: codes (INT8: int8 [n][K], rows of whole 16 bytes; INT4: uint8 [n][ceil(K / 2)], packed), scale
+    float32 [n], and where asked for x16 (float16 [n][K], the values before quantisation) and hidden (float16 [n][K],
+    the residual sum)."""
+    codes: "object"
+    scale: "object"
+    x16: "object" = None
+    hidden: "object" = None
+
+
+def _matrix_rows(t, name, dtype, n, width, index) -> int:
+    """Check an [n][width] tensor whose rows may be strided; returns the stride between rows."""
+    import torch
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index and t.dim() == 2 and \
+            t.shape[0] == n and t.shape[1] == width:
+        s0, s1 = t.stride()
+        if s1 == 1 or width <= 1:
+            if n <= 1:
+                return max(s0, width)
+            if s0 >= width:
+                return s0
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA (HIP) tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on device {index}")
+    raise ValueError(f"{name} must be [{n}][{width}] with contiguous rows that do not overlap, got {tuple(t.shape)}")
+
+
+def _code_rows(codes, dtype, n, K, index):
+    """(address, row stride) of codes as Tokens holds them."""
+    import torch
+    if dtype == INT8:
+        return codes.data_ptr(), _matrix_rows(codes, "codes", torch.int8, n, K, index)
+    if dtype == INT4:
+        return codes.data_ptr(), _matrix_rows(codes, "codes", torch.uint8, n, (K + 1) // 2, index)
+    raise ValueError("codes are INT8 or INT4")
+
+
+def quantize_tokens(X, dtype: int, weight=None, eps: float = 1e-6, residual=None, hidden=None, x16=None, codes=None,
+                    scale=None, stream=None) -> Tokens:
+    """Tokens X float16 [n][K] as INT8 or (packed) INT4 codes with one scale each, for gemm_w8a8 and spmm_w4a4_dq.
+    residual: float16 [n][K], added first (the sum, rounded to float16, goes to `hidden`, which may be X or residual).
+    weight: float16 [K], the tokens are normed first (x / sqrt(mean(x^2) + eps) * weight). x16: True or a tensor for the
+    float16 values that the codes quantise. Every code is the correctly rounded one."""
+    import torch
+    if X.dim() != 2 or not X.is_cuda:
+        raise ValueError("X must be [n][K] on the device")
+    n, K = X.shape
+    index, f16 = X.get_device(), torch.float16
+    if dtype not in (INT8, INT4):
+        raise ValueError("codes are INT8 or INT4")
+    xs = _matrix_rows(X, "X", f16, n, K, index)
+    if residual is None and hidden is not None:
+        raise ValueError("hidden goes with residual")
+    if residual is not None and hidden is None:
+        hidden = _new_output((n, K), f16, X.device, stream)
+    if x16 is True:
+        x16 = _new_output((n, K), f16, X.device, stream)
+    elif x16 is False:
+        x16 = None
+    if codes is None:
+        if dtype == INT8:
+            codes = _new_output((n, (K + 15) // 16 * 16), torch.int8, X.device, stream)[:, :K]
+        else:
+            codes = _new_output((n, (K + 1) // 2), torch.uint8, X.device, stream)
+    if scale is None:
+        scale = _new_output((n,), torch.float32, X.device, stream)
+    cp, cs = _code_rows(codes, dtype, n, K, index)
+    d = _TokensDesc(
+        n, K, X.data_ptr(), xs, _dptr(residual),
+        0 if residual is None else _matrix_rows(residual, "residual", f16, n, K, index),
+        None if weight is None else _flat(weight, "weight", f16, K, index), eps, _dptr(hidden),
+        0 if hidden is None else _matrix_rows(hidden, "hidden", f16, n, K, index), _dptr(x16),
+        0 if x16 is None else _matrix_rows(x16, "x16", f16, n, K, index),
+        _flat(scale, "scale", torch.float32, n, index))
+    rc = _launch(load_library().quantize_tokens_f16, index, stream, ctypes.byref(d), dtype, cp, cs)
+    _check(rc, "quantize_tokens_f16")
+    return Tokens(codes, scale, x16, hidden)
+
+
+def dequantize_tokens(codes, scale, dtype: int, K: int, X=None, stream=None):
+    """float16 X [n][K], the values that the codes of quantize_tokens stand for."""
+    import torch
+    if not scale.is_cuda:
+        raise TypeError("scale must be a CUDA (HIP) tensor")
+    n, index = scale.numel(), scale.get_device()
+    sp = _flat(scale, "scale", torch.float32, n, index)
+    cp, cs = _code_rows(codes, dtype, n, K, index)
+    if X is None:
+        X = _new_output((n, K), torch.float16, scale.device, stream)
+    rc = _launch(load_library().dequantize_tokens_f16, index, stream, cp, cs, dtype, sp, n, K, X.data_ptr(),
+                 _matrix_rows(X, "X", torch.float16, n, K, index))
+    _check(rc, "dequantize_tokens_f16")
+    return X
+
+
+# ---- dense 8-bit product ----
+
+@dataclass
+class EncodedInt8:
+    """A dense int8 matrix laid out for gemm_w8a8 (host): tiles uint8, scale float32 [M]."""
+    M: int
+    K: int
+    tiles: np.ndarray
+    scale: np.ndarray
+
+    def to_device(self, device="cuda") -> "DenseInt8":
+        import torch
+        return DenseInt8(self.M, self.K, torch.from_numpy(self.tiles).to(device),
+                         torch.from_numpy(self.scale).to(device))
+
+
+@dataclass(frozen=True)
+class DenseInt8:
+    """A dense int8 matrix in device memory, as encode_int8 laid it out, with the scale of each row (channel)."""
+    M: int
+    K: int
+    tiles: "object"
+    scale: "object"
+
+    def __post_init__(self):
+        import torch
+        _check_dev(self.tiles, "tiles", torch.uint8, (self.M + 15) // 16 * ((self.K + 63) // 64) * 1024)
+        _flat(self.scale, "scale", torch.float32, self.M, self.tiles.get_device())
+
+
+def encode_int8(W: np.ndarray, scale: np.ndarray) -> EncodedInt8:
+    """Lay out a dense host matrix, int8 [M][K] with float32 [M] scales, for gemm_w8a8."""
+    L = load_library()
+    if W.dtype != np.int8 or W.ndim != 2:
+        raise TypeError("W must be a 2-D int8 array")
+    W = np.ascontiguousarray(W)
+    M, K = W.shape
+    scale = np.ascontiguousarray(scale, np.float32)
+    if scale.shape != (M,):
+        raise ValueError("scale must be [M]")
+    tiles = np.empty(L.int8_tiles_bytes(M, K), np.uint8)
+    _check(L.encode_int8_tiles(_np_ptr(W), M, K, K, _np_ptr(tiles)), "encode_int8_tiles")
+    return EncodedInt8(M, K, tiles, scale)
+
+
+def gemm_workspace_bytes(M: int, K: int, N: int) -> int:
+    """Bytes of workspace gemm_w8a8 uses to split K over workgroups (0: none)."""
+    out = ctypes.c_int64(0)
+    _check(load_library().gemm_w8a8_workspace_bytes(M, K, N, ctypes.byref(out)), "gemm_w8a8_workspace_bytes")
+    return int(out.value)
+
+
+def new_gemm_workspace(W: DenseInt8, N: int, device="cuda"):
+    """A zero-filled workspace for gemm_w8a8 with N tokens (None if none is used).
+    It is cleared on the current stream: calls on another one wait for that."""
+    import torch
+    n = gemm_workspace_bytes(W.M, W.K, N)
+    return torch.zeros(n, dtype=torch.uint8, device=device) if n else None
+
+
+def gemm_w8a8(W: DenseInt8, X, scale_x, Y=None, workspace=None, stream=None):
+    """float16 Y [N][M] = (W x_n) * W.scale[m] * scale_x[n], int32 sums, any N. X: int8 [N][K], rows of whole 16 bytes
+    in memory (as quantize_tokens leaves them); scale_x: float32 [N]. workspace: new_gemm_workspace(W, N), or None for
+    no split over K."""
+    import torch
+    if X.dim() != 2 or X.shape[1] != W.K:
+        raise ValueError("X must be [N][K]")
+    N, index = X.shape[0], W.tiles.get_device()
+    xs = _matrix_rows(X, "X", torch.int8, N, W.K, index)
+    if N <= 1 or W.K == 0:
+        xs = (W.K + 15) // 16 * 16
+    if xs != W.K and N > 0 and X.untyped_storage().nbytes() < X.storage_offset() + N * xs:
+        raise ValueError("X: every row must be readable up to its stride")
+    if Y is None:
+        Y = _new_output((N, W.M), torch.float16, X.device, stream)
+    ys = _matrix_rows(Y, "Y", torch.float16, N, W.M, index)
+    wp, wb = _ws_args(workspace, index)
+    rc = _launch(load_library().gemm_w8a8_dq, index, stream, W.tiles.data_ptr(), W.M, W.K, X.data_ptr(), xs, N,
+                 _flat(W.scale, "W.scale", torch.float32, W.M, index),
+                 _flat(scale_x, "scale_x", torch.float32, N, index), Y.data_ptr(), ys, wp, wb)
+    _check(rc, "gemm_w8a8_dq")
+    return Y

@@ -26,6 +26,13 @@ __device__ __forceinline__ uint16_t bsp_f2h(float f) {
     return __builtin_bit_cast(uint16_t, (_Float16)f);
 }
 
+// The value as fp32, rounded: left to itself the compiler turns a product or sum and
+// its conversion to fp16 into one mixed-precision operation that rounds once.
+__device__ __forceinline__ float bsp_rounded(float f) {
+    asm("" : "+v"(f));
+    return f;
+}
+
 // Sum over the 64 lanes of a wavefront; every lane receives the total.
 template <class T>
 __device__ __forceinline__ T bsp_wave_sum(T v) {

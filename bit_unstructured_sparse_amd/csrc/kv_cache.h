@@ -1,14 +1,102 @@
-// kv_cache.h -- what the cache kernels and the attention kernels share: the
-// scale word of a quantised row and the checks of a cache descriptor.
+// kv_cache.h -- what the kernels that write or read the cache share: the
+// scale word of a quantised row, the quantisation of a row held 8 channels to a
+// lane, and the checks of a cache descriptor.
 #pragma once
 #include <stdint.h>
 
 #include "bitmap_spmm.h"
+#include "device_common.h"
+
+typedef uint32_t kv_u4 __attribute__((ext_vector_type(4)));
+typedef uint32_t kv_u2 __attribute__((ext_vector_type(2)));
+typedef _Float16 kv_h8 __attribute__((ext_vector_type(8)));
 
 // A row's scale word: step as bfloat16 (high half), offset as fp16 (low half).
 __device__ __forceinline__ float kv_word_step(uint32_t w) { return __builtin_bit_cast(float, w & 0xFFFF0000u); }
 __device__ __forceinline__ float kv_word_offset(uint32_t w) {
     return (float)__builtin_bit_cast(_Float16, (uint16_t)w);
+}
+
+// 8 fp16 values at p; element loads when p may be off a 16-byte boundary.
+template <bool VEC>
+__device__ __forceinline__ kv_u4 kv_load8(const uint16_t *p) {
+    if constexpr (VEC) return *reinterpret_cast<const kv_u4 *>(p);
+    kv_u4 v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = (uint32_t)p[2 * i] | ((uint32_t)p[2 * i + 1] << 16);
+    return v;
+}
+
+template <bool VEC>
+__device__ __forceinline__ void kv_store8(uint16_t *p, kv_u4 v) {
+    if constexpr (VEC) {
+        *reinterpret_cast<kv_u4 *>(p) = v;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            p[2 * i] = (uint16_t)v[i];
+            p[2 * i + 1] = (uint16_t)(v[i] >> 16);
+        }
+    }
+}
+
+// Quantise the 8 values of a lane; the row's lanes are LPR neighbours.
+// (x - o) / s is needed correctly rounded, so that a value half way between
+// two codes goes to the even one: with r the correctly rounded reciprocal of
+// s, q = fma(fma(-q0, s, n), r, q0), q0 = n r, is the correctly rounded
+// quotient (Markstein's theorem), at three operations instead of a division.
+template <int LPR>
+__device__ __forceinline__ void kv_quantise(kv_u4 raw, float levels, uint32_t (&u)[8], uint32_t &word) {
+    const kv_h8 h = __builtin_bit_cast(kv_h8, raw);
+    float x[8], lo, hi;
+    uint32_t big = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        x[i] = (float)h[i];
+        lo = i == 0 ? x[0] : fminf(lo, x[i]);
+        hi = i == 0 ? x[0] : fmaxf(hi, x[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) big = max(big, max(raw[i] & 0x7FFFu, (raw[i] >> 16) & 0x7FFFu));
+#pragma unroll
+    for (int d = 1; d < LPR; d <<= 1) {
+        lo = fminf(lo, __shfl_xor(lo, d, 64));
+        hi = fmaxf(hi, __shfl_xor(hi, d, 64));
+        big = max(big, (uint32_t)__shfl_xor((int)big, d, 64));
+    }
+    if (big >= 0x7C00u) {      // an infinity or a NaN in the row
+        word = 0x7FC07E00u;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) u[i] = 0;
+        return;
+    }
+    const uint32_t sb = (__builtin_bit_cast(uint32_t, (hi - lo) / levels) + 0xFFFFu) & 0xFFFF0000u;
+    const float s = __builtin_bit_cast(float, sb);
+    word = sb | bsp_f2h(lo);
+    const float r = sb != 0 ? 1.0f / s : 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float nmr = x[i] - lo;
+        const float q0 = nmr * r;
+        const float q = __builtin_fmaf(__builtin_fmaf(-q0, s, nmr), r, q0);
+        u[i] = (uint32_t)fminf(rintf(q), levels);
+    }
+}
+
+// The codes of channels ch .. ch + 7 of a row, `at` = row * D + ch.
+template <int KIND>
+__device__ __forceinline__ void kv_store_codes(uint8_t *codes, int64_t at, const uint32_t (&u)[8]) {
+    if constexpr (KIND == BSP_INT8) {
+        kv_u2 c;
+        c.x = u[0] | (u[1] << 8) | (u[2] << 16) | (u[3] << 24);
+        c.y = u[4] | (u[5] << 8) | (u[6] << 16) | (u[7] << 24);
+        *reinterpret_cast<kv_u2 *>(codes + at) = c;
+    } else {
+        uint32_t c = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) c |= u[e] << (4 * e);
+        *reinterpret_cast<uint32_t *>(codes + at / 2) = c;
+    }
 }
 
 // Bytes of one cache row.

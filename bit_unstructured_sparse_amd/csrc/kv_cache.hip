@@ -24,10 +24,6 @@
 
 namespace {
 
-typedef uint32_t kv_u4 __attribute__((ext_vector_type(4)));
-typedef uint32_t kv_u2 __attribute__((ext_vector_type(2)));
-typedef _Float16 kv_h8 __attribute__((ext_vector_type(8)));
-
 struct KvArgs {
     const uint16_t *K, *V;       // append: source rows
     uint16_t *Ko, *Vo;           // gather: destination rows
@@ -73,72 +69,6 @@ __device__ __forceinline__ int64_t kv_row(const KvArgs &a, int64_t slot, int hea
     return (((page * a.hkv + head) << a.page_shift)) + off;
 }
 
-// 8 fp16 values at p; element loads when p may be off a 16-byte boundary.
-template <bool VEC>
-__device__ __forceinline__ kv_u4 kv_load8(const uint16_t *p) {
-    if constexpr (VEC) return *reinterpret_cast<const kv_u4 *>(p);
-    kv_u4 v;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = (uint32_t)p[2 * i] | ((uint32_t)p[2 * i + 1] << 16);
-    return v;
-}
-
-template <bool VEC>
-__device__ __forceinline__ void kv_store8(uint16_t *p, kv_u4 v) {
-    if constexpr (VEC) {
-        *reinterpret_cast<kv_u4 *>(p) = v;
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            p[2 * i] = (uint16_t)v[i];
-            p[2 * i + 1] = (uint16_t)(v[i] >> 16);
-        }
-    }
-}
-
-// Quantise the 8 values of a lane; the row's lanes are LPR neighbours.
-// (x - o) / s is needed correctly rounded, so that a value half way between
-// two codes goes to the even one: with r the correctly rounded reciprocal of
-// s, q = fma(fma(-q0, s, n), r, q0), q0 = n r, is the correctly rounded
-// quotient (Markstein's theorem), at three operations instead of a division.
-template <int LPR>
-__device__ __forceinline__ void kv_quantise(kv_u4 raw, float levels, uint32_t (&u)[8], uint32_t &word) {
-    const kv_h8 h = __builtin_bit_cast(kv_h8, raw);
-    float x[8], lo, hi;
-    uint32_t big = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        x[i] = (float)h[i];
-        lo = i == 0 ? x[0] : fminf(lo, x[i]);
-        hi = i == 0 ? x[0] : fmaxf(hi, x[i]);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) big = max(big, max(raw[i] & 0x7FFFu, (raw[i] >> 16) & 0x7FFFu));
-#pragma unroll
-    for (int d = 1; d < LPR; d <<= 1) {
-        lo = fminf(lo, __shfl_xor(lo, d, 64));
-        hi = fmaxf(hi, __shfl_xor(hi, d, 64));
-        big = max(big, (uint32_t)__shfl_xor((int)big, d, 64));
-    }
-    if (big >= 0x7C00u) {      // an infinity or a NaN in the row
-        word = 0x7FC07E00u;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) u[i] = 0;
-        return;
-    }
-    const uint32_t sb = (__builtin_bit_cast(uint32_t, (hi - lo) / levels) + 0xFFFFu) & 0xFFFF0000u;
-    const float s = __builtin_bit_cast(float, sb);
-    word = sb | bsp_f2h(lo);
-    const float r = sb != 0 ? 1.0f / s : 0.0f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float nmr = x[i] - lo;
-        const float q0 = nmr * r;
-        const float q = __builtin_fmaf(__builtin_fmaf(-q0, s, nmr), r, q0);
-        u[i] = (uint32_t)fminf(rintf(q), levels);
-    }
-}
-
 // The fp16 value a code stands for. s * u + o may pass the largest finite fp16
 // (a step rounded up, on a row that reaches it): saturated, so that finite
 // rows read back finite. (The comparison keeps a NaN.)
@@ -176,17 +106,7 @@ __global__ __launch_bounds__(KV_BLOCK) void k_kv_append(const KvArgs a, uint32_t
             uint32_t u[8], word;
             kv_quantise<D / 8>(raw[i], KIND == BSP_INT8 ? 255.0f : 15.0f, u, word);
             if (!ok) continue;
-            if constexpr (KIND == BSP_INT8) {
-                kv_u2 c;
-                c.x = u[0] | (u[1] << 8) | (u[2] << 16) | (u[3] << 24);
-                c.y = u[4] | (u[5] << 8) | (u[6] << 16) | (u[7] << 24);
-                *reinterpret_cast<kv_u2 *>(codes + row * D + it.ch) = c;
-            } else {
-                uint32_t c = 0;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) c |= u[e] << (4 * e);
-                *reinterpret_cast<uint32_t *>(codes + row * (D / 2) + it.ch / 2) = c;
-            }
+            kv_store_codes<KIND>(codes, row * D + it.ch, u);
             if (it.ch == 0) (it.is_v ? a.vw : a.kw)[row] = word;
         }
     }

@@ -1,0 +1,272 @@
+// qk_heads.hip -- query and key heads normed and rotated, and (with the values)
+// written to the paged cache, for gfx950.
+//
+// One lane holds 8 channels of a head (a 16-byte piece), as in the cache kernels: a
+// head is 8, 16 or 32 lanes and a wavefront holds 8, 4 or 2 of them, neighbouring
+// heads of one token. A wavefront works on U such groups of one token and one
+// kind (query, key or value), so that the angles, which all heads of a token share,
+// are found once for U groups, and U loads of 16 bytes a lane are in flight.
+//
+// The angle of pair i at position p is p * freq[i] turns, freq in units of 2^-64
+// turns: the product mod 2^64 is the angle mod one turn, exactly. Its upper 32 bits
+// (2^-32 turns) are split into a multiple of a quarter turn and a rest of at most an
+// eighth, whose sine and cosine are their Taylor sums to x^9 and x^8: at most
+// 2^-24.9 off (the first term left out, (pi/4)^10 / 10!).
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "bitmap_spmm.h"
+#include "device_common.h"
+#include "kv_cache.h"
+
+namespace {
+
+#define QK_BLOCK 256
+
+struct QkArgs {
+    const uint16_t *x[3];         // query, key, value heads
+    uint16_t *o[2];               // their results (o[1] null: keys go to the cache)
+    int64_t xs[3], os[2];         // token strides in elements
+    const uint16_t *weight[2];
+    const uint64_t *freq;
+    const int32_t *positions;
+    const int64_t *slots;
+    uint8_t *codes[2];            // the cache
+    uint32_t *words[2];
+    int64_t nslots;
+    float eps;
+    int heads[3];                 // heads of each kind; values: 0 without a cache
+    uint32_t parts[3];            // running number of a token's items: queries, keys, values
+    uint32_t n;
+    int kind, page_shift, rot, interleaved;
+};
+
+// sin and cos of u * 2^-32 turns.
+__device__ __forceinline__ void qk_sincos(uint32_t u, float &s, float &c) {
+    const uint32_t q = (u + 0x20000000u) >> 30;              // nearest quarter
+    const float x = (float)(int32_t)(u - (q << 30)) * 1.4629180792671596e-9f;     // 2 pi / 2^32
+    const float z = x * x;
+    float sn = __builtin_fmaf(z, 2.7557319223985893e-6f, -1.984126984126984e-4f);
+    sn = __builtin_fmaf(z, sn, 8.333333333333333e-3f);
+    sn = __builtin_fmaf(z, sn, -0.16666666666666666f);
+    sn = __builtin_fmaf(z * x, sn, x);
+    float cs = __builtin_fmaf(z, 2.48015873015873e-5f, -1.388888888888889e-3f);
+    cs = __builtin_fmaf(z, cs, 4.1666666666666664e-2f);
+    cs = __builtin_fmaf(z, cs, -0.5f);
+    cs = __builtin_fmaf(z, cs, 1.0f);
+    s = (q & 1) ? cs : sn;
+    c = (q & 1) ? sn : cs;
+    if (q & 2) s = -s;
+    if ((q + 1) & 2) c = -c;
+}
+
+// The upper 32 bits of p * f mod 2^64, p signed.
+__device__ __forceinline__ uint32_t qk_turn(int32_t p, uint64_t f) {
+    const uint32_t lo = (uint32_t)f, hi = (uint32_t)(f >> 32);
+    return (uint32_t)p * hi + __umulhi((uint32_t)p, lo) - (p < 0 ? lo : 0);
+}
+
+template <int D, bool VEC, int U>
+__global__ __launch_bounds__(QK_BLOCK) void k_qk_heads(const QkArgs a, uint32_t items) {
+    constexpr int LPR = D / 8, RPW = 64 / LPR;
+    const uint32_t item = __builtin_amdgcn_readfirstlane(blockIdx.x * (QK_BLOCK / 64) + (threadIdx.x >> 6));
+    if (item >= items) return;
+    const uint32_t token = item / a.parts[2], part = item - token * a.parts[2];
+    const int kind = part < a.parts[0] ? 0 : part < a.parts[1] ? 1 : 2;
+    const int first = (int)(part - (kind == 0 ? 0 : a.parts[kind - 1])) * (RPW * U);
+    const int lane = threadIdx.x & 63, heads = a.heads[kind];
+    const int ch = (lane % LPR) * 8;
+    const uint16_t *src = a.x[kind] + (int64_t)token * a.xs[kind];
+    kv_u4 raw[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+        // heads past the last are read as head 0, so that every lane of the shuffles holds a value
+        const int h = first + i * RPW + lane / LPR;
+        raw[i] = kv_load8<VEC>(src + (int64_t)(h < heads ? h : 0) * D + ch);
+    }
+    const int rot = kind == 2 ? 0 : a.rot;
+    float sn[8], cs[8];
+    int partner = lane;
+    bool upper = false;
+    if (rot > 0) {
+        const int32_t p = a.positions[token];
+        if (a.interleaved) {
+            if (ch < rot) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) qk_sincos(qk_turn(p, a.freq[ch / 2 + e]), sn[e], cs[e]);
+            }
+        } else if (ch < rot) {
+            const int half = rot / 2;
+            upper = ch >= half;
+            partner = upper ? lane - half / 8 : lane + half / 8;
+            const uint64_t *f = a.freq + (upper ? ch - half : ch);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                qk_sincos(qk_turn(p, f[e]), sn[e], cs[e]);
+                if (!upper) sn[e] = -sn[e];        // y1 cos - y2 sin below, y2 cos + y1 sin above
+            }
+        }
+    }
+    const uint16_t *weight = kind == 2 ? nullptr : a.weight[kind];
+    kv_h8 w;
+    if (weight != nullptr) w = __builtin_bit_cast(kv_h8, *reinterpret_cast<const kv_u4 *>(weight + ch));
+    const int64_t slot = a.o[1] == nullptr && kind > 0 ? a.slots[token] : -1;
+    const bool stored = slot >= 0 && slot < a.nslots;
+    const int64_t page = (stored ? slot : 0) >> a.page_shift;
+    const int64_t off = (stored ? slot : 0) & (((int64_t)1 << a.page_shift) - 1);
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+        const int h = first + i * RPW + lane / LPR;
+        const bool live = h < heads;
+        if (kind != 2) {
+            const kv_h8 x = __builtin_bit_cast(kv_h8, raw[i]);
+            float y[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] = (float)x[e];
+            if (weight != nullptr) {
+                float sum = 0.0f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) sum = __builtin_fmaf(y[e], y[e], sum);
+#pragma unroll
+                for (int d = 1; d < LPR; d <<= 1) sum += __shfl_xor(sum, d, 64);
+                const float r = 1.0f / sqrtf(sum * (1.0f / D) + a.eps);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) y[e] = y[e] * r * (float)w[e];
+            }
+            if (rot > 0) {
+                if (a.interleaved) {
+                    if (ch < rot) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float y1 = y[2 * e], y2 = y[2 * e + 1];
+                            y[2 * e] = y1 * cs[e] - y2 * sn[e];
+                            y[2 * e + 1] = y2 * cs[e] + y1 * sn[e];
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float other = __shfl(y[e], partner, 64);
+                        if (ch < rot) y[e] = y[e] * cs[e] + other * sn[e];
+                    }
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                raw[i][e] = bsp_f2h(bsp_rounded(y[2 * e])) | ((uint32_t)bsp_f2h(bsp_rounded(y[2 * e + 1])) << 16);
+        }
+        if (kind == 0 || a.o[1] != nullptr) {
+            if (live) kv_store8<VEC>(a.o[kind] + (int64_t)token * a.os[kind] + (int64_t)h * D + ch, raw[i]);
+            continue;
+        }
+        const int64_t row = ((page * heads + (live ? h : 0)) << a.page_shift) + off;
+        uint8_t *codes = a.codes[kind - 1];
+        if (a.kind == BSP_FP16) {
+            if (live && stored) *reinterpret_cast<kv_u4 *>(codes + row * (2 * D) + 2 * ch) = raw[i];
+        } else {
+            uint32_t u[8], word;
+            kv_quantise<LPR>(raw[i], a.kind == BSP_INT8 ? 255.0f : 15.0f, u, word);
+            if (!(live && stored)) continue;
+            if (a.kind == BSP_INT8)
+                kv_store_codes<BSP_INT8>(codes, row * D + ch, u);
+            else
+                kv_store_codes<BSP_INT4>(codes, row * D + ch, u);
+            if (ch == 0) a.words[kind - 1][row] = word;
+        }
+    }
+}
+
+template <int D, bool VEC, int U>
+void qk_launch_u(QkArgs &a, hipStream_t stream) {
+    constexpr int RUN = 64 / (D / 8) * U;
+    uint32_t total = 0;
+    for (int k = 0; k < 3; ++k) a.parts[k] = total += (uint32_t)((a.heads[k] + RUN - 1) / RUN);
+    const uint32_t items = a.n * total;
+    const unsigned grid = (items + QK_BLOCK / 64 - 1) / (QK_BLOCK / 64);
+    hipLaunchKernelGGL((k_qk_heads<D, VEC, U>), dim3(grid), dim3(QK_BLOCK), 0, stream, a, items);
+}
+
+template <int D>
+void qk_launch(QkArgs &a, bool vec, hipStream_t stream) {
+    if (vec)
+        qk_launch_u<D, true, 1>(a, stream);
+    else
+        qk_launch_u<D, false, 1>(a, stream);
+}
+
+int qk_common(QkArgs &a, int64_t n, int64_t hq, int64_t hkv, int64_t D, const bsp_rotation *r, bool values,
+              hipStream_t stream) {
+    if (D != 64 && D != 128 && D != 256) return BSP_E_UNSUPPORTED;
+    if (hq > INT32_MAX / 4 || hkv > INT32_MAX / 4) return BSP_E_OVERFLOW;
+    // a launch holds fewer than 2^32 threads (2 heads at least per wavefront)
+    if (n >= (INT64_C(1) << 28) / std::max<int64_t>(hq + 2 * hkv, 1)) return BSP_E_OVERFLOW;
+    if (r->rot < 0 || r->rot > D || r->rot % 16 != 0) return BSP_E_UNSUPPORTED;
+    if (!(r->eps >= 0.0f) || std::isinf(r->eps)) return BSP_E_ARG;
+    if ((((uintptr_t)r->q_weight | (uintptr_t)r->k_weight) & 15u) != 0) return BSP_E_ARG;
+    if (n == 0 || hq + hkv == 0) return BSP_OK;
+    const int64_t heads[3] = {hq, hkv, values ? hkv : 0};
+    uintptr_t bits = 0;
+    int64_t strides = 0;
+    for (int k = 0; k < 3; ++k) {
+        a.heads[k] = (int)heads[k];
+        if (heads[k] == 0) continue;
+        const bool out = k == 0 || (k == 1 && !values);
+        if (a.x[k] == nullptr || (out && a.o[k] == nullptr)) return BSP_E_ARG;
+        if (a.xs[k] < heads[k] * D || (out && a.os[k] < heads[k] * D)) return BSP_E_ARG;
+        bits |= (uintptr_t)a.x[k], strides |= a.xs[k];
+        if (out) bits |= (uintptr_t)a.o[k], strides |= a.os[k];
+    }
+    if ((bits & 1u) != 0) return BSP_E_ARG;
+    if (r->rot > 0) {
+        if (r->freq == nullptr || r->positions == nullptr) return BSP_E_ARG;
+        if (((uintptr_t)r->freq & 7u) != 0 || ((uintptr_t)r->positions & 3u) != 0) return BSP_E_ARG;
+    }
+    a.weight[0] = r->q_weight, a.weight[1] = r->k_weight;
+    a.freq = r->freq, a.positions = r->positions;
+    a.eps = r->eps, a.rot = (int)r->rot, a.interleaved = r->interleaved != 0;
+    a.n = (uint32_t)n;
+    // whole 16-byte pieces of the heads, unless they are off that boundary
+    const bool vec = (bits & 15u) == 0 && (strides & 7) == 0;
+    if (D == 64)
+        qk_launch<64>(a, vec, stream);
+    else if (D == 128)
+        qk_launch<128>(a, vec, stream);
+    else
+        qk_launch<256>(a, vec, stream);
+    return hipGetLastError() == hipSuccess ? BSP_OK : BSP_E_HIP;
+}
+
+}  // namespace
+
+extern "C" int qk_norm_rope_f16(const uint16_t *Q, int64_t q_stride, const uint16_t *K, int64_t k_stride, int64_t n,
+                                int64_t q_heads, int64_t kv_heads, int64_t head_dim, const bsp_rotation *rotation,
+                                uint16_t *Qo, int64_t qo_stride, uint16_t *Ko, int64_t ko_stride,
+                                hipStream_t stream) {
+    if (rotation == nullptr || n < 0 || q_heads < 0 || kv_heads < 0) return BSP_E_ARG;
+    QkArgs a{};
+    a.x[0] = Q, a.x[1] = K, a.xs[0] = q_stride, a.xs[1] = k_stride;
+    a.o[0] = Qo, a.o[1] = Ko, a.os[0] = qo_stride, a.os[1] = ko_stride;
+    return qk_common(a, n, q_heads, kv_heads, head_dim, rotation, false, stream);
+}
+
+extern "C" int qk_norm_rope_append_f16(const uint16_t *Q, int64_t q_stride, const uint16_t *K, int64_t k_stride,
+                                       const uint16_t *V, int64_t v_stride, int64_t n, int64_t q_heads,
+                                       const bsp_rotation *rotation, const bsp_kv_cache *cache, const int64_t *slots,
+                                       uint16_t *Qo, int64_t qo_stride, hipStream_t stream) {
+    const int rc = kv_check_cache(cache);
+    if (rc != BSP_OK) return rc;
+    if (rotation == nullptr || n < 0 || q_heads < 0) return BSP_E_ARG;
+    if (n > 0 && cache->kv_heads > 0 && (slots == nullptr || ((uintptr_t)slots & 7u) != 0)) return BSP_E_ARG;
+    QkArgs a{};
+    a.x[0] = Q, a.x[1] = K, a.x[2] = V, a.xs[0] = q_stride, a.xs[1] = k_stride, a.xs[2] = v_stride;
+    a.o[0] = Qo, a.os[0] = qo_stride;
+    a.slots = slots;
+    a.codes[0] = (uint8_t *)cache->k, a.codes[1] = (uint8_t *)cache->v;
+    a.words[0] = cache->k_scale, a.words[1] = cache->v_scale;
+    a.nslots = cache->num_pages * cache->page_size;
+    a.kind = cache->dtype;
+    a.page_shift = __builtin_ctzll((unsigned long long)cache->page_size);
+    return qk_common(a, n, q_heads, cache->kv_heads, cache->head_dim, rotation, true, stream);
+}

@@ -628,6 +628,189 @@ int spmm_bitmap_w4a4_dq_lora(const uint64_t *bitmaps, const uint32_t *offsets, c
                              int64_t N, const float *scale_w, const float *scale_x, const bsp_lora *lora,
                              uint16_t *Yh, void *workspace, int64_t workspace_bytes, hipStream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Block tables, slots and positions of a step, made on the GPU.
+ *   The pages of a cache are handed to sequences from a list of free ones. All
+ *   of it is device memory that a step reads and updates in place, so a captured
+ *   step needs nothing from the host.
+ *   block_table  int32 [sequences][table_width], as attention_tree_f16 takes it;
+ *                entries past a sequence's held pages mean nothing.
+ *   lens         int32 [sequences], tokens a sequence has in the cache.
+ *   held         int32 [sequences], pages it holds: entries 0 .. held-1 of its row
+ *                (ceil(lens / page_size), or more after it had to wait).
+ *   free_pages   int32 [2 + pool]: the number of free pages, a counter of the call's
+ *                own (zero before its first use, left zero), then the pages,
+ *                the next to be taken last.
+ * Values that cannot be (lens past the table, a count past the pool, ...) are
+ * taken as the nearest that can: nothing outside the arrays is touched.
+ * --------------------------------------------------------------------------- */
+typedef struct bsp_kv_pages {
+    int64_t sequences;      /* 0 .. BSP_PAGES_MAX_SEQUENCES */
+    int64_t table_width;    /* sequences * table_width + pool < 2^31 */
+    int64_t page_size;      /* a power of two, 16 .. 4096; table_width * page_size < 2^31 - 4096 */
+    int64_t pool;           /* pages the list can hold */
+    int32_t *block_table, *lens, *held, *free_pages;   /* DEVICE */
+} bsp_kv_pages;
+
+#define BSP_PAGES_MAX_SEQUENCES 8192
+
+/*
+ * kv_pages_step -- one step of all sequences, asynchronous on `stream`: sequence
+ * b keeps the first keep[b] of its tokens (a rejected draft goes, a finished
+ * request keeps none) and appends new_tokens[b].
+ *   keep, new_tokens  DEVICE int32 [sequences]; keep NULL: all kept. Clamped to
+ *                0 .. lens[b], and to 0 from below.
+ *   tree_mask    DEVICE uint64 [rows], or NULL: attention_tree_f16's words.
+ *   rows         rows of the step's token arrays (0 .. 2^28 - 1), sequence b's from q_start[b].
+ *   slots        DEVICE int64 [rows]: the slot of each new token, for kv_cache_append.
+ *   positions    DEVICE int32 [rows]: keep + i for the i-th new token; with tree_mask,
+ *                in sequences of at most BSP_TREE_MAX new tokens, keep + the number of
+ *                bits below i in its word (its ancestors).
+ *   sequences    DEVICE int32 [rows]: the sequence of each row.
+ *   q_start      DEVICE int32 [sequences + 1]: new tokens before each sequence, at most rows.
+ *   kv_lens      DEVICE int32 [sequences]: the new length, what attention takes.
+ * Rows behind the last sequence get slot -1, position 0 and sequence -1. A
+ * sequence then needs ceil(length / page_size) pages. Pages given back are numbered
+ * in order of sequence and place, pages taken likewise: the n-th taken is the n-th
+ * given back, past those the list's last, last but one, ...; what was given back and
+ * not taken is put onto the list's end, the first given back last (so that a step and
+ * the one that undoes it restore every entry).
+ * A sequence waits when its rows pass `rows`, its pages pass table_width, or it
+ * takes pages and the pages taken up to it are more than there are (then so do the
+ * later ones that take pages): it keeps its pages and its kept tokens, appends none,
+ * gets slots -1 and kv_lens 0 (attention then gives zeros for its rows).
+ * Calls on the same pages must be ordered on one stream. The outputs must not overlap
+ * the inputs.
+ */
+int kv_pages_step(const bsp_kv_pages *pages, const int32_t *keep, const int32_t *new_tokens,
+                  const uint64_t *tree_mask, int64_t rows, int64_t *slots, int32_t *positions, int32_t *sequences,
+                  int32_t *q_start, int32_t *kv_lens, hipStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Queries and keys normed head by head and rotated to their positions.
+ *   y = x / sqrt(mean(x^2) + eps) * weight over a head's channels (no weight: y = x);
+ *   then pairs (y1, y2) of its first `rot` channels become
+ *   (y1 cos a - y2 sin a, y2 cos a + y1 sin a), pair i at the angle of position
+ *   p: a = p * freq[i] turns. Pair i is channels (i, i + rot / 2), or (2 i, 2 i + 1)
+ *   where interleaved. fp32 throughout, one rounding to fp16 at the end.
+ *   freq holds turns per position as fractions of 2^64, so that p * freq[i] mod
+ *   2^64 is the angle mod one turn without a rounding, however far the position.
+ * --------------------------------------------------------------------------- */
+typedef struct bsp_rotation {
+    int64_t rot;                 /* rotated channels: a multiple of 16, 0 .. head_dim (BSP_E_UNSUPPORTED otherwise) */
+    int interleaved;             /* 0: pairs (i, i + rot / 2); 1: pairs (2 i, 2 i + 1) */
+    const uint64_t *freq;        /* DEVICE [rot / 2] */
+    const int32_t *positions;    /* DEVICE [n] */
+    const uint16_t *q_weight;    /* DEVICE fp16 [head_dim], 16-byte aligned, or NULL: queries not normed */
+    const uint16_t *k_weight;    /* the same for keys */
+    float eps;                   /* finite, >= 0 */
+} bsp_rotation;
+
+/*
+ * qk_norm_rope_f16 -- n tokens' query and key heads, asynchronous on `stream`.
+ *   Q, K         DEVICE fp16 [n][q_heads][head_dim], [n][kv_heads][head_dim], token t at
+ *                element t * stride (a slice of a fused projection's output will do).
+ *   Qo, Ko       the results, with strides of their own; may be Q, K with their strides,
+ *                and must not overlap the inputs otherwise.
+ *   head_dim     64, 128 or 256 (BSP_E_UNSUPPORTED otherwise).
+ * n * (q_heads + 2 kv_heads) >= 2^28 is refused (BSP_E_OVERFLOW), here and below.
+ */
+int qk_norm_rope_f16(const uint16_t *Q, int64_t q_stride, const uint16_t *K, int64_t k_stride, int64_t n,
+                     int64_t q_heads, int64_t kv_heads, int64_t head_dim, const bsp_rotation *rotation, uint16_t *Qo,
+                     int64_t qo_stride, uint16_t *Ko, int64_t ko_stride, hipStream_t stream);
+
+/*
+ * qk_norm_rope_append_f16 -- the same, with the keys (rounded to fp16) and the
+ * values V written to the cache's slots: bit for bit what qk_norm_rope_f16 and
+ * kv_cache_append leave there, in one pass. slots as for kv_cache_append.
+ */
+int qk_norm_rope_append_f16(const uint16_t *Q, int64_t q_stride, const uint16_t *K, int64_t k_stride,
+                            const uint16_t *V, int64_t v_stride, int64_t n, int64_t q_heads,
+                            const bsp_rotation *rotation, const bsp_kv_cache *cache, const int64_t *slots,
+                            uint16_t *Qo, int64_t qo_stride, hipStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Hidden states quantised token by token, with the residual sum and the norm
+ * before it, for spmm_bitmap_w4a4_dq (packed int4) and gemm_w8a8_dq (int8).
+ *   h = fp16(x + residual) (or x), y = h * weight (or h), m = max_k |y_k|, L = 127 or 7
+ *   code_k = round-half-even(y_k * L / m), of the exact quotient (0 where m = 0)
+ *   scale  = m / sqrt(mean(h^2) + eps) / L with a weight, m / L without, fp32
+ *   x16    = fp16(y / sqrt(mean(h^2) + eps)), what the codes stand for unquantised
+ *            (the adapters' activations)
+ *   A token with an infinity or a NaN in y gets codes 0 and scale NaN.
+ * --------------------------------------------------------------------------- */
+typedef struct bsp_tokens {
+    int64_t n, K;                /* n * K < 2^40, K < 2^25 */
+    const uint16_t *X;           /* DEVICE fp16 [n][K], token t at element t * x_stride */
+    int64_t x_stride;
+    const uint16_t *residual;    /* DEVICE fp16, or NULL */
+    int64_t residual_stride;
+    const uint16_t *weight;      /* DEVICE fp16 [K], or NULL: no norm */
+    float eps;                   /* finite, >= 0 */
+    uint16_t *hidden;            /* DEVICE fp16, h; required with a residual (may be X or residual, with its
+                                    stride), NULL without */
+    int64_t hidden_stride;
+    uint16_t *x16;               /* DEVICE fp16, or NULL */
+    int64_t x16_stride;
+    float *scale;                /* DEVICE [n] */
+} bsp_tokens;
+
+/*
+ * quantize_tokens_f16 -- asynchronous on `stream`.
+ *   tokens       HOST descriptor (read during the call only).
+ *   dtype        BSP_INT8: codes int8, token t at byte t * code_stride; BSP_INT4: packed as
+ *                pack_int4_activations does (an odd K leaves the last high nibble zero).
+ *   codes        DEVICE; code_stride >= K (int8) or ceil(K / 2) (int4). Bytes between a
+ *                token's codes and the next multiple of 16 inside the stride are zeroed (int8).
+ */
+int quantize_tokens_f16(const bsp_tokens *tokens, int dtype, uint8_t *codes, int64_t code_stride, hipStream_t stream);
+
+/*
+ * dequantize_tokens_f16 -- the values the codes stand for, fp16(scale[t] * code), into
+ * X fp16 [n][K] with token stride x_stride.
+ */
+int dequantize_tokens_f16(const uint8_t *codes, int64_t code_stride, int dtype, const float *scale, int64_t n,
+                          int64_t K, uint16_t *X, int64_t x_stride, hipStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Dense 8-bit product, for layers left unpruned and for prompts (any N):
+ *   Y[n][m] = fp16(fp32(sum_k W[m][k] X[n][k]) * scale_w[m] * scale_x[n])
+ * with int32 sums (exact: K <= BSP_W8_MAX_K). W is laid out once on the host in
+ * the order the matrix instruction takes it: tiles of 16 rows x 64 columns, row band
+ * by row band, 1 KiB each, 16-byte piece l of a tile holding row l % 16, columns
+ * 16 (l / 16) ..; zeros past M and K.
+ * --------------------------------------------------------------------------- */
+#define BSP_W8_MAX_K 131071
+
+/* Bytes of the laid-out form: ceil(M/16) * ceil(K/64) * 1024; -1 for negative sizes. */
+int64_t int8_tiles_bytes(int64_t M, int64_t K);
+
+/*
+ * encode_int8_tiles -- W HOST int8 [M][ldw] -> tiles HOST (int8_tiles_bytes bytes).
+ */
+int encode_int8_tiles(const int8_t *W, int64_t M, int64_t K, int64_t ldw, uint8_t *tiles);
+
+/* Bytes of workspace gemm_w8a8_dq uses to split K over workgroups (0: none). Host only. */
+int gemm_w8a8_workspace_bytes(int64_t M, int64_t K, int64_t N, int64_t *bytes);
+
+/*
+ * gemm_w8a8_dq -- asynchronous on `stream`.
+ *   tiles        DEVICE, 16-byte aligned, as encode_int8_tiles wrote them.
+ *   X            DEVICE int8, token n at byte n * x_stride, 16-byte aligned; x_stride a multiple of
+ *                16, >= K. All N * x_stride bytes are readable; what lies past K is not used.
+ *   scale_w, scale_x   DEVICE fp32 [M], [N].
+ *   Y            DEVICE fp16 [N][M], row n at element n * y_stride >= M. Must not overlap X.
+ *   workspace    DEVICE, NULL (K not split over workgroups) or gemm_w8a8_workspace_bytes()
+ *                bytes, 256-byte aligned, zero-filled before its first use (its first 64 KiB hold
+ *                arrival counters, left zero by every call: a workspace of the other entry points
+ *                will do). Too small: BSP_E_CAPACITY. Calls that share one must be ordered.
+ * K > BSP_W8_MAX_K, M >= 2^31, N >= 2^31: BSP_E_OVERFLOW. K == 0 gives zeros. The result does not
+ * depend on timing or on the workspace.
+ */
+int gemm_w8a8_dq(const uint8_t *tiles, int64_t M, int64_t K, const int8_t *X, int64_t x_stride, int64_t N,
+                 const float *scale_w, const float *scale_x, uint16_t *Y, int64_t y_stride, void *workspace,
+                 int64_t workspace_bytes, hipStream_t stream);
+
 /* Static string for a bsp_status code. */
 const char *bsp_status_string(int status);
 
