@@ -2,10 +2,12 @@
 //
 // v_mfma_i32_16x16x64_i8: a lane brings 16 bytes of one row of W (its tile in memory is
 // in lane order) and 16 bytes of one token, and holds 4 neighbouring channels of
-// one token of the result. Sums are int32 and exact.
+// one token of the result. Sums are int32 and exact, so the order in which parts of K
+// meet changes nothing.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "bitmap_spmm.h"
 #include "device_common.h"
@@ -13,6 +15,10 @@
 namespace {
 
 typedef int w8_i4 __attribute__((ext_vector_type(4)));
+typedef uint32_t w8_u2 __attribute__((ext_vector_type(2)));
+typedef float w8_f4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) void w8_lds_void;
+typedef __attribute__((address_space(3))) const w8_i4 w8_lds_i4;
 
 struct W8Args {
     const uint8_t *tiles;
@@ -23,29 +29,415 @@ struct W8Args {
     int64_t ys, n;
     int M, bands, ktiles;
     int last;                // last 16-byte piece of a token's row, as a byte offset
+    uint32_t mtiles, ntiles; // tiles of the result
+    bool wide;               // 8-byte stores: Y and its rows lie on that boundary
 };
 
-// One wavefront: 16 channels x 16 tokens over all of K.
-__global__ __launch_bounds__(256) void k_w8_plain(const W8Args a) {
-    const int lane = threadIdx.x & 63, band = blockIdx.x * 4 + (threadIdx.x >> 6);
-    if (band >= a.bands) return;
-    const int64_t n = (int64_t)blockIdx.y * 16 + (lane & 15);
-    const uint8_t *w = a.tiles + ((int64_t)band * a.ktiles << 10) + lane * 16;
-    const int8_t *x = a.x + min(n, a.n - 1) * a.xs;
-    w8_i4 acc = {0, 0, 0, 0};
-    for (int t = 0; t < a.ktiles; ++t) {
-        const w8_i4 A = *reinterpret_cast<const w8_i4 *>(w + ((int64_t)t << 10));
-        // past the row's last piece W is zero: any value will do
-        const w8_i4 B = *reinterpret_cast<const w8_i4 *>(x + min(t * 64 + (lane >> 4) * 16, a.last));
-        acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(A, B, acc, 0, 0, 0);
-    }
-    if (n >= a.n) return;
+// 4 neighbouring channels m .. m + 3 of token n.
+__device__ __forceinline__ void w8_store(const W8Args &a, int64_t n, int m, w8_i4 v) {
+    if (n >= a.n || m >= a.M) return;
     const float sx = a.scale_x[n];
+    uint16_t *y = a.y + n * a.ys + m;
+    if (a.wide && m + 3 < a.M) {
+        uint16_t h[4];
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-        const int m = band * 16 + (lane >> 4) * 4 + r;
-        if (m < a.M) a.y[n * a.ys + m] = bsp_f2h(bsp_rounded((float)acc[r] * a.scale_w[m] * sx));
+        for (int r = 0; r < 4; ++r) h[r] = bsp_f2h(bsp_rounded((float)v[r] * a.scale_w[m + r] * sx));
+        *reinterpret_cast<w8_u2 *>(y) = w8_u2{h[0] | ((uint32_t)h[1] << 16), h[2] | ((uint32_t)h[3] << 16)};
+    } else {
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            if (m + r < a.M) y[r] = bsp_f2h(bsp_rounded((float)v[r] * a.scale_w[m + r] * sx));
     }
+}
+
+// The workgroup's tile. Consecutive workgroups go to the 8 dies in turn: where W is read more than once each
+// die is given a run of neighbouring tiles, `deep` rows of tiles at a time, so that it reads few bands and tokens at
+// once. (m = mtiles: none, the grid is a multiple of 8.)
+struct W8Tile {
+    uint32_t m, n;
+};
+
+__device__ __forceinline__ W8Tile w8_tile(const W8Args &a, uint32_t deep) {
+    if (a.ntiles == 1) return W8Tile{min(blockIdx.x, a.mtiles), 0};
+    const uint32_t total = a.mtiles * a.ntiles, per = (total + 7) / 8;
+    const uint32_t tile = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
+    if (tile >= total) return W8Tile{a.mtiles, 0};
+    const uint32_t strip = tile / (deep * a.ntiles), rest = tile - strip * (deep * a.ntiles);
+    const uint32_t rows = min(deep, a.mtiles - strip * deep);
+    return W8Tile{strip * deep + rest % rows, rest / rows};
+}
+
+// ---- few tokens: W streams from memory straight into registers ----
+
+// A workgroup owns MB bands of 16 channels and NB blocks of 16 tokens; its W wavefronts
+// take every W-th column tile of K and meet in LDS.
+template <int NB, int MB, int W, int U>
+__global__ __launch_bounds__(64 * W) void k_w8_stream(const W8Args a) {
+    __shared__ int32_t sums[MB * NB * 256];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const W8Tile tile = w8_tile(a, 1);
+    if (tile.m >= a.mtiles) return;
+    const int band = (int)tile.m * MB;
+    const int64_t n0 = (int64_t)tile.n * (NB * 16);
+    const uint8_t *w[MB];
+#pragma unroll
+    for (int i = 0; i < MB; ++i) w[i] = a.tiles + ((int64_t)min(band + i, a.bands - 1) * a.ktiles << 10) + lane * 16;
+    const int8_t *x[NB];
+#pragma unroll
+    for (int j = 0; j < NB; ++j) x[j] = a.x + min(n0 + j * 16 + (lane & 15), a.n - 1) * a.xs;
+    const int piece = (lane >> 4) * 16;
+    w8_i4 acc[MB][NB];
+#pragma unroll
+    for (int i = 0; i < MB; ++i)
+#pragma unroll
+        for (int j = 0; j < NB; ++j) acc[i][j] = w8_i4{0, 0, 0, 0};
+    for (int i = threadIdx.x; i < MB * NB * 256; i += 64 * W) sums[i] = 0;
+    auto step = [&](int t, auto count) {
+        constexpr int C = decltype(count)::value;
+        w8_i4 A[C][MB], B[C][NB];
+#pragma unroll
+        for (int u = 0; u < C; ++u) {
+            const int k = t + u * W;
+#pragma unroll
+            for (int i = 0; i < MB; ++i) A[u][i] = __builtin_nontemporal_load(reinterpret_cast<const w8_i4 *>(w[i] + ((int64_t)k << 10)));
+#pragma unroll
+            for (int j = 0; j < NB; ++j)     // past the row's last piece W is zero: any value will do
+                B[u][j] = *reinterpret_cast<const w8_i4 *>(x[j] + min(k * 64 + piece, a.last));
+        }
+#pragma unroll
+        for (int u = 0; u < C; ++u)
+#pragma unroll
+            for (int i = 0; i < MB; ++i)
+#pragma unroll
+                for (int j = 0; j < NB; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(A[u][i], B[u][j], acc[i][j], 0, 0, 0);
+    };
+    int t = wave;
+    for (; t + (U - 1) * W < a.ktiles; t += U * W) step(t, std::integral_constant<int, U>{});
+    for (; t < a.ktiles; t += W) step(t, std::integral_constant<int, 1>{});
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < MB; ++i)
+#pragma unroll
+        for (int j = 0; j < NB; ++j)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) atomicAdd(&sums[((i * NB + j) * 4 + r) * 64 + lane], acc[i][j][r]);
+    __syncthreads();
+    for (int f = wave; f < MB * NB; f += W) {
+        w8_i4 v;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) v[r] = sums[(f * 4 + r) * 64 + lane];
+        if (band + f / NB < a.bands)
+            w8_store(a, n0 + f % NB * 16 + (lane & 15), (band + f / NB) * 16 + (lane >> 4) * 4, v);
+    }
+}
+
+// ---- many tokens: both operands through LDS ----
+
+__device__ __forceinline__ void w8_barrier() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+// Waits until at most N pieces of this wavefront are on their way, and its reads of LDS are done.
+template <int N>
+__device__ __forceinline__ void w8_wait_vm() {
+    static_assert(N >= 0 && N < 64, "the counter's range");
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4));
+    asm volatile("" ::: "memory");
+}
+
+// 1 KB from [base, base + bytes) to LDS, 16 bytes a lane from off + more; nothing is read past the end.
+__device__ __forceinline__ void w8_dma(const void *base, uint32_t bytes, uint32_t dst, uint32_t off, uint32_t more) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(bsp_rsrc(base, bytes), (w8_lds_void *)(uintptr_t)dst, 16, off, more, 0, 0);
+}
+
+// Few tokens, through LDS: as k_w8_stream, each wavefront with a ring of P stages of its own (MB bands and NB
+// blocks of tokens, 64 columns), which it alone fills and reads.
+template <int NB, int MB, int W, int P>
+__global__ __launch_bounds__(64 * W) void k_w8_ring(const W8Args a) {
+    constexpr uint32_t STAGE = (MB + NB) * 1024u;
+    extern __shared__ uint8_t w8_lds[];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const W8Tile tile = w8_tile(a, 1);
+    if (tile.m >= a.mtiles) return;
+    const int band = (int)tile.m * MB, nb = min(MB, a.bands - band);
+    const int64_t n0 = (int64_t)tile.n * (NB * 16);
+    const int ntok = (int)min((int64_t)(NB * 16), a.n - n0);
+    const uint8_t *wbase = a.tiles + ((int64_t)band * a.ktiles << 10);
+    const int8_t *xbase = a.x + n0 * a.xs;
+    const uint32_t wbytes = (uint32_t)nb * (uint32_t)a.ktiles << 10, xbytes = (uint32_t)ntok * (uint32_t)a.xs;
+    const uint32_t lds = (uint32_t)(uintptr_t)(w8_lds_void *)w8_lds + wave * (P * STAGE);
+    uint32_t off[MB + NB];
+#pragma unroll
+    for (int c = 0; c < MB + NB; ++c)
+        off[c] = c < MB ? ((uint32_t)min(c, nb - 1) * (uint32_t)a.ktiles << 10) + lane * 16
+                        : (uint32_t)min((c - MB) * 16 + (lane >> 2), ntok - 1) * (uint32_t)a.xs +
+                              (((lane & 3) ^ (-(lane >> 4) & 3)) << 4);
+    auto fetch = [&](int t, uint32_t slot) {
+        const uint32_t k = (uint32_t)min(t, a.ktiles - 1);
+#pragma unroll
+        for (int c = 0; c < MB + NB; ++c) {
+            const uint32_t dst = lds + slot * STAGE + c * 1024u;
+            if (c < MB)
+                w8_dma(wbase, wbytes, dst, off[c], k << 10);
+            else
+                w8_dma(xbase, xbytes, dst, off[c], k << 6);
+        }
+    };
+    const uint32_t abase = lds + lane * 16, brow = lane & 15,
+                   bbase = lds + MB * 1024u + (brow * 4 + ((lane >> 4) ^ (-(brow >> 2) & 3))) * 16;
+    w8_i4 acc[MB][NB];
+#pragma unroll
+    for (int i = 0; i < MB; ++i)
+#pragma unroll
+        for (int j = 0; j < NB; ++j) acc[i][j] = w8_i4{0, 0, 0, 0};
+    uint32_t fill = 0, use = 0;
+#pragma unroll
+    for (int s = 0; s < P - 1; ++s) {
+        fetch(wave + s * W, fill);
+        fill = fill + 1 == P ? 0 : fill + 1;
+    }
+    for (int t = wave; t < a.ktiles; t += W) {
+        w8_wait_vm<(P - 2) * (MB + NB)>();
+        w8_i4 A[MB], B[NB];
+#pragma unroll
+        for (int i = 0; i < MB; ++i) A[i] = *(w8_lds_i4 *)(uintptr_t)(abase + use * STAGE + i * 1024u);
+#pragma unroll
+        for (int j = 0; j < NB; ++j) B[j] = *(w8_lds_i4 *)(uintptr_t)(bbase + use * STAGE + j * 1024u);
+        use = use + 1 == P ? 0 : use + 1;
+        fetch(t + (P - 1) * W, fill);
+        fill = fill + 1 == P ? 0 : fill + 1;
+#pragma unroll
+        for (int i = 0; i < MB; ++i)
+#pragma unroll
+            for (int j = 0; j < NB; ++j)
+                acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(A[i], B[j], acc[i][j], 0, 0, 0);
+    }
+    w8_wait_vm<0>();
+    __syncthreads();
+    int32_t *sums = reinterpret_cast<int32_t *>(w8_lds);
+    for (int i = threadIdx.x; i < MB * NB * 256; i += 64 * W) sums[i] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < MB; ++i)
+#pragma unroll
+        for (int j = 0; j < NB; ++j)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) atomicAdd(&sums[((i * NB + j) * 4 + r) * 64 + lane], acc[i][j][r]);
+    __syncthreads();
+    for (int f = wave; f < MB * NB; f += W) {
+        w8_i4 v;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) v[r] = sums[(f * 4 + r) * 64 + lane];
+        if (band + f / NB < a.bands)
+            w8_store(a, n0 + f % NB * 16 + (lane & 15), (band + f / NB) * 16 + (lane >> 4) * 4, v);
+    }
+}
+
+// A workgroup's result is (WM TM 16) channels x (WN TN 16) tokens; a wavefront's TM x TN
+// blocks of 16 x 16. Stages of KS x 64 columns of K pass through a ring of R in LDS.
+template <int WM, int WN, int TM, int TN, int KS, int R>
+__global__ __launch_bounds__(64 * WM * WN) void k_w8_tiles(const W8Args a) {
+    constexpr int W = WM * WN, MBANDS = WM * TM, NBLOCKS = WN * TN, CHUNKS = MBANDS + NBLOCKS, CW = CHUNKS / W;
+    static_assert(CHUNKS % W == 0, "every wavefront moves as many pieces");
+    static_assert(KS == 1 || KS % 2 == 0, "the operands' two sets of registers change places");
+    constexpr uint32_t STEP = CHUNKS * 1024u, STAGE = KS * STEP;
+    extern __shared__ uint8_t w8_lds[];
+    const uint32_t lds = (uint32_t)(uintptr_t)(w8_lds_void *)w8_lds;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const W8Tile tile = w8_tile(a, 8);
+    if (tile.m >= a.mtiles) return;
+    const int band0 = (int)tile.m * MBANDS;
+    const int64_t n0 = (int64_t)tile.n * (NBLOCKS * 16);
+    const int ntok = (int)min((int64_t)(NBLOCKS * 16), a.n - n0);
+    const int nb = min(MBANDS, a.bands - band0);
+    const uint8_t *wbase = a.tiles + ((int64_t)band0 * a.ktiles << 10);
+    const int8_t *xbase = a.x + n0 * a.xs;
+    const uint32_t wbytes = (uint32_t)nb * (uint32_t)a.ktiles << 10, xbytes = (uint32_t)ntok * (uint32_t)a.xs;
+    // the pieces of 1 KB this wavefront moves for each 64 columns: chunks wave, wave + W, ...
+    uint32_t off[CW];
+#pragma unroll
+    for (int c = 0; c < CW; ++c) {
+        const int chunk = wave + c * W;
+        if (chunk < MBANDS) {
+            off[c] = ((uint32_t)min(chunk, nb - 1) * (uint32_t)a.ktiles << 10) + lane * 16;
+        } else {
+            // lane l brings piece (l % 4) ^ (-(l / 16) % 4) of token l / 4: 64 bytes a token together, and the
+            // lanes that read LDS in the same cycle on different banks
+            const int row = min((chunk - MBANDS) * 16 + (lane >> 2), ntok - 1);
+            off[c] = (uint32_t)row * (uint32_t)a.xs + (((lane & 3) ^ (-(lane >> 4) & 3)) << 4);
+        }
+    }
+    auto fetch = [&](int t, uint32_t slot) {
+#pragma unroll
+        for (int q = 0; q < KS; ++q) {
+            const uint32_t k = (uint32_t)min(t * KS + q, a.ktiles - 1);
+#pragma unroll
+            for (int c = 0; c < CW; ++c) {
+                const int chunk = wave + c * W;
+                const uint32_t dst = lds + slot * STAGE + q * STEP + (uint32_t)chunk * 1024u;
+                if (chunk < MBANDS)
+                    w8_dma(wbase, wbytes, dst, off[c], k << 10);
+                else
+                    w8_dma(xbase, xbytes, dst, off[c], k << 6);
+            }
+        }
+    };
+    const int wm = wave / WN, wn = wave % WN;
+    const uint32_t abase = lds + (uint32_t)(wm * TM) * 1024u + lane * 16;
+    const uint32_t brow = lane & 15, bbase = lds + (uint32_t)(MBANDS + wn * TN) * 1024u +
+                                            (brow * 4 + ((lane >> 4) ^ (-(brow >> 2) & 3))) * 16;
+    w8_i4 acc[TM][TN];
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j) acc[i][j] = w8_i4{0, 0, 0, 0};
+    // The operands of 64 columns are in registers when their turn comes: the next ones are read from
+    // LDS under their matrix instructions, and at the last ones of stage t stage t + R takes its place.
+    w8_i4 A[2][TM], B[2][TN];
+    uint32_t slot = 0;
+    auto read = [&](uint32_t at, w8_i4 (&x)[TM], w8_i4 (&y)[TN]) {
+#pragma unroll
+        for (int j = 0; j < TN; ++j) y[j] = *(w8_lds_i4 *)(uintptr_t)(bbase + at + j * 1024u);
+#pragma unroll
+        for (int i = 0; i < TM; ++i) x[i] = *(w8_lds_i4 *)(uintptr_t)(abase + at + i * 1024u);
+    };
+    auto multiply = [&](w8_i4 (&x)[TM], w8_i4 (&y)[TN], auto pieces) {
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+            for (int j = 0; j < TN; ++j)
+                acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(x[i], y[j], acc[i][j], 0, 0, 0);
+        // reads and pieces spread over the matrix instructions
+        constexpr int READS = TM + TN, VM = decltype(pieces)::value, PER = TM * TN / (READS + VM) > 0 ? TM * TN / (READS + VM) : 1;
+#pragma unroll
+        for (int c = 0; c < READS; ++c) {
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x8, PER, 0);
+        }
+#pragma unroll
+        for (int c = 0; c < VM; ++c) {
+            __builtin_amdgcn_sched_group_barrier(0x20, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x8, PER, 0);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    auto turn = [&](int t, w8_i4 (&x)[TM], w8_i4 (&y)[TN], w8_i4 (&x1)[TM], w8_i4 (&y1)[TN]) {
+#pragma unroll
+        for (int q = 0; q + 1 < KS; ++q) {
+            const bool odd = q & 1;
+            read(slot * STAGE + (q + 1) * STEP, odd ? x : x1, odd ? y : y1);
+            if (q == 0 || t * KS + q < a.ktiles) multiply(odd ? x1 : x, odd ? y1 : y, std::integral_constant<int, 0>{});
+        }
+        w8_wait_vm<(R - 2) * CW * KS>();      // this wavefront's pieces of stage t + 1, and its reads of stage t
+        w8_barrier();                         // every wavefront's
+        fetch(t + R, slot);
+        slot = slot + 1 == R ? 0 : slot + 1;
+        constexpr bool last = KS > 1;         // (KS even: the last operands lie in the second set, the next in the first)
+        read(slot * STAGE, last ? x : x1, last ? y : y1);
+        if (KS == 1 || t * KS + KS - 1 < a.ktiles) multiply(last ? x1 : x, last ? y1 : y, std::integral_constant<int, CW * KS>{});
+    };
+#pragma unroll
+    for (int s = 0; s < R; ++s) fetch(s, s);
+    w8_wait_vm<(R - 1) * CW * KS>();
+    w8_barrier();
+    read(0, A[0], B[0]);
+    int t = 0;
+    if constexpr (KS > 1) {
+        for (; t * KS < a.ktiles; ++t) turn(t, A[0], B[0], A[1], B[1]);
+    } else {
+        for (; t + 1 < a.ktiles; t += 2) {
+            turn(t, A[0], B[0], A[1], B[1]);
+            turn(t + 1, A[1], B[1], A[0], B[0]);
+        }
+        if (t < a.ktiles) turn(t, A[0], B[0], A[1], B[1]);
+    }
+    w8_wait_vm<0>();
+    const int m0 = (band0 + wm * TM) * 16 + (lane >> 4) * 4;
+    const int64_t n1 = n0 + wn * TN * 16 + (lane & 15);
+    if (a.wide && (band0 + MBANDS) * 16 <= a.M && ntok == NBLOCKS * 16) {
+        float sx[TN];
+#pragma unroll
+        for (int j = 0; j < TN; ++j) sx[j] = a.scale_x[n1 + j * 16];
+#pragma unroll
+        for (int i = 0; i < TM; ++i) {
+            w8_f4 sw;
+            __builtin_memcpy(&sw, a.scale_w + m0 + i * 16, 16);
+#pragma unroll
+            for (int j = 0; j < TN; ++j) {
+                uint16_t h[4];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) h[r] = bsp_f2h(bsp_rounded((float)acc[i][j][r] * sw[r] * sx[j]));
+                *reinterpret_cast<w8_u2 *>(a.y + (n1 + j * 16) * a.ys + m0 + i * 16) =
+                    w8_u2{h[0] | ((uint32_t)h[1] << 16), h[2] | ((uint32_t)h[3] << 16)};
+            }
+        }
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < TN; ++j)
+#pragma unroll
+        for (int i = 0; i < TM; ++i) w8_store(a, n1 + j * 16, m0 + i * 16, acc[i][j]);
+}
+
+// Launches are for a grid of whole eights (w8_tile).
+unsigned w8_grid(W8Args &a, int bands, int blocks) {
+    a.mtiles = (uint32_t)((a.bands + bands - 1) / bands), a.ntiles = (uint32_t)((a.n + blocks * 16 - 1) / (blocks * 16));
+    return (a.mtiles * a.ntiles + 7) / 8 * 8;
+}
+
+template <int W, int U>
+void w8_stream(W8Args &a, hipStream_t stream) {
+    const unsigned grid = w8_grid(a, 1, 1);
+    hipLaunchKernelGGL((k_w8_stream<1, 1, W, U>), dim3(grid), dim3(64 * W), 0, stream, a);
+}
+
+template <int NB, int MB, int W, int P>
+void w8_ring(W8Args &a, hipStream_t stream) {
+    constexpr unsigned LDS = (MB + NB) * 1024u * P * W;
+    const unsigned grid = w8_grid(a, MB, NB);
+    (void)hipFuncSetAttribute((const void *)k_w8_ring<NB, MB, W, P>, hipFuncAttributeMaxDynamicSharedMemorySize, (int)LDS);
+    hipLaunchKernelGGL((k_w8_ring<NB, MB, W, P>), dim3(grid), dim3(64 * W), LDS, stream, a);
+}
+
+template <int WM, int WN, int TM, int TN, int KS, int R>
+void w8_tiles(W8Args &a, hipStream_t stream) {
+    constexpr unsigned LDS = (WM * TM + WN * TN) * 1024u * KS * R;
+    const unsigned grid = w8_grid(a, WM * TM, WN * TN);
+    (void)hipFuncSetAttribute((const void *)k_w8_tiles<WM, WN, TM, TN, KS, R>, hipFuncAttributeMaxDynamicSharedMemorySize, (int)LDS);
+    hipLaunchKernelGGL((k_w8_tiles<WM, WN, TM, TN, KS, R>), dim3(grid), dim3(64 * WM * WN), LDS, stream, a);
+}
+
+struct W8Plan {
+    int bands, blocks;       // a workgroup's tile, in 16s
+    void (*run)(W8Args &, hipStream_t);
+};
+
+// By the shape of the tile alone. The first five split K over their wavefronts, the others the tile.
+const W8Plan W8_PLANS[] = {
+    {1, 1, w8_ring<1, 1, 8, 4>}, {1, 2, w8_ring<2, 1, 8, 3>}, {2, 2, w8_ring<2, 2, 8, 4>}, {1, 4, w8_ring<4, 1, 4, 4>},
+    {2, 4, w8_ring<4, 2, 8, 3>}, {4, 4, w8_tiles<2, 2, 2, 2, 4, 3>}, {8, 4, w8_tiles<2, 2, 4, 2, 2, 3>},
+    {8, 8, w8_tiles<2, 4, 4, 2, 1, 4>}, {16, 8, w8_tiles<2, 4, 8, 2, 1, 4>}, {16, 16, w8_tiles<2, 4, 8, 4, 1, 4>},
+};
+
+// A tile's time is that of its operands' way into the CU (a KB of them every 1 / 57 us, whatever the
+// tile) or of its matrix instructions (a 16 x 16 x 64 block every 1 / 330 us), whichever is longer; the tiles of
+// a CU come one after the other.
+void (*w8_plan(int64_t bands, int64_t ktiles, int64_t n))(W8Args &, hipStream_t) {
+    if (n <= 4 && bands * ktiles >= 32768) return bands > 512 && ktiles < 128 ? w8_stream<8, 4> : w8_stream<16, 2>;
+    if (n <= 16 && bands > 256) return w8_ring<1, 1, 4, 4>;
+    const W8Plan *best = nullptr;
+    double least = 0.0;
+    for (const W8Plan &p : W8_PLANS) {
+        const int64_t tiles = (bands + p.bands - 1) / p.bands * ((n + p.blocks * 16 - 1) / (p.blocks * 16));
+        const double one = std::max((p.bands + p.blocks) / 57.0, p.bands * p.blocks / 330.0);
+        const double t = (double)((tiles + 255) / 256) * one;
+        if (best == nullptr || t < least) best = &p, least = t;
+    }
+    return best->run;
 }
 
 }  // namespace
@@ -72,7 +464,7 @@ extern "C" int gemm_w8a8_dq(const uint8_t *tiles, int64_t M, int64_t K, const in
     a.tiles = tiles, a.x = X, a.xs = x_stride, a.scale_w = scale_w, a.scale_x = scale_x, a.y = Y, a.ys = y_stride;
     a.n = N, a.M = (int)M, a.bands = (int)((M + 15) / 16), a.ktiles = (int)((K + 63) / 64);
     a.last = (int)std::max<int64_t>(x_stride - 16, 0);
-    hipLaunchKernelGGL(k_w8_plain, dim3((unsigned)((a.bands + 3) / 4), (unsigned)((N + 15) / 16)), dim3(256), 0, stream,
-                       a);
+    a.wide = ((uintptr_t)Y & 7u) == 0 && y_stride % 4 == 0;
+    w8_plan(a.bands, a.ktiles, N)(a, stream);
     return hipGetLastError() == hipSuccess ? BSP_OK : BSP_E_HIP;
 }
