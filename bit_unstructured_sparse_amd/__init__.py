@@ -16,6 +16,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from dataclasses import dataclass
 from typing import NamedTuple, Optional
 
@@ -738,9 +739,9 @@ def _rows(t, name, n, heads, dim, index) -> int:
     if isinstance(t, torch.Tensor) and t.dtype is torch.float16 and t.get_device() == index and t.dim() == 3:
         m, h, d = t.shape
         if h == heads and d == dim and (n is None or m == n):
-            s0, s1, s2 = t.stride()
             if t.is_contiguous():
                 return width
+            s0, s1, s2 = t.stride()
             if s2 == 1 and (heads == 1 or s1 == dim):
                 if m <= 1:
                     return width
@@ -1106,26 +1107,26 @@ def kv_step(pages: KVPages, keep, new_tokens, rows: int, tree_mask=None, out: Op
     index, B = pages._index, pages.sequences
     i32 = torch.int32
     if out is None:
-        shapes = ((rows, torch.int64), (rows, i32), (rows, i32), (B + 1, i32), (B, i32))
-        out = KVStep(*(_new_output((n,), t, pages.device, stream) for n, t in shapes))
+        dev = pages.device
+        out = KVStep(_new_output((rows,), torch.int64, dev, stream), _new_output((rows,), i32, dev, stream),
+                     _new_output((rows,), i32, dev, stream), _new_output((B + 1,), i32, dev, stream),
+                     _new_output((B,), i32, dev, stream))
+    slots, positions, sequences, q_start, kv_lens = out
     rc = _launch(
         load_library().kv_pages_step, index, stream, pages._ref,
         None if keep is None else _flat(keep, "keep", i32, B, index), _flat(new_tokens, "new_tokens", i32, B, index),
         None if tree_mask is None else _flat(tree_mask, "tree_mask", torch.int64, rows, index), rows,
-        _flat(out.slots, "slots", torch.int64, rows, index), _flat(out.positions, "positions", i32, rows, index),
-        _flat(out.sequences, "sequences", i32, rows, index), _flat(out.q_start, "q_start", i32, B + 1, index),
-        _flat(out.kv_lens, "kv_lens", i32, B, index))
+        _flat(slots, "slots", torch.int64, rows, index), _flat(positions, "positions", i32, rows, index),
+        _flat(sequences, "sequences", i32, rows, index), _flat(q_start, "q_start", i32, B + 1, index),
+        _flat(kv_lens, "kv_lens", i32, B, index))
     _check(rc, "kv_pages_step")
     return out
 
 
 # ---- query and key heads normed, rotated, and written to the cache ----
 
-class _RotationDesc(ctypes.Structure):
-    """bsp_rotation of include/bitmap_spmm.h."""
-    _fields_ = [("rot", ctypes.c_int64), ("interleaved", ctypes.c_int), ("freq", ctypes.c_void_p),
-                ("positions", ctypes.c_void_p), ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p),
-                ("eps", ctypes.c_float)]
+# bsp_rotation of include/bitmap_spmm.h, packed: a call's descriptors are bytes (a ctypes structure takes three times as long)
+_ROTATION = struct.Struct("@qiPPPPf4x")
 
 
 def rope_frequencies(rot: int, base: float = 10000.0, angles=None, device="cuda"):
@@ -1145,15 +1146,17 @@ def rope_frequencies(rot: int, base: float = 10000.0, angles=None, device="cuda"
     return torch.from_numpy(words.view(np.int64)).to(device)
 
 
-def _rotation(positions, freq, q_weight, k_weight, eps, interleaved, n, dim, index) -> _RotationDesc:
+def _rotation(positions, freq, q_weight, k_weight, eps, interleaved, n, dim, index) -> bytes:
     import torch
-    rot = 0 if freq is None else 2 * freq.numel()
     f16 = torch.float16
-    return _RotationDesc(
-        rot, 1 if interleaved else 0, None if freq is None else _flat(freq, "freq", torch.int64, rot // 2, index),
-        None if freq is None else _flat(positions, "positions", torch.int32, n, index),
-        None if q_weight is None else _flat(q_weight, "q_weight", f16, dim, index),
-        None if k_weight is None else _flat(k_weight, "k_weight", f16, dim, index), eps)
+    rot = f = p = 0
+    if freq is not None:
+        rot = 2 * freq.numel()
+        f = _flat(freq, "freq", torch.int64, rot // 2, index)
+        p = _flat(positions, "positions", torch.int32, n, index)
+    return _ROTATION.pack(rot, 1 if interleaved else 0, f, p,
+                          0 if q_weight is None else _flat(q_weight, "q_weight", f16, dim, index),
+                          0 if k_weight is None else _flat(k_weight, "k_weight", f16, dim, index), eps)
 
 
 def _heads(t, name):
@@ -1174,13 +1177,16 @@ def qk_norm_rope(Q, K, positions, freq, q_weight=None, k_weight=None, eps: float
     index = Q.get_device()
     qs, ks = _rows(Q, "Q", n, hq, dim, index), _rows(K, "K", n, hkv, dim, index)
     if Qo is None:
-        Qo = _new_output((n, hq, dim), torch.float16, Q.device, stream)
+        Qo, qo = _new_output((n, hq, dim), torch.float16, Q.device, stream), hq * dim
+    else:
+        qo = _rows(Qo, "Qo", n, hq, dim, index)
     if Ko is None:
-        Ko = _new_output((n, hkv, dim), torch.float16, Q.device, stream)
-    qo, ko = _rows(Qo, "Qo", n, hq, dim, index), _rows(Ko, "Ko", n, hkv, dim, index)
+        Ko, ko = _new_output((n, hkv, dim), torch.float16, Q.device, stream), hkv * dim
+    else:
+        ko = _rows(Ko, "Ko", n, hkv, dim, index)
     d = _rotation(positions, freq, q_weight, k_weight, eps, interleaved, n, dim, index)
     rc = _launch(load_library().qk_norm_rope_f16, index, stream, Q.data_ptr(), qs, K.data_ptr(), ks, n, hq, hkv, dim,
-                 ctypes.byref(d), Qo.data_ptr(), qo, Ko.data_ptr(), ko)
+                 d, Qo.data_ptr(), qo, Ko.data_ptr(), ko)
     _check(rc, "qk_norm_rope_f16")
     return Qo, Ko
 
@@ -1194,11 +1200,12 @@ def qk_norm_rope_append(Q, K, V, positions, freq, cache: KVCache, slots, q_weigh
     hkv, dim, index = cache.kv_heads, cache.head_dim, cache._index
     qs, ks, vs = _rows(Q, "Q", n, hq, dim, index), _rows(K, "K", n, hkv, dim, index), _rows(V, "V", n, hkv, dim, index)
     if Qo is None:
-        Qo = _new_output((n, hq, dim), torch.float16, cache.device, stream)
-    qo = _rows(Qo, "Qo", n, hq, dim, index)
+        Qo, qo = _new_output((n, hq, dim), torch.float16, cache.device, stream), hq * dim
+    else:
+        qo = _rows(Qo, "Qo", n, hq, dim, index)
     d = _rotation(positions, freq, q_weight, k_weight, eps, interleaved, n, dim, index)
     rc = _launch(load_library().qk_norm_rope_append_f16, index, stream, Q.data_ptr(), qs, K.data_ptr(), ks,
-                 V.data_ptr(), vs, n, hq, ctypes.byref(d), cache._ref, _flat(slots, "slots", torch.int64, n, index),
+                 V.data_ptr(), vs, n, hq, d, cache._ref, _flat(slots, "slots", torch.int64, n, index),
                  Qo.data_ptr(), qo)
     _check(rc, "qk_norm_rope_append_f16")
     return Qo
@@ -1206,12 +1213,8 @@ def qk_norm_rope_append(Q, K, V, positions, freq, cache: KVCache, slots, q_weigh
 
 # ---- hidden states quantised token by token ----
 
-class _TokensDesc(ctypes.Structure):
-    """bsp_tokens of include/bitmap_spmm.h."""
-    _fields_ = [("n", ctypes.c_int64), ("K", ctypes.c_int64), ("X", ctypes.c_void_p), ("x_stride", ctypes.c_int64),
-                ("residual", ctypes.c_void_p), ("residual_stride", ctypes.c_int64), ("weight", ctypes.c_void_p),
-                ("eps", ctypes.c_float), ("hidden", ctypes.c_void_p), ("hidden_stride", ctypes.c_int64),
-                ("x16", ctypes.c_void_p), ("x16_stride", ctypes.c_int64), ("scale", ctypes.c_void_p)]
+# bsp_tokens of include/bitmap_spmm.h, packed
+_TOKENS = struct.Struct("@qqPqPqPf4xPqPqP")
 
 
 class Tokens(NamedTuple):
@@ -1227,12 +1230,14 @@ class Tokens(NamedTuple):
 def _matrix_rows(t, name, dtype, n, width, index) -> int:
     """Check an [n][width] tensor whose rows may be strided; returns the stride between rows."""
     import torch
-    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index and t.dim() == 2 and \
-            t.shape[0] == n and t.shape[1] == width:
+    # the common case in few steps; what is wrong is named below
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index and t.shape == (n, width):
+        if t.is_contiguous():
+            return width
         s0, s1 = t.stride()
         if s1 == 1 or width <= 1:
             if n <= 1:
-                return max(s0, width)
+                return width
             if s0 >= width:
                 return s0
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
@@ -1264,34 +1269,45 @@ def quantize_tokens(X, dtype: int, weight=None, eps: float = 1e-6, residual=None
     if X.dim() != 2 or not X.is_cuda:
         raise ValueError("X must be [n][K] on the device")
     n, K = X.shape
-    index, f16 = X.get_device(), torch.float16
-    if dtype not in (INT8, INT4):
-        raise ValueError("codes are INT8 or INT4")
+    index, f16, dev = X.get_device(), torch.float16, X.device
     xs = _matrix_rows(X, "X", f16, n, K, index)
-    if residual is None and hidden is not None:
+    if codes is None and dtype == INT8:
+        cs = (K + 15) // 16 * 16
+        codes = _new_output((n, cs), torch.int8, dev, stream)
+        cp = codes.data_ptr()
+        if cs != K:
+            codes = codes[:, :K]
+    elif codes is None and dtype == INT4:
+        cs = (K + 1) // 2
+        codes = _new_output((n, cs), torch.uint8, dev, stream)
+        cp = codes.data_ptr()
+    else:
+        cp, cs = _code_rows(codes, dtype, n, K, index)
+    if scale is None:
+        scale = _new_output((n,), torch.float32, dev, stream)
+        sp = scale.data_ptr()
+    else:
+        sp = _flat(scale, "scale", torch.float32, n, index)
+    r = rs = h = hs = x = x16s = 0
+    if residual is not None:
+        rs, hs = _matrix_rows(residual, "residual", f16, n, K, index), K
+        if hidden is None:
+            hidden = _new_output((n, K), f16, dev, stream)
+        else:
+            hs = _matrix_rows(hidden, "hidden", f16, n, K, index)
+        r, h = residual.data_ptr(), hidden.data_ptr()
+    elif hidden is not None:
         raise ValueError("hidden goes with residual")
-    if residual is not None and hidden is None:
-        hidden = _new_output((n, K), f16, X.device, stream)
     if x16 is True:
-        x16 = _new_output((n, K), f16, X.device, stream)
+        x16 = _new_output((n, K), f16, dev, stream)
     elif x16 is False:
         x16 = None
-    if codes is None:
-        if dtype == INT8:
-            codes = _new_output((n, (K + 15) // 16 * 16), torch.int8, X.device, stream)[:, :K]
-        else:
-            codes = _new_output((n, (K + 1) // 2), torch.uint8, X.device, stream)
-    if scale is None:
-        scale = _new_output((n,), torch.float32, X.device, stream)
-    cp, cs = _code_rows(codes, dtype, n, K, index)
-    d = _TokensDesc(
-        n, K, X.data_ptr(), xs, _dptr(residual),
-        0 if residual is None else _matrix_rows(residual, "residual", f16, n, K, index),
-        None if weight is None else _flat(weight, "weight", f16, K, index), eps, _dptr(hidden),
-        0 if hidden is None else _matrix_rows(hidden, "hidden", f16, n, K, index), _dptr(x16),
-        0 if x16 is None else _matrix_rows(x16, "x16", f16, n, K, index),
-        _flat(scale, "scale", torch.float32, n, index))
-    rc = _launch(load_library().quantize_tokens_f16, index, stream, ctypes.byref(d), dtype, cp, cs)
+    if x16 is not None:
+        x16s = _matrix_rows(x16, "x16", f16, n, K, index)
+        x = x16.data_ptr()
+    d = _TOKENS.pack(n, K, X.data_ptr(), xs, r, rs, 0 if weight is None else _flat(weight, "weight", f16, K, index), eps,
+                     h, hs, x, x16s, sp)
+    rc = _launch(load_library().quantize_tokens_f16, index, stream, d, dtype, cp, cs)
     _check(rc, "quantize_tokens_f16")
     return Tokens(codes, scale, x16, hidden)
 
@@ -1305,9 +1321,10 @@ def dequantize_tokens(codes, scale, dtype: int, K: int, X=None, stream=None):
     sp = _flat(scale, "scale", torch.float32, n, index)
     cp, cs = _code_rows(codes, dtype, n, K, index)
     if X is None:
-        X = _new_output((n, K), torch.float16, scale.device, stream)
-    rc = _launch(load_library().dequantize_tokens_f16, index, stream, cp, cs, dtype, sp, n, K, X.data_ptr(),
-                 _matrix_rows(X, "X", torch.float16, n, K, index))
+        X, xs = _new_output((n, K), torch.float16, scale.device, stream), K
+    else:
+        xs = _matrix_rows(X, "X", torch.float16, n, K, index)
+    rc = _launch(load_library().dequantize_tokens_f16, index, stream, cp, cs, dtype, sp, n, K, X.data_ptr(), xs)
     _check(rc, "dequantize_tokens_f16")
     return X
 
@@ -1339,7 +1356,16 @@ class DenseInt8:
     def __post_init__(self):
         import torch
         _check_dev(self.tiles, "tiles", torch.uint8, (self.M + 15) // 16 * ((self.K + 63) // 64) * 1024)
-        _flat(self.scale, "scale", torch.float32, self.M, self.tiles.get_device())
+        index = self.tiles.get_device()
+        _flat(self.scale, "scale", torch.float32, self.M, index)
+        object.__setattr__(self, "_index", index)
+        object.__setattr__(self, "_at", (self.tiles.data_ptr(), self.scale.data_ptr()))
+
+    def _pointers(self):
+        """Where the tensors lie; one given another storage is taken up, and checked, by the next call."""
+        if (self.tiles.data_ptr(), self.scale.data_ptr()) != self._at:
+            self.__post_init__()
+        return self._at
 
 
 def encode_int8(W: np.ndarray, scale: np.ndarray) -> EncodedInt8:
@@ -1379,18 +1405,19 @@ def gemm_w8a8(W: DenseInt8, X, scale_x, Y=None, workspace=None, stream=None):
     import torch
     if X.dim() != 2 or X.shape[1] != W.K:
         raise ValueError("X must be [N][K]")
-    N, index = X.shape[0], W.tiles.get_device()
-    xs = _matrix_rows(X, "X", torch.int8, N, W.K, index)
-    if N <= 1 or W.K == 0:
-        xs = (W.K + 15) // 16 * 16
-    if xs != W.K and N > 0 and X.untyped_storage().nbytes() < X.storage_offset() + N * xs:
+    tiles, scale_w = W._pointers()
+    N, M, K, index = X.shape[0], W.M, W.K, W._index
+    xs = _matrix_rows(X, "X", torch.int8, N, K, index)
+    if N <= 1 or K == 0:
+        xs = (K + 15) // 16 * 16
+    if xs != K and N > 0 and X.untyped_storage().nbytes() < X.storage_offset() + N * xs:
         raise ValueError("X: every row must be readable up to its stride")
     if Y is None:
-        Y = _new_output((N, W.M), torch.float16, X.device, stream)
-    ys = _matrix_rows(Y, "Y", torch.float16, N, W.M, index)
-    wp, wb = _ws_args(workspace, index)
-    rc = _launch(load_library().gemm_w8a8_dq, index, stream, W.tiles.data_ptr(), W.M, W.K, X.data_ptr(), xs, N,
-                 _flat(W.scale, "W.scale", torch.float32, W.M, index),
+        Y, ys = _new_output((N, M), torch.float16, X.device, stream), M
+    else:
+        ys = _matrix_rows(Y, "Y", torch.float16, N, M, index)
+    wp, wb = (None, 0) if workspace is None else _ws_args(workspace, index)
+    rc = _launch(load_library().gemm_w8a8_dq, index, stream, tiles, M, K, X.data_ptr(), xs, N, scale_w,
                  _flat(scale_x, "scale_x", torch.float32, N, index), Y.data_ptr(), ys, wp, wb)
     _check(rc, "gemm_w8a8_dq")
     return Y

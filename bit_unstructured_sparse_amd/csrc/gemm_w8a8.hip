@@ -7,6 +7,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <type_traits>
 
 #include "bitmap_spmm.h"
@@ -383,6 +384,17 @@ __global__ __launch_bounds__(64 * WM * WN) void k_w8_tiles(const W8Args a) {
         for (int i = 0; i < TM; ++i) w8_store(a, n1 + j * 16, m0 + i * 16, acc[i][j]);
 }
 
+// Allows a kernel its LDS, once for each device.
+template <class Kernel>
+void w8_allow(Kernel *kernel, unsigned lds, std::atomic<uint64_t> &done) {
+    int device = 0;
+    if (lds <= 65536 || hipGetDevice(&device) != hipSuccess) return;
+    const uint64_t bit = UINT64_C(1) << (device & 63);
+    if (device < 64 && (done.load(std::memory_order_relaxed) & bit) != 0) return;
+    if (hipFuncSetAttribute((const void *)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds) == hipSuccess)
+        done.fetch_or(bit, std::memory_order_relaxed);
+}
+
 // Launches are for a grid of whole eights (w8_tile).
 unsigned w8_grid(W8Args &a, int bands, int blocks) {
     a.mtiles = (uint32_t)((a.bands + bands - 1) / bands), a.ntiles = (uint32_t)((a.n + blocks * 16 - 1) / (blocks * 16));
@@ -399,7 +411,8 @@ template <int NB, int MB, int W, int P>
 void w8_ring(W8Args &a, hipStream_t stream) {
     constexpr unsigned LDS = (MB + NB) * 1024u * P * W;
     const unsigned grid = w8_grid(a, MB, NB);
-    (void)hipFuncSetAttribute((const void *)k_w8_ring<NB, MB, W, P>, hipFuncAttributeMaxDynamicSharedMemorySize, (int)LDS);
+    static std::atomic<uint64_t> done{0};
+    w8_allow(k_w8_ring<NB, MB, W, P>, LDS, done);
     hipLaunchKernelGGL((k_w8_ring<NB, MB, W, P>), dim3(grid), dim3(64 * W), LDS, stream, a);
 }
 
@@ -407,7 +420,8 @@ template <int WM, int WN, int TM, int TN, int KS, int R>
 void w8_tiles(W8Args &a, hipStream_t stream) {
     constexpr unsigned LDS = (WM * TM + WN * TN) * 1024u * KS * R;
     const unsigned grid = w8_grid(a, WM * TM, WN * TN);
-    (void)hipFuncSetAttribute((const void *)k_w8_tiles<WM, WN, TM, TN, KS, R>, hipFuncAttributeMaxDynamicSharedMemorySize, (int)LDS);
+    static std::atomic<uint64_t> done{0};
+    w8_allow(k_w8_tiles<WM, WN, TM, TN, KS, R>, LDS, done);
     hipLaunchKernelGGL((k_w8_tiles<WM, WN, TM, TN, KS, R>), dim3(grid), dim3(64 * WM * WN), LDS, stream, a);
 }
 

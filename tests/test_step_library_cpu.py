@@ -38,14 +38,14 @@ def test_pages():
 
 def _rotation(**kw):
     a = dict(dict(rot=64, interleaved=0, freq=FAKE, positions=FAKE, q_weight=None, k_weight=None, eps=1e-6), **kw)
-    return bsp._RotationDesc(*(a[n] for n, _ in bsp._RotationDesc._fields_))
+    return bsp._ROTATION.pack(*(a[n] or 0 for n in ("rot", "interleaved", "freq", "positions", "q_weight", "k_weight", "eps")))
 
 
 def test_heads():
     L = bsp.load_library()
 
     def call(none=False, Q=FAKE, qs=512, K=FAKE, ks=128, n=4, hq=8, hkv=2, D=64, Qo=FAKE, qos=512, Ko=FAKE, kos=128, **kw):
-        r = None if none else ctypes.byref(_rotation(**kw))
+        r = None if none else _rotation(**kw)
         return L.qk_norm_rope_f16(Q, qs, K, ks, n, hq, hkv, D, r, Qo, qos, Ko, kos, None)
 
     for bad in (dict(none=True), dict(n=-1), dict(hq=-1), dict(hkv=-1), dict(Q=None), dict(K=None), dict(Qo=None),
@@ -64,7 +64,7 @@ def test_heads_to_the_cache():
     L = bsp.load_library()
 
     def call(c=cache(), Q=FAKE, V=FAKE, vs=128, n=4, hq=8, slots=FAKE, none=False, **kw):
-        r = None if none else ctypes.byref(_rotation(**kw))
+        r = None if none else _rotation(**kw)
         return L.qk_norm_rope_append_f16(Q, 512, FAKE, 128, V, vs, n, hq, r, None if c is None else ctypes.byref(c), slots,
                                          FAKE, 512, None)
 
@@ -80,14 +80,14 @@ def test_heads_to_the_cache():
 def _tokens(**kw):
     a = dict(dict(n=3, K=64, X=FAKE, x_stride=64, residual=None, residual_stride=0, weight=None, eps=1e-6, hidden=None,
                   hidden_stride=0, x16=None, x16_stride=0, scale=FAKE), **kw)
-    return bsp._TokensDesc(*(a[n] for n, _ in bsp._TokensDesc._fields_))
+    return bsp._TOKENS.pack(*(v or 0 for v in a.values()))
 
 
 def test_tokens():
     L = bsp.load_library()
 
     def call(none=False, dtype=bsp.INT8, codes=FAKE, stride=64, **kw):
-        return L.quantize_tokens_f16(None if none else ctypes.byref(_tokens(**kw)), dtype, codes, stride, None)
+        return L.quantize_tokens_f16(None if none else _tokens(**kw), dtype, codes, stride, None)
 
     pair = dict(residual=FAKE, hidden=FAKE, residual_stride=64, hidden_stride=64)
     for bad in (dict(none=True), dict(dtype=bsp.FP16), dict(dtype=bsp.INT2), dict(dtype=9), dict(n=-1), dict(K=-1),
