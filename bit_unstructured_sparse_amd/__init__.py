@@ -661,7 +661,7 @@ def new_workspace(dtype: int, M: int, K: int, N: int, nnz: int = -1, device="cud
 # ---- paged key/value cache, quantised as it is written ----
 
 TREE_MAX = 64
-PAGES_MAX_SEQUENCES = 8192
+PAGES_MAX_SEQUENCES = 4096
 
 
 class _KVCacheDesc(ctypes.Structure):

@@ -26,8 +26,8 @@ namespace {
 
 #define PG_BLOCK 256
 #define PG_WAVES (PG_BLOCK / BSP_WAVE)
-#define PG_ROWS 4            // rows a thread, so that long calls reach few workgroups
-#define PG_MAX_GRID 512
+#define PG_MAX_GRID 256
+#define PG_WAITS 0x80000000u      // beside a sequence's kept tokens: its rows or its row of the table do not fit
 
 struct PgArgs {
     int32_t *table, *lens, *held, *free_pages;
@@ -38,44 +38,14 @@ struct PgArgs {
     int32_t n, width, shift, pool, rows;
 };
 
-// What a sequence asks for: its kept and new tokens, and the pages it holds, takes and gives back.
-struct PgSeq {
-    uint32_t kept, more, held;      // more: at most rows + 1
-    uint32_t grow, shrink;
-    bool fits;                      // its rows and its row of the table
-};
-
-// end: new tokens up to and with this sequence, at most rows + 1
-__device__ __forceinline__ PgSeq pg_seq(const PgArgs &a, int b, uint32_t end) {
-    PgSeq s;
-    const uint32_t len = (uint32_t)min(max(a.lens[b], 0), a.width << a.shift);
-    s.kept = a.keep == nullptr ? len : min((uint32_t)max(a.keep[b], 0), len);
-    s.more = (uint32_t)min(max(a.more[b], 0), a.rows + 1);
-    s.held = (uint32_t)min(max(a.held[b], 0), a.width);
-    const uint32_t want = (s.kept + s.more + (1u << a.shift) - 1) >> a.shift;
-    s.fits = s.more == 0 || (end <= (uint32_t)a.rows && want <= (uint32_t)a.width);
-    s.grow = s.fits && want > s.held ? want - s.held : 0;
-    s.shrink = s.fits && want < s.held ? s.held - want : 0;
-    return s;
-}
-
-// Inclusive running sums of v over the workgroup, from `carry` on, at most `most`
-// (a sum cut off there is associative for values that are not negative).
-__device__ __forceinline__ uint32_t pg_scan(uint32_t v, uint32_t carry, uint32_t most, uint32_t *sums) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const uint32_t o = (uint32_t)__shfl_up((int)v, d, 64);
-        if (lane >= d) v = min(v + o, most);
-    }
-    if (lane == 63) sums[wave] = v;
-    __syncthreads();
-    uint32_t before = carry;
-#pragma unroll
-    for (int w = 0; w < PG_WAVES; ++w)
-        if (w < wave) before = min(before + sums[w], most);
-    __syncthreads();
-    return min(v + before, most);
+// Inclusive running sums over the wavefront, cut off at `most` (sums of values that are not negative, cut off
+// there, are associative). Lanes 1, 2, 4, 8 below in a row of 16, then the last lane of the rows below.
+__device__ __forceinline__ uint32_t pg_wave_scan(uint32_t v, uint32_t most) {
+#define PG_STEP(ctrl, rows) \
+    v = min(v + (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, ctrl, rows, 0xF, false), most);
+    PG_STEP(0x111, 0xF) PG_STEP(0x112, 0xF) PG_STEP(0x114, 0xF) PG_STEP(0x118, 0xF) PG_STEP(0x142, 0xA) PG_STEP(0x143, 0xC)
+#undef PG_STEP
+    return v;
 }
 
 // The first b with end[b] > x (n when there is none).
@@ -92,40 +62,64 @@ __device__ __forceinline__ int pg_upper(const uint32_t *end, int n, uint32_t x) 
 }
 
 __global__ __launch_bounds__(PG_BLOCK) void k_pages_step(const PgArgs a) {
+    // of each sequence: the running sums of rows (cut off at rows + 1), pages taken and pages given back, with its
+    // own; its kept tokens (and PG_WAITS); the pages it holds
     extern __shared__ uint32_t pg_lds[];
-    __shared__ uint32_t sums[PG_WAVES];
+    __shared__ uint32_t row_sums[PG_WAVES], take_sums[PG_WAVES], give_sums[PG_WAVES];
     __shared__ int last;
-    uint32_t *rows_end = pg_lds, *take_end = rows_end + a.n, *give_end = take_end + a.n;
-    const int tid = threadIdx.x;
+    uint32_t *rows_end = pg_lds, *take_end = rows_end + a.n, *give_end = take_end + a.n, *kept_of = give_end + a.n,
+             *held_of = kept_of + a.n;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const uint32_t count = (uint32_t)min(max(a.free_pages[0], 0), a.pool), most = (uint32_t)a.rows + 1;
     uint32_t rows_sum = 0, take_sum = 0, give_sum = 0;
     for (int b0 = 0; b0 < a.n; b0 += PG_BLOCK) {
         const int b = b0 + tid;
-        const bool in = b < a.n;
-        const uint32_t more = in ? (uint32_t)min(max(a.more[b], 0), a.rows + 1) : 0;
-        const uint32_t end = pg_scan(more, rows_sum, (uint32_t)a.rows + 1, sums);
-        uint32_t grow = 0, shrink = 0;
-        if (in) {
-            const PgSeq s = pg_seq(a, b, end);
-            grow = s.grow, shrink = s.shrink;
+        uint32_t kept = 0, more = 0, held = 0;
+        if (b < a.n) {
+            const uint32_t len = (uint32_t)min(max(a.lens[b], 0), a.width << a.shift);
+            kept = a.keep == nullptr ? len : min((uint32_t)max(a.keep[b], 0), len);
+            more = min((uint32_t)max(a.more[b], 0), most);
+            held = (uint32_t)min(max(a.held[b], 0), a.width);
         }
-        const uint32_t take = pg_scan(grow, take_sum, 0x7FFFFFFFu, sums);
-        const uint32_t give = pg_scan(shrink, give_sum, 0x7FFFFFFFu, sums);
-        if (in) rows_end[b] = end, take_end[b] = take, give_end[b] = give;
+        uint32_t end = pg_wave_scan(more, most);
+        if (lane == 63) row_sums[wave] = end;
         __syncthreads();
-        const int top = min(b0 + PG_BLOCK, a.n) - 1;
-        rows_sum = rows_end[top], take_sum = take_end[top], give_sum = give_end[top];
+        for (int w = 0; w < PG_WAVES; ++w) {
+            if (w < wave) end = min(end + row_sums[w], most);
+        }
+        end = min(end + rows_sum, most);
+        const uint32_t want = (kept + more + (1u << a.shift) - 1) >> a.shift;
+        const bool fits = more == 0 || (end <= (uint32_t)a.rows && want <= (uint32_t)a.width);
+        uint32_t take = pg_wave_scan(fits && want > held ? want - held : 0, 0x7FFFFFFFu);
+        uint32_t give = pg_wave_scan(fits && want < held ? held - want : 0, 0x7FFFFFFFu);
+        if (lane == 63) take_sums[wave] = take, give_sums[wave] = give;
+        __syncthreads();
+        for (int w = 0; w < PG_WAVES; ++w) {
+            if (w < wave) take += take_sums[w], give += give_sums[w];
+            rows_sum = min(rows_sum + row_sums[w], most);
+        }
+        if (b < a.n) {
+            rows_end[b] = end, take_end[b] = take_sum + take, give_end[b] = give_sum + give;
+            kept_of[b] = fits ? kept : kept | PG_WAITS, held_of[b] = held;
+        }
+        for (int w = 0; w < PG_WAVES; ++w) take_sum += take_sums[w], give_sum += give_sums[w];
+        __syncthreads();
     }
-    const uint32_t count = (uint32_t)min(max(a.free_pages[0], 0), a.pool);
     int32_t *list = a.free_pages + 2;
-    // pages taken by the sequences that need not wait: the running sum up to the first one that does
+    // pages taken: all that are asked for, or those up to the first sequence that takes more than there are
     const uint32_t have = count + give_sum;
-    const int wait = pg_upper(take_end, a.n, have);
-    const uint32_t taken = wait > 0 ? take_end[wait - 1] : 0;
-
+    uint32_t taken = take_sum;
+    if (taken > have) {
+        const int wait = pg_upper(take_end, a.n, have);
+        taken = wait > 0 ? take_end[wait - 1] : 0;
+    }
+    auto before = [](const uint32_t *end, int b) { return b > 0 ? end[b - 1] : 0u; };
+    auto goes = [&](int b) {      // whether the sequence need not wait
+        return (kept_of[b] & PG_WAITS) == 0 && (take_end[b] <= have || take_end[b] == before(take_end, b));
+    };
     auto given = [&](uint32_t n) {      // the n-th page given back
         const int b = pg_upper(give_end, a.n, n);
-        const PgSeq s = pg_seq(a, b, rows_end[b]);
-        return a.table[(int64_t)b * a.width + (s.held - s.shrink) + (n - (give_end[b] - s.shrink))];
+        return a.table[(int64_t)b * a.width + held_of[b] - (give_end[b] - n)];
     };
     auto page_taken = [&](uint32_t n) { return n < give_sum ? given(n) : list[count - 1 - (n - give_sum)]; };
 
@@ -135,53 +129,48 @@ __global__ __launch_bounds__(PG_BLOCK) void k_pages_step(const PgArgs a) {
         int64_t slot = -1;
         int32_t position = 0;
         if (b < a.n) {
-            const PgSeq s = pg_seq(a, b, rows_end[b]);
-            const uint32_t i = r - (b > 0 ? rows_end[b - 1] : 0), t = s.kept + i, p = t >> a.shift;
-            if (s.fits && (s.grow == 0 || take_end[b] <= have)) {
-                const int32_t page = p < s.held ? a.table[(int64_t)b * a.width + p]
-                                                : page_taken(take_end[b] - s.grow + (p - s.held));
-                slot = ((int64_t)page << a.shift) + (t & ((1u << a.shift) - 1));
-            }
+            const uint32_t kept = kept_of[b] & ~PG_WAITS, i = r - before(rows_end, b), t = kept + i, p = t >> a.shift;
             position = (int32_t)t;
             if (a.mask != nullptr && a.more[b] <= BSP_TREE_MAX)
-                position = (int32_t)s.kept + __popcll(a.mask[r] & ((UINT64_C(1) << i) - 1));
+                position = (int32_t)kept + __popcll(a.mask[r] & ((UINT64_C(1) << i) - 1));
+            if (goes(b)) {
+                const int32_t page = p < held_of[b] ? a.table[(int64_t)b * a.width + p]
+                                                    : page_taken(before(take_end, b) + (p - held_of[b]));
+                slot = ((int64_t)page << a.shift) + (t & ((1u << a.shift) - 1));
+            }
         }
         a.slots[r] = slot;
         a.positions[r] = position;
         a.sequences[r] = b < a.n ? b : -1;
     }
-    for (uint32_t n = me; n < max(taken, give_sum); n += all) {
+    // pages, from the last thread down: short calls have them beside the rows
+    for (uint32_t n = all - 1 - me; n < max(taken, give_sum); n += all) {
         if (n < taken) {
             const int b = pg_upper(take_end, a.n, n);
-            const PgSeq s = pg_seq(a, b, rows_end[b]);
-            a.table[(int64_t)b * a.width + s.held + (n - (take_end[b] - s.grow))] = page_taken(n);
+            a.table[(int64_t)b * a.width + held_of[b] + (n - before(take_end, b))] = page_taken(n);
         } else {
             const uint32_t at = have - 1 - n;
             if (at < (uint32_t)a.pool) list[at] = given(n);
         }
     }
+    auto length = [&](int b) { return (int32_t)((kept_of[b] & ~PG_WAITS) + rows_end[b] - before(rows_end, b)); };
     for (uint32_t b = me; b <= (uint32_t)a.n; b += all) {
-        a.q_start[b] = (int32_t)min(b > 0 ? rows_end[b - 1] : 0, (uint32_t)a.rows);
-        if (b < (uint32_t)a.n) {
-            const PgSeq s = pg_seq(a, (int)b, rows_end[b]);
-            const bool ok = s.fits && (s.grow == 0 || take_end[b] <= have);
-            a.kv_lens[b] = ok ? (int32_t)(s.kept + s.more) : 0;
-        }
+        a.q_start[b] = (int32_t)min(before(rows_end, (int)b), (uint32_t)a.rows);
+        if (b < (uint32_t)a.n) a.kv_lens[b] = goes((int)b) ? length((int)b) : 0;
     }
-    // the last workgroup: every other has read all it needs
+    // the state, once every workgroup has read all it needs: by the last one. What was read has been used, in
+    // stores or in LDS, before the barrier; nothing that another workgroup wrote is read, so no fence is needed
     __syncthreads();
-    if (tid == 0) {
-        __threadfence();
-        last = atomicAdd(&a.free_pages[1], 1) == (int)gridDim.x - 1;
+    if (gridDim.x > 1) {
+        if (tid == 0) last = atomicAdd(&a.free_pages[1], 1) == (int)gridDim.x - 1;
+        __syncthreads();
+        if (!last) return;
     }
-    __syncthreads();
-    if (!last) return;
-    __threadfence();
     for (int b = tid; b < a.n; b += PG_BLOCK) {
-        const PgSeq s = pg_seq(a, b, rows_end[b]);
-        const bool ok = s.fits && (s.grow == 0 || take_end[b] <= have);
-        a.lens[b] = (int32_t)(ok ? s.kept + s.more : s.kept);
-        a.held[b] = (int32_t)(ok ? s.held + s.grow - s.shrink : s.held);
+        const bool ok = goes(b);
+        a.lens[b] = ok ? length(b) : (int32_t)(kept_of[b] & ~PG_WAITS);
+        a.held[b] = (int32_t)(ok ? held_of[b] + (take_end[b] - before(take_end, b)) - (give_end[b] - before(give_end, b))
+                                 : held_of[b]);
     }
     if (tid == 0) {
         a.free_pages[0] = (int32_t)min(have - taken, (uint32_t)a.pool);
@@ -219,9 +208,10 @@ extern "C" int kv_pages_step(const bsp_kv_pages *pages, const int32_t *keep, con
     a.slots = slots, a.positions = positions, a.sequences = sequences, a.q_start = q_start, a.kv_lens = kv_lens;
     a.n = (int32_t)p->sequences, a.width = (int32_t)p->table_width, a.pool = (int32_t)p->pool, a.rows = (int32_t)rows;
     a.shift = __builtin_ctzll((unsigned long long)p->page_size);
-    const int64_t work = std::max<int64_t>(rows, p->sequences);
-    const unsigned grid = (unsigned)std::min<int64_t>(std::max<int64_t>((work + PG_BLOCK * PG_ROWS - 1) /
-                                                                        (PG_BLOCK * PG_ROWS), 1), PG_MAX_GRID);
-    hipLaunchKernelGGL(k_pages_step, dim3(grid), dim3(PG_BLOCK), (unsigned)(3 * 4 * p->sequences), stream, a);
+    const unsigned grid = (unsigned)std::min<int64_t>(std::max<int64_t>((rows + PG_BLOCK - 1) / PG_BLOCK, 1), PG_MAX_GRID);
+    const unsigned lds = (unsigned)(5 * 4 * p->sequences);
+    if (lds > 65536)
+        (void)hipFuncSetAttribute((const void *)k_pages_step, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+    hipLaunchKernelGGL(k_pages_step, dim3(grid), dim3(PG_BLOCK), lds, stream, a);
     return hipGetLastError() == hipSuccess ? BSP_OK : BSP_E_HIP;
 }

@@ -652,7 +652,7 @@ typedef struct bsp_kv_pages {
     int32_t *block_table, *lens, *held, *free_pages;   /* DEVICE */
 } bsp_kv_pages;
 
-#define BSP_PAGES_MAX_SEQUENCES 8192
+#define BSP_PAGES_MAX_SEQUENCES 4096
 
 /*
  * kv_pages_step -- one step of all sequences, asynchronous on `stream`: sequence

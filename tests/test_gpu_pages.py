@@ -141,7 +141,7 @@ def test_values_that_cannot_be_touch_nothing_outside(dev):
 
 def test_many_rows_and_most_sequences(dev):
     rng = np.random.default_rng(12)
-    # 8192 sequences, the most a call takes
+    # the most sequences a call takes
     pages, ref = _state(rng, bsp.PAGES_MAX_SEQUENCES, 16, 40, 8, 3000, dev)
     new = rng.integers(0, 9, bsp.PAGES_MAX_SEQUENCES)
     rows = int(new.sum())

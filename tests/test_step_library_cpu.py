@@ -32,7 +32,7 @@ def test_pages():
         assert call(**bad) == bsp.E_ARG, bad
     assert call(sequences=bsp.PAGES_MAX_SEQUENCES + 1) == bsp.E_UNSUPPORTED
     for bad in (dict(rows=1 << 28), dict(table_width=1 << 27), dict(pool=1 << 32), dict(pool=INT32_MAX - 11),
-                dict(sequences=8192, table_width=1 << 18), dict(table_width=(INT32_MAX - 4095) // 16)):
+                dict(sequences=4096, table_width=1 << 19), dict(table_width=(INT32_MAX - 4095) // 16)):
         assert call(**bad) == bsp.E_OVERFLOW, bad
 
 
