@@ -68,15 +68,28 @@ __device__ __forceinline__ uint32_t qk_turn(int32_t p, uint64_t f) {
     return (uint32_t)p * hi + __umulhi((uint32_t)p, lo) - (p < 0 ? lo : 0);
 }
 
-template <int D, bool VEC, int U>
+// 8 values at any 2-byte address: the memory takes 16 bytes anywhere.
+__device__ __forceinline__ kv_u4 qk_load(const uint16_t *p) {
+    kv_u4 v;
+    __builtin_memcpy(&v, p, 16);
+    return v;
+}
+
+__device__ __forceinline__ void qk_store(uint16_t *p, kv_u4 v) { __builtin_memcpy(p, &v, 16); }
+
+typedef float qk_f4 __attribute__((ext_vector_type(4)));
+
+template <int D, int U>
 __global__ __launch_bounds__(QK_BLOCK) void k_qk_heads(const QkArgs a, uint32_t items) {
     constexpr int LPR = D / 8, RPW = 64 / LPR;
-    const uint32_t item = __builtin_amdgcn_readfirstlane(blockIdx.x * (QK_BLOCK / 64) + (threadIdx.x >> 6));
+    __shared__ __align__(16) float turns[QK_BLOCK / 64][2][D / 2];      // each wavefront's cosines and sines
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    const uint32_t item = __builtin_amdgcn_readfirstlane(blockIdx.x * (QK_BLOCK / 64) + wave);
     if (item >= items) return;
     const uint32_t token = item / a.parts[2], part = item - token * a.parts[2];
     const int kind = part < a.parts[0] ? 0 : part < a.parts[1] ? 1 : 2;
     const int first = (int)(part - (kind == 0 ? 0 : a.parts[kind - 1])) * (RPW * U);
-    const int lane = threadIdx.x & 63, heads = a.heads[kind];
+    const int heads = a.heads[kind];
     const int ch = (lane % LPR) * 8;
     const uint16_t *src = a.x[kind] + (int64_t)token * a.xs[kind];
     kv_u4 raw[U];
@@ -84,34 +97,58 @@ __global__ __launch_bounds__(QK_BLOCK) void k_qk_heads(const QkArgs a, uint32_t 
     for (int i = 0; i < U; ++i) {
         // heads past the last are read as head 0, so that every lane of the shuffles holds a value
         const int h = first + i * RPW + lane / LPR;
-        raw[i] = kv_load8<VEC>(src + (int64_t)(h < heads ? h : 0) * D + ch);
+        raw[i] = qk_load(src + (int64_t)(h < heads ? h : 0) * D + ch);
     }
-    const int rot = kind == 2 ? 0 : a.rot;
-    float sn[8], cs[8];
+    const int rot = kind == 2 ? 0 : a.rot, half = rot / 2;
+    const uint16_t *weight = kind == 2 ? nullptr : a.weight[kind];
+    // y = (x own + other pair) / sqrt(mean + eps): own and pair hold weight times cosine and sine
+    float own[8], pair[8];
     int partner = lane;
-    bool upper = false;
-    if (rot > 0) {
-        const int32_t p = a.positions[token];
-        if (a.interleaved) {
-            if (ch < rot) {
+    if (kind != 2) {
+        const bool upper = !a.interleaved && ch >= half, turned = ch < rot;
+        if (!a.interleaved && turned) partner = upper ? lane - half / 8 : lane + half / 8;
+        kv_h8 w, wp;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) qk_sincos(qk_turn(p, a.freq[ch / 2 + e]), sn[e], cs[e]);
+        for (int e = 0; e < 8; ++e) w[e] = wp[e] = (_Float16)1.0f;
+        if (weight != nullptr) {
+            w = __builtin_bit_cast(kv_h8, *reinterpret_cast<const kv_u4 *>(weight + ch));
+            wp = __builtin_bit_cast(kv_h8, *reinterpret_cast<const kv_u4 *>(weight + (partner - lane) * 8 + ch));
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) own[e] = (float)w[e], pair[e] = 0.0f;
+        if (rot > 0) {
+            // each pair's angle once for the wavefront, by way of its own LDS
+            const int32_t p = a.positions[token];
+#pragma unroll
+            for (int i = 0; i < D / 2; i += 64) {
+                const int j = i + lane;
+                if (j < half) qk_sincos(qk_turn(p, a.freq[j]), turns[wave][1][j], turns[wave][0][j]);
             }
-        } else if (ch < rot) {
-            const int half = rot / 2;
-            upper = ch >= half;
-            partner = upper ? lane - half / 8 : lane + half / 8;
-            const uint64_t *f = a.freq + (upper ? ch - half : ch);
+            __builtin_amdgcn_wave_barrier();
+            if (turned && a.interleaved) {
+                const qk_f4 c = *reinterpret_cast<const qk_f4 *>(&turns[wave][0][ch / 2]);
+                const qk_f4 s = *reinterpret_cast<const qk_f4 *>(&turns[wave][1][ch / 2]);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                qk_sincos(qk_turn(p, f[e]), sn[e], cs[e]);
-                if (!upper) sn[e] = -sn[e];        // y1 cos - y2 sin below, y2 cos + y1 sin above
+                for (int e = 0; e < 8; e += 2) {
+                    const float w1 = own[e], w2 = own[e + 1];
+                    own[e] = w1 * c[e / 2], pair[e] = -w2 * s[e / 2];
+                    own[e + 1] = w2 * c[e / 2], pair[e + 1] = w1 * s[e / 2];
+                }
+            } else if (turned) {
+                const int i0 = upper ? ch - half : ch;
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const qk_f4 c = *reinterpret_cast<const qk_f4 *>(&turns[wave][0][i0 + 4 * q]);
+                    const qk_f4 s = *reinterpret_cast<const qk_f4 *>(&turns[wave][1][i0 + 4 * q]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        own[4 * q + e] *= c[e];
+                        pair[4 * q + e] = (float)wp[4 * q + e] * (upper ? s[e] : -s[e]);
+                    }
+                }
             }
         }
     }
-    const uint16_t *weight = kind == 2 ? nullptr : a.weight[kind];
-    kv_h8 w;
-    if (weight != nullptr) w = __builtin_bit_cast(kv_h8, *reinterpret_cast<const kv_u4 *>(weight + ch));
     const int64_t slot = a.o[1] == nullptr && kind > 0 ? a.slots[token] : -1;
     const bool stored = slot >= 0 && slot < a.nslots;
     const int64_t page = (stored ? slot : 0) >> a.page_shift;
@@ -123,42 +160,36 @@ __global__ __launch_bounds__(QK_BLOCK) void k_qk_heads(const QkArgs a, uint32_t 
         if (kind != 2) {
             const kv_h8 x = __builtin_bit_cast(kv_h8, raw[i]);
             float y[8];
+            if (rot > 0 && !a.interleaved) {
+                kv_u4 there;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = (float)x[e];
+                for (int e = 0; e < 4; ++e) there[e] = ch < rot ? (uint32_t)__shfl((int)raw[i][e], partner, 64) : 0u;
+                const kv_h8 z = __builtin_bit_cast(kv_h8, there);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) y[e] = __builtin_fmaf((float)z[e], pair[e], (float)x[e] * own[e]);
+            } else if (ch < rot) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) y[e] = __builtin_fmaf((float)x[e ^ 1], pair[e], (float)x[e] * own[e]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) y[e] = (float)x[e] * own[e];
+            }
             if (weight != nullptr) {
                 float sum = 0.0f;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) sum = __builtin_fmaf(y[e], y[e], sum);
+                for (int e = 0; e < 8; ++e) sum = __builtin_fmaf((float)x[e], (float)x[e], sum);
 #pragma unroll
                 for (int d = 1; d < LPR; d <<= 1) sum += __shfl_xor(sum, d, 64);
-                const float r = 1.0f / sqrtf(sum * (1.0f / D) + a.eps);
+                const float r = __builtin_amdgcn_rsqf(__builtin_fmaf(sum, 1.0f / D, a.eps));
 #pragma unroll
-                for (int e = 0; e < 8; ++e) y[e] = y[e] * r * (float)w[e];
-            }
-            if (rot > 0) {
-                if (a.interleaved) {
-                    if (ch < rot) {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float y1 = y[2 * e], y2 = y[2 * e + 1];
-                            y[2 * e] = y1 * cs[e] - y2 * sn[e];
-                            y[2 * e + 1] = y2 * cs[e] + y1 * sn[e];
-                        }
-                    }
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const float other = __shfl(y[e], partner, 64);
-                        if (ch < rot) y[e] = y[e] * cs[e] + other * sn[e];
-                    }
-                }
+                for (int e = 0; e < 8; ++e) y[e] *= r;
             }
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 raw[i][e] = bsp_f2h(bsp_rounded(y[2 * e])) | ((uint32_t)bsp_f2h(bsp_rounded(y[2 * e + 1])) << 16);
         }
         if (kind == 0 || a.o[1] != nullptr) {
-            if (live) kv_store8<VEC>(a.o[kind] + (int64_t)token * a.os[kind] + (int64_t)h * D + ch, raw[i]);
+            if (live) qk_store(a.o[kind] + (int64_t)token * a.os[kind] + (int64_t)h * D + ch, raw[i]);
             continue;
         }
         const int64_t row = ((page * heads + (live ? h : 0)) << a.page_shift) + off;
@@ -178,22 +209,26 @@ __global__ __launch_bounds__(QK_BLOCK) void k_qk_heads(const QkArgs a, uint32_t 
     }
 }
 
-template <int D, bool VEC, int U>
+template <int D, int U>
 void qk_launch_u(QkArgs &a, hipStream_t stream) {
     constexpr int RUN = 64 / (D / 8) * U;
     uint32_t total = 0;
     for (int k = 0; k < 3; ++k) a.parts[k] = total += (uint32_t)((a.heads[k] + RUN - 1) / RUN);
     const uint32_t items = a.n * total;
     const unsigned grid = (items + QK_BLOCK / 64 - 1) / (QK_BLOCK / 64);
-    hipLaunchKernelGGL((k_qk_heads<D, VEC, U>), dim3(grid), dim3(QK_BLOCK), 0, stream, a, items);
+    hipLaunchKernelGGL((k_qk_heads<D, U>), dim3(grid), dim3(QK_BLOCK), 0, stream, a, items);
 }
 
+// Heads of 128, many of them: two groups a wavefront (8192 tokens x 64 heads 51.8 us against 61.3, 512 x 80
+// 7.4 against 7.8, 128 x 80 5.0 against 4.5; four groups 50.1, 8.0, 5.9). Heads of 64, 8 to a group, gain nothing
+// (8192 x 40 20.5 against 20.6, with an int8 cache 28.4 against 26.2), nor do those of 256 (23.7 against 25.5, 32.1
+// against 30.9).
 template <int D>
-void qk_launch(QkArgs &a, bool vec, hipStream_t stream) {
-    if (vec)
-        qk_launch_u<D, true, 1>(a, stream);
+void qk_launch(QkArgs &a, hipStream_t stream) {
+    if (D == 128 && (int64_t)a.n * (a.heads[0] + a.heads[1] + a.heads[2]) >= 32768)
+        qk_launch_u<128, 2>(a, stream);
     else
-        qk_launch_u<D, false, 1>(a, stream);
+        qk_launch_u<D, 1>(a, stream);
 }
 
 int qk_common(QkArgs &a, int64_t n, int64_t hq, int64_t hkv, int64_t D, const bsp_rotation *r, bool values,
@@ -208,15 +243,14 @@ int qk_common(QkArgs &a, int64_t n, int64_t hq, int64_t hkv, int64_t D, const bs
     if (n == 0 || hq + hkv == 0) return BSP_OK;
     const int64_t heads[3] = {hq, hkv, values ? hkv : 0};
     uintptr_t bits = 0;
-    int64_t strides = 0;
     for (int k = 0; k < 3; ++k) {
         a.heads[k] = (int)heads[k];
         if (heads[k] == 0) continue;
         const bool out = k == 0 || (k == 1 && !values);
         if (a.x[k] == nullptr || (out && a.o[k] == nullptr)) return BSP_E_ARG;
         if (a.xs[k] < heads[k] * D || (out && a.os[k] < heads[k] * D)) return BSP_E_ARG;
-        bits |= (uintptr_t)a.x[k], strides |= a.xs[k];
-        if (out) bits |= (uintptr_t)a.o[k], strides |= a.os[k];
+        bits |= (uintptr_t)a.x[k];
+        if (out) bits |= (uintptr_t)a.o[k];
     }
     if ((bits & 1u) != 0) return BSP_E_ARG;
     if (r->rot > 0) {
@@ -227,14 +261,12 @@ int qk_common(QkArgs &a, int64_t n, int64_t hq, int64_t hkv, int64_t D, const bs
     a.freq = r->freq, a.positions = r->positions;
     a.eps = r->eps, a.rot = (int)r->rot, a.interleaved = r->interleaved != 0;
     a.n = (uint32_t)n;
-    // whole 16-byte pieces of the heads, unless they are off that boundary
-    const bool vec = (bits & 15u) == 0 && (strides & 7) == 0;
     if (D == 64)
-        qk_launch<64>(a, vec, stream);
+        qk_launch<64>(a, stream);
     else if (D == 128)
-        qk_launch<128>(a, vec, stream);
+        qk_launch<128>(a, stream);
     else
-        qk_launch<256>(a, vec, stream);
+        qk_launch<256>(a, stream);
     return hipGetLastError() == hipSuccess ? BSP_OK : BSP_E_HIP;
 }
 
