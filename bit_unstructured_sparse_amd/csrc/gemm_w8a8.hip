@@ -20,6 +20,7 @@ typedef uint32_t w8_u2 __attribute__((ext_vector_type(2)));
 typedef float w8_f4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) void w8_lds_void;
 typedef __attribute__((address_space(3))) const w8_i4 w8_lds_i4;
+typedef __attribute__((address_space(3))) w8_u2 w8_lds_u2;
 
 struct W8Args {
     const uint8_t *tiles;
@@ -357,31 +358,54 @@ __global__ __launch_bounds__(64 * WM * WN) void k_w8_tiles(const W8Args a) {
         if (t < a.ktiles) turn(t, A[0], B[0], A[1], B[1]);
     }
     w8_wait_vm<0>();
-    const int m0 = (band0 + wm * TM) * 16 + (lane >> 4) * 4;
-    const int64_t n1 = n0 + wn * TN * 16 + (lane & 15);
-    if (a.wide && (band0 + MBANDS) * 16 <= a.M && ntok == NBLOCKS * 16) {
-        float sx[TN];
+    w8_barrier();
+    // The result by way of LDS, 16 tokens at a time in the wavefront's own part of it: a token's TM x 16 channels
+    // leave together, 16 bytes a lane.
+    constexpr int PITCH = TM * 16 + 8, LPR = TM * 2, RPI = 64 / LPR;      // halves a token, lanes a token, tokens at once
+    static_assert(W * 16 * PITCH * 2 <= (int)(R * STAGE), "the ring holds it");
+    const uint32_t out = lds + (uint32_t)(wave * 16 * PITCH * 2);
+    const int m0 = (band0 + wm * TM) * 16;
+    w8_f4 sw[TM];
 #pragma unroll
-        for (int j = 0; j < TN; ++j) sx[j] = a.scale_x[n1 + j * 16];
+    for (int i = 0; i < TM; ++i) {
+        const int m = m0 + i * 16 + (lane >> 4) * 4;
+        if (m + 3 < a.M) {
+            __builtin_memcpy(&sw[i], a.scale_w + m, 16);
+        } else {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) sw[i][r] = m + r < a.M ? a.scale_w[m + r] : 0.0f;
+        }
+    }
+    const int piece = m0 + lane % LPR * 8;      // the lane's 8 channels
+#pragma unroll
+    for (int j = 0; j < TN; ++j) {
+        const int first = (wn * TN + j) * 16;
+        const float sx = a.scale_x[n0 + min(first + (lane & 15), ntok - 1)];
 #pragma unroll
         for (int i = 0; i < TM; ++i) {
-            w8_f4 sw;
-            __builtin_memcpy(&sw, a.scale_w + m0 + i * 16, 16);
+            uint16_t h[4];
 #pragma unroll
-            for (int j = 0; j < TN; ++j) {
-                uint16_t h[4];
+            for (int r = 0; r < 4; ++r) h[r] = bsp_f2h(bsp_rounded((float)acc[i][j][r] * sw[i][r] * sx));
+            *(w8_lds_u2 *)(uintptr_t)(out + (uint32_t)((lane & 15) * PITCH + i * 16 + (lane >> 4) * 4) * 2) =
+                w8_u2{h[0] | ((uint32_t)h[1] << 16), h[2] | ((uint32_t)h[3] << 16)};
+        }
+        __builtin_amdgcn_wave_barrier();
 #pragma unroll
-                for (int r = 0; r < 4; ++r) h[r] = bsp_f2h(bsp_rounded((float)acc[i][j][r] * sw[r] * sx[j]));
-                *reinterpret_cast<w8_u2 *>(a.y + (n1 + j * 16) * a.ys + m0 + i * 16) =
-                    w8_u2{h[0] | ((uint32_t)h[1] << 16), h[2] | ((uint32_t)h[3] << 16)};
+        for (int c = 0; c < 16 / RPI; ++c) {
+            const int row = c * RPI + lane / LPR;
+            const w8_i4 v = *(w8_lds_i4 *)(uintptr_t)(out + (uint32_t)(row * PITCH + lane % LPR * 8) * 2);
+            if (first + row >= ntok) continue;
+            uint16_t *y = a.y + (n0 + first + row) * a.ys + piece;
+            if (piece + 8 <= a.M) {
+                __builtin_memcpy(y, &v, 16);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (piece + e < a.M) y[e] = (uint16_t)((uint32_t)v[e / 2] >> (16 * (e & 1)));
             }
         }
-        return;
+        __builtin_amdgcn_wave_barrier();
     }
-#pragma unroll
-    for (int j = 0; j < TN; ++j)
-#pragma unroll
-        for (int i = 0; i < TM; ++i) w8_store(a, n1 + j * 16, m0 + i * 16, acc[i][j]);
 }
 
 // Allows a kernel its LDS, once for each device.
@@ -434,7 +458,7 @@ struct W8Plan {
 const W8Plan W8_PLANS[] = {
     {1, 1, w8_ring<1, 1, 8, 4>}, {1, 2, w8_ring<2, 1, 8, 3>}, {2, 2, w8_ring<2, 2, 8, 4>}, {1, 4, w8_ring<4, 1, 4, 4>},
     {2, 4, w8_ring<4, 2, 8, 3>}, {4, 4, w8_tiles<2, 2, 2, 2, 4, 3>}, {8, 4, w8_tiles<2, 2, 4, 2, 2, 3>},
-    {8, 8, w8_tiles<2, 4, 4, 2, 1, 4>}, {16, 8, w8_tiles<2, 4, 8, 2, 1, 4>}, {16, 16, w8_tiles<2, 4, 8, 4, 1, 4>},
+    {8, 8, w8_tiles<2, 4, 4, 2, 1, 4>}, {16, 8, w8_tiles<2, 4, 8, 2, 1, 4>}, {16, 16, w8_tiles<2, 4, 8, 4, 1, 3>},
 };
 
 // A tile's time is that of its operands' way into the CU (a KB of them every 1 / 57 us, whatever the
