@@ -709,7 +709,7 @@ class KVCache:
                             _dptr(self.k_scale), _dptr(self.v_scale))
         for name, value in (("num_pages", pages), ("kv_heads", heads), ("page_size", page_size), ("head_dim", dim),
                             ("device", self.k.device), ("_index", self.k.get_device()), ("_desc", desc),
-                            ("_ref", ctypes.byref(desc))):
+                            ("_ref", ctypes.addressof(desc))):
             object.__setattr__(self, name, value)
 
 
@@ -779,6 +779,8 @@ def _launch(fn, index: int, stream, *args) -> int:
     with the tensors' device as the current one: kernels go to the current
     device, and its default stream has the same handle as every other device's."""
     import torch
+    if not _native_tried:
+        _use_native()
     if stream is None:
         handle = torch._C._cuda_getCurrentRawStream(index)
     elif stream.device_index == index:
@@ -789,6 +791,28 @@ def _launch(fn, index: int, stream, *args) -> int:
         return fn(*args, handle)
     with torch.cuda.device(index):
         return fn(*args, handle)
+
+
+_native_tried = False
+
+
+def _use_native() -> None:
+    """From the first launch on, the steps above and the outputs' allocation natively (_binding.so), where it has
+    been built: the same results, and these functions for every case that is not the common one."""
+    global _native_tried, _flat, _rows, _matrix_rows, _new_output, _launch
+    _native_tried = True
+    try:
+        import torch
+        from . import _binding
+    except ImportError:
+        return
+    L = load_library()
+    if not isinstance(L, ctypes.CDLL):
+        return
+    _binding.bind(L._handle, {name: getattr(L, name) for name in EXPORTS},
+                  (_flat, _rows, _matrix_rows, _new_output, _launch), torch)
+    _flat, _rows, _matrix_rows, _new_output, _launch = (_binding.flat, _binding.rows, _binding.matrix_rows,
+                                                        _binding.new_output, _binding.launch)
 
 
 def _weights_on(W: DeviceMatrix, index: int) -> None:
@@ -1068,7 +1092,7 @@ class KVPages:
         desc = _KVPagesDesc(B, width, self.page_size, self.free.numel() - 2, _dptr(self.block_table), _dptr(self.lens),
                             _dptr(self.held), _dptr(self.free))
         for name, value in (("sequences", B), ("width", width), ("device", self.block_table.device),
-                            ("_index", index), ("_desc", desc), ("_ref", ctypes.byref(desc))):
+                            ("_index", index), ("_desc", desc), ("_ref", ctypes.addressof(desc))):
             object.__setattr__(self, name, value)
 
 

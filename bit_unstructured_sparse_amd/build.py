@@ -1,5 +1,6 @@
 """Builds libbitmap_spmm.so (and the streaming-read probe libbsp_probe.so)
-in this directory with hipcc for gfx950.
+in this directory with hipcc for gfx950, and the binding's native steps
+(_binding.so) with the host compiler against PyTorch's headers.
 
     python -m bit_unstructured_sparse_amd.build
 
@@ -13,9 +14,11 @@ pass warns that it does not know that feature, which is harmless.
 """
 from __future__ import annotations
 
+import importlib.util
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -33,6 +36,26 @@ SOURCES = [os.path.join(CSRC, "spmm.hip"), os.path.join(CSRC, "encode.cpp"), os.
 PROBE_SOURCES = [os.path.join(CSRC, "probe_read.hip")]
 
 
+# The steps that the binding's calls repeat, natively; without PyTorch there is nothing to build them for.
+BINDING = os.path.join(HERE, "_binding.so")
+BINDING_SOURCES = [os.path.join(CSRC, "binding.cpp")]
+
+
+def binding_command(out: str):
+    """The host compiler's command, or None without PyTorch."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        return None
+    torch = spec.submodule_search_locations[0]
+    rocm = os.path.dirname(os.path.dirname(HIPCC))
+    return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__",
+            "-DUSE_ROCM", "-I", os.path.join(ROOT, "include"), "-isystem", os.path.join(torch, "include"),
+            "-isystem", os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+            "-isystem", sysconfig.get_paths()["include"], "-isystem", os.path.join(rocm, "include"),
+            *BINDING_SOURCES, "-o", out, "-L", os.path.join(torch, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu",
+            "-ltorch_hip", "-lc10", "-lc10_hip"]
+
+
 def command(out: str, sources=SOURCES):
     return [HIPCC, f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC", "-shared",
             "-I", os.path.join(ROOT, "include"), "-I", CSRC,
@@ -41,16 +64,16 @@ def command(out: str, sources=SOURCES):
             *sources, "-o", out, "-lpthread"]
 
 
-def _compile(out: str, sources, verbose: bool) -> str:
+def _compile(out: str, make, verbose: bool) -> str:
     tmp = out + f".tmp{os.getpid()}"
-    cmd = command(tmp, sources)
+    cmd = make(tmp)
     if verbose:
         print(" ".join(cmd), flush=True)
     r = subprocess.run(cmd, capture_output=True, text=True)
     noise = "'-packed-fp32-ops' is not a recognized feature"
     msgs = [ln for ln in (r.stdout + r.stderr).splitlines() if noise not in ln]
     if r.returncode != 0:
-        raise RuntimeError("hipcc failed:\n" + "\n".join(msgs))
+        raise RuntimeError(f"{os.path.basename(cmd[0])} failed:\n" + "\n".join(msgs))
     if verbose and msgs:
         print("\n".join(msgs))
     os.replace(tmp, out)
@@ -58,8 +81,10 @@ def _compile(out: str, sources, verbose: bool) -> str:
 
 
 def build(verbose: bool = False) -> str:
-    _compile(PROBE_LIB, PROBE_SOURCES, verbose)
-    return _compile(LIB, SOURCES, verbose)
+    _compile(PROBE_LIB, lambda out: command(out, PROBE_SOURCES), verbose)
+    if binding_command(BINDING) is not None:
+        _compile(BINDING, binding_command, verbose)
+    return _compile(LIB, command, verbose)
 
 
 if __name__ == "__main__":
