@@ -800,6 +800,8 @@ def _use_native() -> None:
     """From the first launch on, the steps above and the outputs' allocation natively (_binding.so), where it has
     been built: the same results, and these functions for every case that is not the common one."""
     global _native_tried, _flat, _rows, _matrix_rows, _new_output, _launch
+    if _native_tried:
+        return
     _native_tried = True
     try:
         import torch

@@ -30,6 +30,9 @@ struct W8Args {
     uint16_t *y;
     int64_t ys, n;
     int M, bands, ktiles;
+    int splits, per;         // workgroups that share a tile, column tiles of each (the last may have fewer)
+    uint32_t *counters;      // splits > 1: arrivals at each tile, zero between calls
+    uint8_t *parts;          // and their sums
     int last;                // last 16-byte piece of a token's row, as a byte offset
     uint32_t mtiles, ntiles; // tiles of the result
     bool wide;               // 8-byte stores: Y and its rows lie on that boundary
@@ -56,17 +59,48 @@ __device__ __forceinline__ void w8_store(const W8Args &a, int64_t n, int m, w8_i
 // die is given a run of neighbouring tiles, `deep` rows of tiles at a time, so that it reads few bands and tokens at
 // once. (m = mtiles: none, the grid is a multiple of 8.)
 struct W8Tile {
-    uint32_t m, n;
+    uint32_t m, n, split;
 };
 
 __device__ __forceinline__ W8Tile w8_tile(const W8Args &a, uint32_t deep) {
-    if (a.ntiles == 1) return W8Tile{min(blockIdx.x, a.mtiles), 0};
-    const uint32_t total = a.mtiles * a.ntiles, per = (total + 7) / 8;
-    const uint32_t tile = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
-    if (tile >= total) return W8Tile{a.mtiles, 0};
+    const uint32_t total = a.mtiles * a.ntiles * (uint32_t)a.splits, per = (total + 7) / 8;
+    if (a.ntiles == 1 && a.splits == 1) return W8Tile{min(blockIdx.x, a.mtiles), 0, 0};
+    const uint32_t at = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
+    if (at >= total) return W8Tile{a.mtiles, 0, 0};
+    const uint32_t tile = at / (uint32_t)a.splits, split = at - tile * (uint32_t)a.splits;
     const uint32_t strip = tile / (deep * a.ntiles), rest = tile - strip * (deep * a.ntiles);
     const uint32_t rows = min(deep, a.mtiles - strip * deep);
-    return W8Tile{strip * deep + rest % rows, rest / rows};
+    return W8Tile{strip * deep + rest % rows, rest / rows, split};
+}
+
+// Agent-scope 16-byte stores and loads (aux 16: sc1): they go to the point of coherence that all dies share, so
+// that a part is there for the workgroup that adds it once its store has completed.
+__device__ __forceinline__ void w8_part_store(void *base, uint32_t bytes, uint32_t off, w8_i4 v) {
+    typedef unsigned u4 __attribute__((ext_vector_type(4)));
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u4, v), bsp_rsrc(base, bytes), off, 0, 16);
+}
+__device__ __forceinline__ w8_i4 w8_part_load(const void *base, uint32_t bytes, uint32_t off) {
+    return __builtin_bit_cast(w8_i4, __builtin_amdgcn_raw_buffer_load_b128(bsp_rsrc(base, bytes), off, 0, 16));
+}
+
+// The e-th of the tile's splits after this one, e < splits.
+__device__ __forceinline__ uint32_t w8_other(const W8Args &a, const W8Tile &tile, int e) {
+    const uint32_t s = tile.split + (uint32_t)e;
+    return s < (uint32_t)a.splits ? s : s - (uint32_t)a.splits;
+}
+
+// Whether this workgroup is the last to come to its tile (every thread gets the same answer). Each thread's part
+// is stored before the call and complete before the barrier, the arrival follows it: the last one finds all parts.
+__device__ __forceinline__ bool w8_last(const W8Args &a, const W8Tile &tile) {
+    __shared__ uint32_t arrived;
+    uint32_t *counter = a.counters + tile.m * a.ntiles + tile.n;
+    __builtin_amdgcn_s_waitcnt(0);
+    __syncthreads();
+    if (threadIdx.x == 0) arrived = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __syncthreads();
+    if (arrived != (uint32_t)a.splits - 1) return false;
+    if (threadIdx.x == 0) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    return true;
 }
 
 // ---- few tokens: W streams from memory straight into registers ----
@@ -161,16 +195,17 @@ __device__ __forceinline__ void w8_dma(const void *base, uint32_t bytes, uint32_
 template <int NB, int MB, int W, int P>
 __global__ __launch_bounds__(64 * W) void k_w8_ring(const W8Args a) {
     constexpr uint32_t STAGE = (MB + NB) * 1024u;
-    extern __shared__ uint8_t w8_lds[];
+    extern __shared__ __attribute__((aligned(128))) uint8_t w8_lds[];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const W8Tile tile = w8_tile(a, 1);
     if (tile.m >= a.mtiles) return;
     const int band = (int)tile.m * MB, nb = min(MB, a.bands - band);
     const int64_t n0 = (int64_t)tile.n * (NB * 16);
     const int ntok = (int)min((int64_t)(NB * 16), a.n - n0);
-    const uint8_t *wbase = a.tiles + ((int64_t)band * a.ktiles << 10);
-    const int8_t *xbase = a.x + n0 * a.xs;
-    const uint32_t wbytes = (uint32_t)nb * (uint32_t)a.ktiles << 10, xbytes = (uint32_t)ntok * (uint32_t)a.xs;
+    const int k0 = (int)tile.split * a.per, kn = min(a.per, a.ktiles - k0);
+    const uint8_t *wbase = a.tiles + (((int64_t)band * a.ktiles + k0) << 10);
+    const int8_t *xbase = a.x + n0 * a.xs + k0 * 64;
+    const uint32_t wbytes = ((uint32_t)nb * (uint32_t)a.ktiles - k0) << 10, xbytes = (uint32_t)ntok * (uint32_t)a.xs - k0 * 64;
     const uint32_t lds = (uint32_t)(uintptr_t)(w8_lds_void *)w8_lds + wave * (P * STAGE);
     uint32_t off[MB + NB];
 #pragma unroll
@@ -179,7 +214,7 @@ __global__ __launch_bounds__(64 * W) void k_w8_ring(const W8Args a) {
                         : (uint32_t)min((c - MB) * 16 + (lane >> 2), ntok - 1) * (uint32_t)a.xs +
                               (((lane & 3) ^ (-(lane >> 4) & 3)) << 4);
     auto fetch = [&](int t, uint32_t slot) {
-        const uint32_t k = (uint32_t)min(t, a.ktiles - 1);
+        const uint32_t k = (uint32_t)min(t, kn - 1);
 #pragma unroll
         for (int c = 0; c < MB + NB; ++c) {
             const uint32_t dst = lds + slot * STAGE + c * 1024u;
@@ -202,7 +237,7 @@ __global__ __launch_bounds__(64 * W) void k_w8_ring(const W8Args a) {
         fetch(wave + s * W, fill);
         fill = fill + 1 == P ? 0 : fill + 1;
     }
-    for (int t = wave; t < a.ktiles; t += W) {
+    for (int t = wave; t < kn; t += W) {
         w8_wait_vm<(P - 2) * (MB + NB)>();
         w8_i4 A[MB], B[NB];
 #pragma unroll
@@ -230,10 +265,34 @@ __global__ __launch_bounds__(64 * W) void k_w8_ring(const W8Args a) {
 #pragma unroll
             for (int r = 0; r < 4; ++r) atomicAdd(&sums[((i * NB + j) * 4 + r) * 64 + lane], acc[i][j][r]);
     __syncthreads();
-    for (int f = wave; f < MB * NB; f += W) {
+    // the wavefront's blocks of the tile: f = wave, wave + W, ...
+    constexpr uint32_t PART = MB * NB * 1024u;
+    auto block = [&](int f) {
         w8_i4 v;
 #pragma unroll
         for (int r = 0; r < 4; ++r) v[r] = sums[(f * 4 + r) * 64 + lane];
+        return v;
+    };
+    uint8_t *parts = a.parts + (int64_t)(tile.m * a.ntiles + tile.n) * a.splits * PART;
+    if (a.splits > 1) {
+        for (int f = wave; f < MB * NB; f += W)
+            w8_part_store(parts, PART * (uint32_t)a.splits, tile.split * PART + f * 1024u + lane * 16, block(f));
+        if (!w8_last(a, tile)) return;
+    }
+    for (int f = wave; f < MB * NB; f += W) {
+        w8_i4 v = block(f);
+        // the others' parts, eight on their way at once
+        for (int s = 1; s < a.splits; s += 8) {
+            w8_i4 p[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                p[e] = w8_i4{0, 0, 0, 0};
+                if (s + e < a.splits)
+                    p[e] = w8_part_load(parts, PART * (uint32_t)a.splits, w8_other(a, tile, s + e) * PART + f * 1024u + lane * 16);
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v += p[e];
+        }
         if (band + f / NB < a.bands)
             w8_store(a, n0 + f % NB * 16 + (lane & 15), (band + f / NB) * 16 + (lane >> 4) * 4, v);
     }
@@ -247,7 +306,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_w8_tiles(const W8Args a) {
     static_assert(CHUNKS % W == 0, "every wavefront moves as many pieces");
     static_assert(KS == 1 || KS % 2 == 0, "the operands' two sets of registers change places");
     constexpr uint32_t STEP = CHUNKS * 1024u, STAGE = KS * STEP;
-    extern __shared__ uint8_t w8_lds[];
+    extern __shared__ __attribute__((aligned(128))) uint8_t w8_lds[];
     const uint32_t lds = (uint32_t)(uintptr_t)(w8_lds_void *)w8_lds;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const W8Tile tile = w8_tile(a, 8);
@@ -256,9 +315,10 @@ __global__ __launch_bounds__(64 * WM * WN) void k_w8_tiles(const W8Args a) {
     const int64_t n0 = (int64_t)tile.n * (NBLOCKS * 16);
     const int ntok = (int)min((int64_t)(NBLOCKS * 16), a.n - n0);
     const int nb = min(MBANDS, a.bands - band0);
-    const uint8_t *wbase = a.tiles + ((int64_t)band0 * a.ktiles << 10);
-    const int8_t *xbase = a.x + n0 * a.xs;
-    const uint32_t wbytes = (uint32_t)nb * (uint32_t)a.ktiles << 10, xbytes = (uint32_t)ntok * (uint32_t)a.xs;
+    const int k0 = (int)tile.split * a.per, kn = min(a.per, a.ktiles - k0);
+    const uint8_t *wbase = a.tiles + (((int64_t)band0 * a.ktiles + k0) << 10);
+    const int8_t *xbase = a.x + n0 * a.xs + k0 * 64;
+    const uint32_t wbytes = ((uint32_t)nb * (uint32_t)a.ktiles - k0) << 10, xbytes = (uint32_t)ntok * (uint32_t)a.xs - k0 * 64;
     // the pieces of 1 KB this wavefront moves for each 64 columns: chunks wave, wave + W, ...
     uint32_t off[CW];
 #pragma unroll
@@ -276,7 +336,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_w8_tiles(const W8Args a) {
     auto fetch = [&](int t, uint32_t slot) {
 #pragma unroll
         for (int q = 0; q < KS; ++q) {
-            const uint32_t k = (uint32_t)min(t * KS + q, a.ktiles - 1);
+            const uint32_t k = (uint32_t)min(t * KS + q, kn - 1);
 #pragma unroll
             for (int c = 0; c < CW; ++c) {
                 const int chunk = wave + c * W;
@@ -332,7 +392,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_w8_tiles(const W8Args a) {
         for (int q = 0; q + 1 < KS; ++q) {
             const bool odd = q & 1;
             read(slot * STAGE + (q + 1) * STEP, odd ? x : x1, odd ? y : y1);
-            if (q == 0 || t * KS + q < a.ktiles) multiply(odd ? x1 : x, odd ? y1 : y, std::integral_constant<int, 0>{});
+            if (q == 0 || t * KS + q < kn) multiply(odd ? x1 : x, odd ? y1 : y, std::integral_constant<int, 0>{});
         }
         w8_wait_vm<(R - 2) * CW * KS>();      // this wavefront's pieces of stage t + 1, and its reads of stage t
         w8_barrier();                         // every wavefront's
@@ -340,7 +400,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_w8_tiles(const W8Args a) {
         slot = slot + 1 == R ? 0 : slot + 1;
         constexpr bool last = KS > 1;         // (KS even: the last operands lie in the second set, the next in the first)
         read(slot * STAGE, last ? x : x1, last ? y : y1);
-        if (KS == 1 || t * KS + KS - 1 < a.ktiles) multiply(last ? x1 : x, last ? y1 : y, std::integral_constant<int, CW * KS>{});
+        if (KS == 1 || t * KS + KS - 1 < kn) multiply(last ? x1 : x, last ? y1 : y, std::integral_constant<int, CW * KS>{});
     };
 #pragma unroll
     for (int s = 0; s < R; ++s) fetch(s, s);
@@ -349,16 +409,49 @@ __global__ __launch_bounds__(64 * WM * WN) void k_w8_tiles(const W8Args a) {
     read(0, A[0], B[0]);
     int t = 0;
     if constexpr (KS > 1) {
-        for (; t * KS < a.ktiles; ++t) turn(t, A[0], B[0], A[1], B[1]);
+        for (; t * KS < kn; ++t) turn(t, A[0], B[0], A[1], B[1]);
     } else {
-        for (; t + 1 < a.ktiles; t += 2) {
+        for (; t + 1 < kn; t += 2) {
             turn(t, A[0], B[0], A[1], B[1]);
             turn(t + 1, A[1], B[1], A[0], B[0]);
         }
-        if (t < a.ktiles) turn(t, A[0], B[0], A[1], B[1]);
+        if (t < kn) turn(t, A[0], B[0], A[1], B[1]);
     }
     w8_wait_vm<0>();
     w8_barrier();
+    if (a.splits > 1) {
+        constexpr uint32_t PART = MBANDS * NBLOCKS * 1024u;
+        uint8_t *parts = a.parts + (int64_t)(tile.m * a.ntiles + tile.n) * a.splits * PART;
+        const uint32_t all = PART * (uint32_t)a.splits, mine = (uint32_t)(wave * TM * TN) * 1024u + lane * 16;
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+            for (int j = 0; j < TN; ++j)
+                w8_part_store(parts, all, tile.split * PART + mine + (i * TN + j) * 1024u, acc[i][j]);
+        if (!w8_last(a, tile)) return;
+        // the others' parts, as many on their way at once as registers hold
+        constexpr int AT_ONCE = TM * TN <= 4 ? 8 : TM * TN <= 8 ? 4 : TM * TN <= 16 ? 2 : 1;
+        for (int s = 1; s < a.splits; s += AT_ONCE) {
+            w8_i4 p[AT_ONCE][TM][TN];
+#pragma unroll
+            for (int e = 0; e < AT_ONCE; ++e) {
+                const uint32_t from = w8_other(a, tile, s + e) * PART + mine;
+#pragma unroll
+                for (int i = 0; i < TM; ++i)
+#pragma unroll
+                    for (int j = 0; j < TN; ++j) {
+                        p[e][i][j] = w8_i4{0, 0, 0, 0};
+                        if (s + e < a.splits) p[e][i][j] = w8_part_load(parts, all, from + (i * TN + j) * 1024u);
+                    }
+            }
+#pragma unroll
+            for (int e = 0; e < AT_ONCE; ++e)
+#pragma unroll
+                for (int i = 0; i < TM; ++i)
+#pragma unroll
+                    for (int j = 0; j < TN; ++j) acc[i][j] += p[e][i][j];
+        }
+    }
     // The result by way of LDS, 16 tokens at a time in the wavefront's own part of it: a token's TM x 16 channels
     // leave together, 16 bytes a lane.
     constexpr int PITCH = TM * 16 + 8, LPR = TM * 2, RPI = 64 / LPR;      // halves a token, lanes a token, tokens at once
@@ -422,7 +515,7 @@ void w8_allow(Kernel *kernel, unsigned lds, std::atomic<uint64_t> &done) {
 // Launches are for a grid of whole eights (w8_tile).
 unsigned w8_grid(W8Args &a, int bands, int blocks) {
     a.mtiles = (uint32_t)((a.bands + bands - 1) / bands), a.ntiles = (uint32_t)((a.n + blocks * 16 - 1) / (blocks * 16));
-    return (a.mtiles * a.ntiles + 7) / 8 * 8;
+    return (a.mtiles * a.ntiles * (uint32_t)a.splits + 7) / 8 * 8;
 }
 
 template <int W, int U>
@@ -434,48 +527,72 @@ void w8_stream(W8Args &a, hipStream_t stream) {
 template <int NB, int MB, int W, int P>
 void w8_ring(W8Args &a, hipStream_t stream) {
     constexpr unsigned LDS = (MB + NB) * 1024u * P * W;
-    const unsigned grid = w8_grid(a, MB, NB);
     static std::atomic<uint64_t> done{0};
     w8_allow(k_w8_ring<NB, MB, W, P>, LDS, done);
+    const unsigned grid = w8_grid(a, MB, NB);
     hipLaunchKernelGGL((k_w8_ring<NB, MB, W, P>), dim3(grid), dim3(64 * W), LDS, stream, a);
 }
 
 template <int WM, int WN, int TM, int TN, int KS, int R>
 void w8_tiles(W8Args &a, hipStream_t stream) {
     constexpr unsigned LDS = (WM * TM + WN * TN) * 1024u * KS * R;
-    const unsigned grid = w8_grid(a, WM * TM, WN * TN);
     static std::atomic<uint64_t> done{0};
     w8_allow(k_w8_tiles<WM, WN, TM, TN, KS, R>, LDS, done);
+    const unsigned grid = w8_grid(a, WM * TM, WN * TN);
     hipLaunchKernelGGL((k_w8_tiles<WM, WN, TM, TN, KS, R>), dim3(grid), dim3(64 * WM * WN), LDS, stream, a);
 }
 
-struct W8Plan {
+typedef void (*W8Run)(W8Args &, hipStream_t);
+
+struct W8Shape {
     int bands, blocks;       // a workgroup's tile, in 16s
-    void (*run)(W8Args &, hipStream_t);
+    W8Run run;
 };
 
-// By the shape of the tile alone. The first five split K over their wavefronts, the others the tile.
-const W8Plan W8_PLANS[] = {
+// The first six split K over their wavefronts, the others the tile.
+const W8Shape W8_SHAPES[] = {
     {1, 1, w8_ring<1, 1, 8, 4>}, {1, 2, w8_ring<2, 1, 8, 3>}, {2, 2, w8_ring<2, 2, 8, 4>}, {1, 4, w8_ring<4, 1, 4, 4>},
-    {2, 4, w8_ring<4, 2, 8, 3>}, {4, 4, w8_tiles<2, 2, 2, 2, 4, 3>}, {8, 4, w8_tiles<2, 2, 4, 2, 2, 3>},
+    {4, 2, w8_ring<2, 4, 8, 3>}, {2, 4, w8_ring<4, 2, 8, 3>}, {4, 4, w8_tiles<2, 2, 2, 2, 4, 3>}, {8, 4, w8_tiles<2, 2, 4, 2, 2, 3>},
     {8, 8, w8_tiles<2, 4, 4, 2, 1, 4>}, {16, 8, w8_tiles<2, 4, 8, 2, 1, 4>}, {16, 16, w8_tiles<2, 4, 8, 4, 1, 3>},
+};
+
+#define W8_COUNTERS 16384      // arrival counters at the head of a workspace (64 KB, as everywhere in the library)
+#define W8_MOST_TILES ((INT64_C(1) << 31) - 8)
+
+struct W8Plan {
+    W8Run run;
+    int64_t tiles;
+    int splits, per;
+    int64_t part_bytes;      // of all tiles and splits
 };
 
 // A tile's time is that of its operands' way into the CU (a KB of them every 1 / 57 us, whatever the
 // tile) or of its matrix instructions (a 16 x 16 x 64 block every 1 / 330 us), whichever is longer; the tiles of
-// a CU come one after the other.
-void (*w8_plan(int64_t bands, int64_t ktiles, int64_t n))(W8Args &, hipStream_t) {
-    if (n <= 4 && bands * ktiles >= 32768) return bands > 512 && ktiles < 128 ? w8_stream<8, 4> : w8_stream<16, 2>;
-    if (n <= 16 && bands > 256) return w8_ring<1, 1, 4, 4>;
-    const W8Plan *best = nullptr;
+// a CU come one after the other. Splitting K shares a tile among workgroups, which then store and one of which
+// adds the parts: 2.5 us, 1.3 for each, and their bytes at 4 TB/s.
+W8Plan w8_plan(int64_t bands, int64_t ktiles, int64_t n, bool split) {
+    const int k = (int)ktiles;
+    if (k == 0 || (n <= 4 && bands * ktiles >= 32768))
+        return {bands > 512 && ktiles < 128 ? w8_stream<8, 4> : w8_stream<16, 2>, bands * ((n + 15) / 16), 1, k, 0};
+    if (n <= 16 && bands > 256) return {w8_ring<1, 1, 4, 4>, bands, 1, k, 0};
+    W8Plan best{nullptr, 0, 1, k, 0};
     double least = 0.0;
-    for (const W8Plan &p : W8_PLANS) {
+    for (const W8Shape &p : W8_SHAPES) {
         const int64_t tiles = (bands + p.bands - 1) / p.bands * ((n + p.blocks * 16 - 1) / (p.blocks * 16));
         const double one = std::max((p.bands + p.blocks) / 57.0, p.bands * p.blocks / 330.0);
-        const double t = (double)((tiles + 255) / 256) * one;
-        if (best == nullptr || t < least) best = &p, least = t;
+        for (int splits = 1; splits <= 16; splits *= 2) {
+            const int per = (k + splits - 1) / splits, used = (k + per - 1) / per;
+            double t = (double)((tiles * used + 255) / 256) * one * per;
+            int64_t bytes = 0;
+            if (splits > 1) {
+                if (!split || per < 8 || tiles > 256 || tiles > W8_COUNTERS) break;
+                bytes = tiles * used * p.bands * p.blocks * 1024;
+                t += 2.5 + 1.3 * splits + (double)bytes * 0.25e-6;
+            }
+            if (best.run == nullptr || t < least) best = W8Plan{p.run, tiles, used, per, bytes}, least = t;
+        }
     }
-    return best->run;
+    return best;
 }
 
 }  // namespace
@@ -484,6 +601,9 @@ extern "C" int gemm_w8a8_workspace_bytes(int64_t M, int64_t K, int64_t N, int64_
     if (bytes == nullptr || M < 0 || K < 0 || N < 0) return BSP_E_ARG;
     if (K > BSP_W8_MAX_K || M > INT32_MAX || N > INT32_MAX) return BSP_E_OVERFLOW;
     *bytes = 0;
+    if (M == 0 || K == 0 || N == 0) return BSP_OK;
+    const W8Plan p = w8_plan((M + 15) / 16, (K + 63) / 64, N, true);
+    if (p.splits > 1) *bytes = W8_COUNTERS * 4 + p.part_bytes;
     return BSP_OK;
 }
 
@@ -498,11 +618,20 @@ extern "C" int gemm_w8a8_dq(const uint8_t *tiles, int64_t M, int64_t K, const in
     if ((((uintptr_t)tiles | (uintptr_t)X) & 15u) != 0 || ((uintptr_t)Y & 1u) != 0) return BSP_E_ARG;
     if ((((uintptr_t)scale_w | (uintptr_t)scale_x) & 3u) != 0) return BSP_E_ARG;
     if ((workspace == nullptr) != (workspace_bytes == 0) || ((uintptr_t)workspace & 255u) != 0) return BSP_E_ARG;
+    // the tokens of a tile (256 at most) are reached by 32-bit offsets
+    if (K > 0 && x_stride >= INT64_C(1) << 23) return BSP_E_OVERFLOW;
     W8Args a{};
     a.tiles = tiles, a.x = X, a.xs = x_stride, a.scale_w = scale_w, a.scale_x = scale_x, a.y = Y, a.ys = y_stride;
     a.n = N, a.M = (int)M, a.bands = (int)((M + 15) / 16), a.ktiles = (int)((K + 63) / 64);
     a.last = (int)std::max<int64_t>(x_stride - 16, 0);
     a.wide = ((uintptr_t)Y & 7u) == 0 && y_stride % 4 == 0;
-    w8_plan(a.bands, a.ktiles, N)(a, stream);
+    const W8Plan p = w8_plan(a.bands, a.ktiles, N, workspace != nullptr);
+    if (p.tiles > W8_MOST_TILES) return BSP_E_OVERFLOW;
+    a.splits = p.splits, a.per = p.per;
+    if (p.splits > 1) {
+        if (workspace_bytes < W8_COUNTERS * 4 + p.part_bytes) return BSP_E_CAPACITY;
+        a.counters = (uint32_t *)workspace, a.parts = (uint8_t *)workspace + W8_COUNTERS * 4;
+    }
+    p.run(a, stream);
     return hipGetLastError() == hipSuccess ? BSP_OK : BSP_E_HIP;
 }

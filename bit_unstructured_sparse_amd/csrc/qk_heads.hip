@@ -209,14 +209,27 @@ __global__ __launch_bounds__(QK_BLOCK) void k_qk_heads(const QkArgs a, uint32_t 
     }
 }
 
+// A launch holds fewer than 2^32 threads: more tokens go in several.
 template <int D, int U>
-void qk_launch_u(QkArgs &a, hipStream_t stream) {
+void qk_launch_u(const QkArgs &all, hipStream_t stream) {
     constexpr int RUN = 64 / (D / 8) * U;
-    uint32_t total = 0;
-    for (int k = 0; k < 3; ++k) a.parts[k] = total += (uint32_t)((a.heads[k] + RUN - 1) / RUN);
-    const uint32_t items = a.n * total;
-    const unsigned grid = (items + QK_BLOCK / 64 - 1) / (QK_BLOCK / 64);
-    hipLaunchKernelGGL((k_qk_heads<D, U>), dim3(grid), dim3(QK_BLOCK), 0, stream, a, items);
+    uint32_t parts[3], total = 0;
+    for (int k = 0; k < 3; ++k) parts[k] = total += (uint32_t)((all.heads[k] + RUN - 1) / RUN);
+    const uint32_t most = std::max<uint32_t>((UINT32_C(1) << 25) / total, 1);
+    for (uint32_t t = 0; t < all.n; t += std::min(most, all.n - t)) {
+        QkArgs a = all;
+        a.n = std::min(most, all.n - t);
+        for (int k = 0; k < 3; ++k) {
+            a.parts[k] = parts[k];
+            if (a.heads[k] > 0) a.x[k] += t * a.xs[k];
+            if (k < 2 && a.o[k] != nullptr) a.o[k] += t * a.os[k];
+        }
+        if (a.positions != nullptr) a.positions += t;
+        if (a.slots != nullptr) a.slots += t;
+        const uint32_t items = a.n * total;
+        const unsigned grid = (items + QK_BLOCK / 64 - 1) / (QK_BLOCK / 64);
+        hipLaunchKernelGGL((k_qk_heads<D, U>), dim3(grid), dim3(QK_BLOCK), 0, stream, a, items);
+    }
 }
 
 // Heads of 128, many of them: two groups a wavefront (8192 tokens x 64 heads 51.8 us against 61.3, 512 x 80
@@ -224,7 +237,7 @@ void qk_launch_u(QkArgs &a, hipStream_t stream) {
 // (8192 x 40 20.5 against 20.6, with an int8 cache 28.4 against 26.2), nor do those of 256 (23.7 against 25.5, 32.1
 // against 30.9).
 template <int D>
-void qk_launch(QkArgs &a, hipStream_t stream) {
+void qk_launch(const QkArgs &a, hipStream_t stream) {
     if (D == 128 && (int64_t)a.n * (a.heads[0] + a.heads[1] + a.heads[2]) >= 32768)
         qk_launch_u<128, 2>(a, stream);
     else
@@ -234,8 +247,7 @@ void qk_launch(QkArgs &a, hipStream_t stream) {
 int qk_common(QkArgs &a, int64_t n, int64_t hq, int64_t hkv, int64_t D, const bsp_rotation *r, bool values,
               hipStream_t stream) {
     if (D != 64 && D != 128 && D != 256) return BSP_E_UNSUPPORTED;
-    if (hq > INT32_MAX / 4 || hkv > INT32_MAX / 4) return BSP_E_OVERFLOW;
-    // a launch holds fewer than 2^32 threads (2 heads at least per wavefront)
+    if (hq > INT64_C(1) << 20 || hkv > INT64_C(1) << 20) return BSP_E_OVERFLOW;
     if (n >= (INT64_C(1) << 28) / std::max<int64_t>(hq + 2 * hkv, 1)) return BSP_E_OVERFLOW;
     if (r->rot < 0 || r->rot > D || r->rot % 16 != 0) return BSP_E_UNSUPPORTED;
     if (!(r->eps >= 0.0f) || std::isinf(r->eps)) return BSP_E_ARG;

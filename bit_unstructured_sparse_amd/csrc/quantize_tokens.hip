@@ -31,7 +31,7 @@ struct QtArgs {
     float *scale;
     uint8_t *codes;
     int64_t n;
-    int K, K16;             // K16: channels with the zeroed ones behind them
+    int K;
     float eps;
 };
 
@@ -216,9 +216,6 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_quantize(const QtArgs
             give(held[0], k);
         }
     }
-    if constexpr (DTYPE == BSP_INT8)
-        if (k0 < 16)                       // at most 15 bytes: thread 0 the even ones, thread 1 the odd ones
-            for (int k = a.K + k0 / 8; k < a.K16; k += 2) codes[k] = 0;
 }
 
 template <int DTYPE>
@@ -256,11 +253,20 @@ __global__ __launch_bounds__(256) void k_dequantize(const uint8_t *codes, int64_
     qt_store(x + t * xs, k, K, o);
 }
 
+// A launch holds fewer than 2^32 threads: more tokens go in several.
 template <int DTYPE, int TPR, int C>
-void qt_run(const QtArgs &a, hipStream_t stream) {
+void qt_run(const QtArgs &all, hipStream_t stream) {
     constexpr int RPB = TPR < 256 ? 256 / TPR : 1;
-    hipLaunchKernelGGL((k_quantize<DTYPE, TPR, C>), dim3((unsigned)((a.n + RPB - 1) / RPB)), dim3(TPR < 256 ? 256 : TPR), 0,
-                       stream, a);
+    const int64_t most = (INT64_C(1) << 31) / TPR;
+    for (int64_t t = 0; t < all.n; t += most) {
+        QtArgs a = all;
+        a.n = std::min(all.n - t, most);
+        a.x += t * a.xs, a.scale += t, a.codes += t * a.cs;
+        if (a.residual != nullptr) a.residual += t * a.rs, a.hidden += t * a.hs;
+        if (a.x16 != nullptr) a.x16 += t * a.x16s;
+        hipLaunchKernelGGL((k_quantize<DTYPE, TPR, C>), dim3((unsigned)((a.n + RPB - 1) / RPB)), dim3(TPR < 256 ? 256 : TPR),
+                           0, stream, a);
+    }
 }
 
 // One piece a thread while tokens are few (one token of 4096: 3.5 us over 512 threads, 4.4 over 256): most
@@ -319,7 +325,6 @@ extern "C" int quantize_tokens_f16(const bsp_tokens *tokens, int dtype, uint8_t 
     a.x = d->X, a.residual = d->residual, a.weight = d->weight, a.hidden = d->hidden, a.x16 = d->x16;
     a.xs = d->x_stride, a.rs = d->residual_stride, a.hs = d->hidden_stride, a.x16s = d->x16_stride, a.cs = code_stride;
     a.scale = d->scale, a.codes = codes, a.n = d->n, a.K = (int)d->K, a.eps = d->eps;
-    a.K16 = (int)std::min<int64_t>((d->K + 15) / 16 * 16, code_stride);
     if (dtype == BSP_INT8)
         qt_launch<BSP_INT8>(a, stream);
     else
@@ -338,9 +343,13 @@ extern "C" int dequantize_tokens_f16(const uint8_t *codes, int64_t code_stride, 
     if (code_stride < bytes || x_stride < K) return BSP_E_ARG;
     if (((uintptr_t)X & 1u) != 0 || ((uintptr_t)scale & 3u) != 0) return BSP_E_ARG;
     const uint32_t pieces = (uint32_t)((K + 7) / 8);
-    const dim3 grid((unsigned)((n * pieces + 255) / 256)), block(256);
+    const int64_t most = (INT64_C(1) << 31) / pieces;      // fewer than 2^32 threads a launch
     auto run = [&](auto kernel) {
-        hipLaunchKernelGGL(kernel, grid, block, 0, stream, codes, code_stride, scale, n, (int)K, pieces, X, x_stride);
+        for (int64_t t = 0; t < n; t += most) {
+            const int64_t m = std::min(n - t, most);
+            hipLaunchKernelGGL(kernel, dim3((unsigned)((m * pieces + 255) / 256)), dim3(256), 0, stream, codes + t * code_stride,
+                               code_stride, scale + t, m, (int)K, pieces, X + t * x_stride, x_stride);
+        }
     };
     if (dtype == BSP_INT8)
         run(k_dequantize<BSP_INT8>);

@@ -713,7 +713,8 @@ typedef struct bsp_rotation {
  *   Qo, Ko       the results, with strides of their own; may be Q, K with their strides,
  *                and must not overlap the inputs otherwise.
  *   head_dim     64, 128 or 256 (BSP_E_UNSUPPORTED otherwise).
- * n * (q_heads + 2 kv_heads) >= 2^28 is refused (BSP_E_OVERFLOW), here and below.
+ * n * (q_heads + 2 kv_heads) >= 2^28 and more than 2^20 heads are refused (BSP_E_OVERFLOW),
+ * here and below.
  */
 int qk_norm_rope_f16(const uint16_t *Q, int64_t q_stride, const uint16_t *K, int64_t k_stride, int64_t n,
                      int64_t q_heads, int64_t kv_heads, int64_t head_dim, const bsp_rotation *rotation, uint16_t *Qo,
@@ -760,8 +761,9 @@ typedef struct bsp_tokens {
  *   tokens       HOST descriptor (read during the call only).
  *   dtype        BSP_INT8: codes int8, token t at byte t * code_stride; BSP_INT4: packed as
  *                pack_int4_activations does (an odd K leaves the last high nibble zero).
- *   codes        DEVICE; code_stride >= K (int8) or ceil(K / 2) (int4). Bytes between a
- *                token's codes and the next multiple of 16 inside the stride are zeroed (int8).
+ *   codes        DEVICE; code_stride >= K (int8) or ceil(K / 2) (int4). What lies between a token's
+ *                codes and the next token's is left as it is.
+ * n == 0 or K == 0 launches nothing.
  */
 int quantize_tokens_f16(const bsp_tokens *tokens, int dtype, uint8_t *codes, int64_t code_stride, hipStream_t stream);
 
@@ -804,7 +806,7 @@ int gemm_w8a8_workspace_bytes(int64_t M, int64_t K, int64_t N, int64_t *bytes);
  *                bytes, 256-byte aligned, zero-filled before its first use (its first 64 KiB hold
  *                arrival counters, left zero by every call: a workspace of the other entry points
  *                will do). Too small: BSP_E_CAPACITY. Calls that share one must be ordered.
- * K > BSP_W8_MAX_K, M >= 2^31, N >= 2^31: BSP_E_OVERFLOW. K == 0 gives zeros. The result does not
+ * K > BSP_W8_MAX_K, M >= 2^31, N >= 2^31, x_stride >= 2^23: BSP_E_OVERFLOW. K == 0 gives zeros. The result does not
  * depend on timing or on the workspace.
  */
 int gemm_w8a8_dq(const uint8_t *tiles, int64_t M, int64_t K, const int8_t *X, int64_t x_stride, int64_t N,

@@ -98,9 +98,7 @@ def test_strided_rows_and_sums_in_place(dtype, K, off, dev):
     keep = torch.ones(pitch, dtype=torch.bool, device=dev)
     keep[off:off + K] = False
     assert torch.equal(res[:, keep], before[:, keep])
-    # int8: zeros up to the next multiple of 16, nothing past it
-    end = -(-K // 16) * 16 if dtype == bsp.INT8 else bytes_
-    assert (store[:, end:] == 99).all() and not store[:, bytes_:end].any()
+    assert (store[:, bytes_:] == 99).all()
     back = torch.zeros((n, pitch), dtype=torch.float16, device=dev)
     bsp.dequantize_tokens(t.codes, t.scale, dtype, K, X=back[:, off:off + K])
     assert torch.equal(back[:, off:off + K], bsp.dequantize_tokens(t.codes, t.scale, dtype, K))
