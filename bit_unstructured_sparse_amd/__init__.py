@@ -872,7 +872,7 @@ def kv_gather(cache: KVCache, slots, K=None, V=None, stream=None):
     if K is None:
         K = _new_output((n, heads, dim), torch.float16, cache.device, stream)
     if V is None:
-        V = torch.empty_like(K) if stream is None else _new_output((n, heads, dim), torch.float16, cache.device, stream)
+        V = _new_output((n, heads, dim), torch.float16, cache.device, stream)
     ks, vs = _rows(K, "K", n, heads, dim, index), _rows(V, "V", n, heads, dim, index)
     rc = _launch(load_library().kv_cache_gather, index, stream, cache._ref, at, n, K.data_ptr(), ks, V.data_ptr(), vs)
     _check(rc, "kv_cache_gather")

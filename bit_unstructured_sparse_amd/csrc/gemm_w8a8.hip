@@ -3,7 +3,24 @@
 // v_mfma_i32_16x16x64_i8: a lane brings 16 bytes of one row of W (its tile in memory is
 // in lane order) and 16 bytes of one token, and holds 4 neighbouring channels of
 // one token of the result. Sums are int32 and exact, so the order in which parts of K
-// meet changes nothing.
+// meet changes nothing: K is split over wavefronts and workgroups wherever that is faster,
+// and every plan gives the same bits.
+//
+// Three kernels. For at most 4 tokens and weights of 32 MB and more W streams past LDS into registers
+// (k_w8_stream). Up to a few hundred tokens a tile is small and its wavefronts share K: each fills and reads a
+// ring of its own in LDS by DMA, so that no barrier stands between memory and the matrix instructions
+// (k_w8_ring). Past that a workgroup's wavefronts share the tile and a ring (k_w8_tiles).
+//
+// What bounds them. A CU takes in about 57 KB/us (24 bytes a cycle) of operands, from any level past its
+// L1 and however many are on their way: the time of all but the largest tiles is (bands + blocks) KB per 64
+// columns at that rate (N = 128, 4096 x 4096, 64 x 64 tiles: 8 KB a step, 0.14 us; rings 4 to 16 stages deep
+// within 3 % of each other). It is why tiles are chosen by their bytes, and why four bands and two blocks beat one and
+// four. The 256 x 256 tiles are bound by the matrix cores and the power they draw: 8192 tokens x 12288 x 4096, 332
+// us (2,480 TOP/s), 62 % of the cycles in matrix instructions at 1.92 GHz, LDS reads and the DMA's writes taking as many
+// cycles as those. What brought them there from 600 us: operands read one step ahead into a second set of registers
+// (with the scheduler told to spread the reads: left alone it sinks them behind all matrix instructions),
+// a swizzle that leaves no bank conflict (440 to 385 us), three stages rather than four (less power), the result
+// through LDS in whole rows (366 to 332). 4 wavefronts of 128 x 128 need 512 registers and hide no latency: 490 us.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -35,7 +52,6 @@ struct W8Args {
     uint8_t *parts;          // and their sums
     int last;                // last 16-byte piece of a token's row, as a byte offset
     uint32_t mtiles, ntiles; // tiles of the result
-    bool wide;               // 8-byte stores: Y and its rows lie on that boundary
 };
 
 // 4 neighbouring channels m .. m + 3 of token n.
@@ -43,11 +59,11 @@ __device__ __forceinline__ void w8_store(const W8Args &a, int64_t n, int m, w8_i
     if (n >= a.n || m >= a.M) return;
     const float sx = a.scale_x[n];
     uint16_t *y = a.y + n * a.ys + m;
-    if (a.wide && m + 3 < a.M) {
+    if (m + 3 < a.M) {
         uint16_t h[4];
 #pragma unroll
         for (int r = 0; r < 4; ++r) h[r] = bsp_f2h(bsp_rounded((float)v[r] * a.scale_w[m + r] * sx));
-        *reinterpret_cast<w8_u2 *>(y) = w8_u2{h[0] | ((uint32_t)h[1] << 16), h[2] | ((uint32_t)h[3] << 16)};
+        __builtin_memcpy(y, h, 8);      // (at any 2-byte address)
     } else {
 #pragma unroll
         for (int r = 0; r < 4; ++r)
@@ -103,72 +119,51 @@ __device__ __forceinline__ bool w8_last(const W8Args &a, const W8Tile &tile) {
     return true;
 }
 
-// ---- few tokens: W streams from memory straight into registers ----
+// ---- at most 16 tokens: W streams from memory straight into registers ----
 
-// A workgroup owns MB bands of 16 channels and NB blocks of 16 tokens; its W wavefronts
-// take every W-th column tile of K and meet in LDS.
-template <int NB, int MB, int W, int U>
+// A workgroup owns a band of 16 channels; its W wavefronts take every W-th column tile of K, U of them
+// on their way at once, and meet in LDS. W is read once: marked so, it costs the last-level cache nothing (one
+// token x 12288 x 4096, cold: 10.0 us, through a ring 11.5).
+template <int W, int U>
 __global__ __launch_bounds__(64 * W) void k_w8_stream(const W8Args a) {
-    __shared__ int32_t sums[MB * NB * 256];
+    __shared__ int32_t sums[256];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const W8Tile tile = w8_tile(a, 1);
     if (tile.m >= a.mtiles) return;
-    const int band = (int)tile.m * MB;
-    const int64_t n0 = (int64_t)tile.n * (NB * 16);
-    const uint8_t *w[MB];
-#pragma unroll
-    for (int i = 0; i < MB; ++i) w[i] = a.tiles + ((int64_t)min(band + i, a.bands - 1) * a.ktiles << 10) + lane * 16;
-    const int8_t *x[NB];
-#pragma unroll
-    for (int j = 0; j < NB; ++j) x[j] = a.x + min(n0 + j * 16 + (lane & 15), a.n - 1) * a.xs;
+    const int64_t n = (int64_t)tile.n * 16 + (lane & 15);
+    const uint8_t *w = a.tiles + ((int64_t)tile.m * a.ktiles << 10) + lane * 16;
+    const int8_t *x = a.x + min(n, a.n - 1) * a.xs;
     const int piece = (lane >> 4) * 16;
-    w8_i4 acc[MB][NB];
-#pragma unroll
-    for (int i = 0; i < MB; ++i)
-#pragma unroll
-        for (int j = 0; j < NB; ++j) acc[i][j] = w8_i4{0, 0, 0, 0};
-    for (int i = threadIdx.x; i < MB * NB * 256; i += 64 * W) sums[i] = 0;
+    w8_i4 acc = {0, 0, 0, 0};
+    if (threadIdx.x < 256) sums[threadIdx.x] = 0;
     auto step = [&](int t, auto count) {
         constexpr int C = decltype(count)::value;
-        w8_i4 A[C][MB], B[C][NB];
+        w8_i4 A[C], B[C];
 #pragma unroll
         for (int u = 0; u < C; ++u) {
             const int k = t + u * W;
-#pragma unroll
-            for (int i = 0; i < MB; ++i) A[u][i] = __builtin_nontemporal_load(reinterpret_cast<const w8_i4 *>(w[i] + ((int64_t)k << 10)));
-#pragma unroll
-            for (int j = 0; j < NB; ++j)     // past the row's last piece W is zero: any value will do
-                B[u][j] = *reinterpret_cast<const w8_i4 *>(x[j] + min(k * 64 + piece, a.last));
+            A[u] = __builtin_nontemporal_load(reinterpret_cast<const w8_i4 *>(w + ((int64_t)k << 10)));
+            // past the row's last piece W is zero: any value will do
+            B[u] = *reinterpret_cast<const w8_i4 *>(x + min(k * 64 + piece, a.last));
         }
 #pragma unroll
-        for (int u = 0; u < C; ++u)
-#pragma unroll
-            for (int i = 0; i < MB; ++i)
-#pragma unroll
-                for (int j = 0; j < NB; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(A[u][i], B[u][j], acc[i][j], 0, 0, 0);
+        for (int u = 0; u < C; ++u) acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(A[u], B[u], acc, 0, 0, 0);
     };
     int t = wave;
     for (; t + (U - 1) * W < a.ktiles; t += U * W) step(t, std::integral_constant<int, U>{});
     for (; t < a.ktiles; t += W) step(t, std::integral_constant<int, 1>{});
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < MB; ++i)
-#pragma unroll
-        for (int j = 0; j < NB; ++j)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) atomicAdd(&sums[((i * NB + j) * 4 + r) * 64 + lane], acc[i][j][r]);
+    for (int r = 0; r < 4; ++r) atomicAdd(&sums[r * 64 + lane], acc[r]);
     __syncthreads();
-    for (int f = wave; f < MB * NB; f += W) {
-        w8_i4 v;
+    if (wave != 0) return;
+    w8_i4 v;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) v[r] = sums[(f * 4 + r) * 64 + lane];
-        if (band + f / NB < a.bands)
-            w8_store(a, n0 + f % NB * 16 + (lane & 15), (band + f / NB) * 16 + (lane >> 4) * 4, v);
-    }
+    for (int r = 0; r < 4; ++r) v[r] = sums[r * 64 + lane];
+    w8_store(a, n, (int)tile.m * 16 + (lane >> 4) * 4, v);
 }
 
-// ---- many tokens: both operands through LDS ----
+// ---- more tokens: both operands through LDS ----
 
 __device__ __forceinline__ void w8_barrier() {
     asm volatile("" ::: "memory");
@@ -521,7 +516,7 @@ unsigned w8_grid(W8Args &a, int bands, int blocks) {
 template <int W, int U>
 void w8_stream(W8Args &a, hipStream_t stream) {
     const unsigned grid = w8_grid(a, 1, 1);
-    hipLaunchKernelGGL((k_w8_stream<1, 1, W, U>), dim3(grid), dim3(64 * W), 0, stream, a);
+    hipLaunchKernelGGL((k_w8_stream<W, U>), dim3(grid), dim3(64 * W), 0, stream, a);
 }
 
 template <int NB, int MB, int W, int P>
@@ -624,7 +619,6 @@ extern "C" int gemm_w8a8_dq(const uint8_t *tiles, int64_t M, int64_t K, const in
     a.tiles = tiles, a.x = X, a.xs = x_stride, a.scale_w = scale_w, a.scale_x = scale_x, a.y = Y, a.ys = y_stride;
     a.n = N, a.M = (int)M, a.bands = (int)((M + 15) / 16), a.ktiles = (int)((K + 63) / 64);
     a.last = (int)std::max<int64_t>(x_stride - 16, 0);
-    a.wide = ((uintptr_t)Y & 7u) == 0 && y_stride % 4 == 0;
     const W8Plan p = w8_plan(a.bands, a.ktiles, N, workspace != nullptr);
     if (p.tiles > W8_MOST_TILES) return BSP_E_OVERFLOW;
     a.splits = p.splits, a.per = p.per;

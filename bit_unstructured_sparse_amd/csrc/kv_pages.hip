@@ -6,15 +6,18 @@
 // over the first finds, the n-th page taken to the one that a search over the
 // second finds, and the page it gets is the n-th given back (a search over the
 // third) or an entry of the list. So one launch does it, without an order between
-// workgroups: each one computes the sums for itself, in LDS (2 KB of lengths
-// for 128 sequences, from L2), and then its share of the rows and pages.
+// workgroups: each one computes the sums for itself, into LDS (20 bytes a sequence),
+// and then its share of the rows and pages.
 //
 // In place, without a race: what a call writes (table entries past the held ones of
 // growing sequences, list entries at and past the count) no workgroup of it
 // reads; what all of them read (lens, held, the count) is written by the last
 // workgroup to finish, which an arrival counter beside the count names.
 //
-// Bound by latency: two launches' worth of dependent loads (lengths, then table).
+// Bound by latency: four dependent trips to memory (lengths; a row's page; an arrival; the
+// state) beside an empty launch's 1.8 us. 32 sequences of one token 3.7 us, 256 with trees
+// (7,700 rows) 5.2 us, 512 with prompts (62,000 rows) 9.6 us (at most 256 workgroups: with 64
+// 12.5, with 1024 11.2; with a fence before the arrival 16).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
