@@ -40,6 +40,23 @@ __device__ __forceinline__ void kv_store8(uint16_t *p, kv_u4 v) {
     }
 }
 
+template <int CTRL>
+__device__ __forceinline__ float kv_dpp(float v) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xF, 0xF, true));
+}
+
+// The value of the neighbouring run of d lanes, where all lanes of a run hold the same: the steps of a reduction over
+// a row's lanes. Up to 16 lanes a move within the vector unit, not a trip through LDS.
+__device__ __forceinline__ float kv_other(float v, int d) {
+    switch (d) {
+        case 1: return kv_dpp<0xB1>(v);       // within four lanes
+        case 2: return kv_dpp<0x4E>(v);
+        case 4: return kv_dpp<0x141>(v);      // eight lanes mirrored
+        case 8: return kv_dpp<0x140>(v);      // sixteen mirrored
+        default: return __shfl_xor(v, d, 64);
+    }
+}
+
 // Quantise the 8 values of a lane; the row's lanes are LPR neighbours.
 // (x - o) / s is needed correctly rounded, so that a value half way between
 // two codes goes to the even one: with r the correctly rounded reciprocal of
@@ -60,9 +77,9 @@ __device__ __forceinline__ void kv_quantise(kv_u4 raw, float levels, uint32_t (&
     for (int i = 0; i < 4; ++i) big = max(big, max(raw[i] & 0x7FFFu, (raw[i] >> 16) & 0x7FFFu));
 #pragma unroll
     for (int d = 1; d < LPR; d <<= 1) {
-        lo = fminf(lo, __shfl_xor(lo, d, 64));
-        hi = fmaxf(hi, __shfl_xor(hi, d, 64));
-        big = max(big, (uint32_t)__shfl_xor((int)big, d, 64));
+        lo = fminf(lo, kv_other(lo, d));
+        hi = fmaxf(hi, kv_other(hi, d));
+        big = max(big, __builtin_bit_cast(uint32_t, kv_other(__builtin_bit_cast(float, big), d)));
     }
     if (big >= 0x7C00u) {      // an infinity or a NaN in the row
         word = 0x7FC07E00u;

@@ -6,17 +6,27 @@
 // heads of one token and one kind (query, key or value), in U such groups.
 //
 // The angle of pair i at position p is p * freq[i] turns, freq in units of 2^-64
-// turns: the product mod 2^64 is the angle mod one turn, exactly. Its upper 32 bits
-// (2^-32 turns) are split into a multiple of a quarter turn and a rest of at most an
-// eighth, whose sine and cosine are their Taylor sums to x^9 and x^8: at most
-// 2^-24.9 off (the first term left out, (pi/4)^10 / 10!). A wavefront computes each of its token's
-// angles once, a pair a lane, and shares them through LDS; the norm's weights are multiplied into
-// them, so that a channel is x own + other pair, times 1 / sqrt(mean + eps) at the end.
+// turns: the product mod 2^64 is the angle mod one turn, exactly. Split into a multiple
+// of a quarter turn and a rest x of at most an eighth, its sine and cosine are Taylor
+// sums to x^13 and x^12 (the first terms left out are 2^-45 and 2^-41), the leading
+// terms in 64 bits, the others, under 2^-14, in 32: both come out as the nearest float
+// but where they lie within 2^-11 of a step from the middle of two. A wavefront
+// computes each of its token's angles once, a pair a lane, and shares them through LDS.
+//
+// Everything between the input and the result is 32-bit, each operation rounded once and none contracted, in the
+// order of the definition: y = x / sqrt(mean + eps), a correctly rounded quotient (rc = 1 / r,
+// q = fma(fma(-q0, r, x), rc, q0), q0 = x rc, Markstein), times w, then y1 c - y2 s and y2 c + y1 s. A key whose
+// fp16 neighbour would do as well still lands in another code of an int4 row, a sixteenth of the row's range: an
+// evaluation in the plain order gives the same codes but for one result in 10^7. (A form with w and the norm folded
+// into the sines, within 2^-24 of the definition too, differed from it in 1.3 results of 10^4, at the same speed.)
+// The mean's squares are added as a 16-byte piece holds them, its halves of four in turn (heads of 64: neighbours
+// first), then the lanes' sums neighbours first.
 //
 // Bound by memory where tokens are many: 8192 tokens, 32 query and 32 key heads of 128, 268 MB in 51.8 us
-// (5.2 TB/s); with values into an fp16 cache 403 MB in 75 us (5.4 TB/s). Into an int8 cache 336 MB take 84 us: a row's
+// (5.2 TB/s); with values into an fp16 cache 403 MB in 76 us (5.3 TB/s). Into an int8 cache 336 MB take 86 us: a row's
 // minimum, maximum and codes cost as many vector instructions as the rotation, and no longer hide. (With each lane its
-// own 8 angles a group: 84 and 127 us.) Few tokens are launch latency: 3.7 us, 4.1 with an int8 cache.
+// own 8 angles a group: 84 and 127 us. With 64-bit sines throughout 55 and 91.) Few tokens are launch latency: 3.8 us,
+// 4.2 with an int8 cache.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -48,29 +58,28 @@ struct QkArgs {
     int kind, page_shift, rot, interleaved;
 };
 
-// sin and cos of u * 2^-32 turns.
-__device__ __forceinline__ void qk_sincos(uint32_t u, float &s, float &c) {
-    const uint32_t q = (u + 0x20000000u) >> 30;              // nearest quarter
-    const float x = (float)(int32_t)(u - (q << 30)) * 1.4629180792671596e-9f;     // 2 pi / 2^32
-    const float z = x * x;
-    float sn = __builtin_fmaf(z, 2.7557319223985893e-6f, -1.984126984126984e-4f);
-    sn = __builtin_fmaf(z, sn, 8.333333333333333e-3f);
-    sn = __builtin_fmaf(z, sn, -0.16666666666666666f);
-    sn = __builtin_fmaf(z * x, sn, x);
-    float cs = __builtin_fmaf(z, 2.48015873015873e-5f, -1.388888888888889e-3f);
-    cs = __builtin_fmaf(z, cs, 4.1666666666666664e-2f);
-    cs = __builtin_fmaf(z, cs, -0.5f);
-    cs = __builtin_fmaf(z, cs, 1.0f);
-    s = (q & 1) ? cs : sn;
-    c = (q & 1) ? sn : cs;
+// sin and cos of t * 2^-64 turns, rounded to 32 bits.
+__device__ __forceinline__ void qk_sincos(uint64_t t, float &s, float &c) {
+    const uint32_t q = (uint32_t)((t + (UINT64_C(1) << 61)) >> 62);              // nearest quarter
+    const double x = (double)(int64_t)(t - ((uint64_t)q << 62)) * 3.4061215800865545e-19;      // 2 pi / 2^64
+    const double z = x * x;
+    const float y = (float)z;
+    float ps = __builtin_fmaf(y, 1.6059043836821613e-10f, -2.505210838544172e-8f);
+    ps = __builtin_fmaf(y, ps, 2.7557319223985893e-6f);
+    ps = __builtin_fmaf(y, ps, -1.984126984126984e-4f);
+    double sn = __builtin_fma(z, (double)ps, 8.333333333333333e-3);
+    sn = __builtin_fma(z, sn, -0.16666666666666666);
+    sn = __builtin_fma(z * x, sn, x);
+    float pc = __builtin_fmaf(y, 2.08767569878681e-9f, -2.755731922398589e-7f);
+    pc = __builtin_fmaf(y, pc, 2.48015873015873e-5f);
+    pc = __builtin_fmaf(y, pc, -1.388888888888889e-3f);
+    double cs = __builtin_fma(z, (double)pc, 4.1666666666666664e-2);
+    cs = __builtin_fma(z, cs, -0.5);
+    cs = __builtin_fma(z, cs, 1.0);
+    s = (float)((q & 1) ? cs : sn);
+    c = (float)((q & 1) ? sn : cs);
     if (q & 2) s = -s;
     if ((q + 1) & 2) c = -c;
-}
-
-// The upper 32 bits of p * f mod 2^64, p signed.
-__device__ __forceinline__ uint32_t qk_turn(int32_t p, uint64_t f) {
-    const uint32_t lo = (uint32_t)f, hi = (uint32_t)(f >> 32);
-    return (uint32_t)p * hi + __umulhi((uint32_t)p, lo) - (p < 0 ? lo : 0);
 }
 
 // 8 values at any 2-byte address: the memory takes 16 bytes anywhere.
@@ -106,51 +115,35 @@ __global__ __launch_bounds__(QK_BLOCK) void k_qk_heads(const QkArgs a, uint32_t 
     }
     const int rot = kind == 2 ? 0 : a.rot, half = rot / 2;
     const uint16_t *weight = kind == 2 ? nullptr : a.weight[kind];
-    // y = (x own + other pair) / sqrt(mean + eps): own and pair hold weight times cosine and sine
-    float own[8], pair[8];
+    float cs[8], sn[8];
+    kv_h8 w;
     int partner = lane;
-    if (kind != 2) {
-        const bool upper = !a.interleaved && ch >= half, turned = ch < rot;
-        if (!a.interleaved && turned) partner = upper ? lane - half / 8 : lane + half / 8;
-        kv_h8 w, wp;
+    const bool turned = ch < rot;
+    if (weight != nullptr) w = __builtin_bit_cast(kv_h8, *reinterpret_cast<const kv_u4 *>(weight + ch));
+    if (rot > 0) {
+        // each pair's angle once for the wavefront, by way of its own LDS
+        const int32_t p = a.positions[token];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) w[e] = wp[e] = (_Float16)1.0f;
-        if (weight != nullptr) {
-            w = __builtin_bit_cast(kv_h8, *reinterpret_cast<const kv_u4 *>(weight + ch));
-            wp = __builtin_bit_cast(kv_h8, *reinterpret_cast<const kv_u4 *>(weight + (partner - lane) * 8 + ch));
+        for (int i = 0; i < D / 2; i += 64) {
+            const int j = i + lane;
+            if (j < half) qk_sincos((uint64_t)(int64_t)p * a.freq[j], turns[wave][1][j], turns[wave][0][j]);
         }
+        __builtin_amdgcn_wave_barrier();
+        const bool upper = !a.interleaved && ch >= half;
+        if (turned && a.interleaved) {
+            const qk_f4 c = *reinterpret_cast<const qk_f4 *>(&turns[wave][0][ch / 2]);
+            const qk_f4 s = *reinterpret_cast<const qk_f4 *>(&turns[wave][1][ch / 2]);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) own[e] = (float)w[e], pair[e] = 0.0f;
-        if (rot > 0) {
-            // each pair's angle once for the wavefront, by way of its own LDS
-            const int32_t p = a.positions[token];
+            for (int e = 0; e < 8; ++e) cs[e] = c[e / 2], sn[e] = (e & 1) ? s[e / 2] : -s[e / 2];
+        } else if (turned) {
+            partner = upper ? lane - half / 8 : lane + half / 8;
+            const int i0 = upper ? ch - half : ch;
 #pragma unroll
-            for (int i = 0; i < D / 2; i += 64) {
-                const int j = i + lane;
-                if (j < half) qk_sincos(qk_turn(p, a.freq[j]), turns[wave][1][j], turns[wave][0][j]);
-            }
-            __builtin_amdgcn_wave_barrier();
-            if (turned && a.interleaved) {
-                const qk_f4 c = *reinterpret_cast<const qk_f4 *>(&turns[wave][0][ch / 2]);
-                const qk_f4 s = *reinterpret_cast<const qk_f4 *>(&turns[wave][1][ch / 2]);
+            for (int q = 0; q < 2; ++q) {
+                const qk_f4 c = *reinterpret_cast<const qk_f4 *>(&turns[wave][0][i0 + 4 * q]);
+                const qk_f4 s = *reinterpret_cast<const qk_f4 *>(&turns[wave][1][i0 + 4 * q]);
 #pragma unroll
-                for (int e = 0; e < 8; e += 2) {
-                    const float w1 = own[e], w2 = own[e + 1];
-                    own[e] = w1 * c[e / 2], pair[e] = -w2 * s[e / 2];
-                    own[e + 1] = w2 * c[e / 2], pair[e + 1] = w1 * s[e / 2];
-                }
-            } else if (turned) {
-                const int i0 = upper ? ch - half : ch;
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    const qk_f4 c = *reinterpret_cast<const qk_f4 *>(&turns[wave][0][i0 + 4 * q]);
-                    const qk_f4 s = *reinterpret_cast<const qk_f4 *>(&turns[wave][1][i0 + 4 * q]);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        own[4 * q + e] *= c[e];
-                        pair[4 * q + e] = (float)wp[4 * q + e] * (upper ? s[e] : -s[e]);
-                    }
-                }
+                for (int e = 0; e < 4; ++e) cs[4 * q + e] = c[e], sn[4 * q + e] = upper ? s[e] : -s[e];
             }
         }
     }
@@ -163,31 +156,41 @@ __global__ __launch_bounds__(QK_BLOCK) void k_qk_heads(const QkArgs a, uint32_t 
         const int h = first + i * RPW + lane / LPR;
         const bool live = h < heads;
         if (kind != 2) {
+#pragma clang fp contract(off)
             const kv_h8 x = __builtin_bit_cast(kv_h8, raw[i]);
             float y[8];
-            if (rot > 0 && !a.interleaved) {
-                kv_u4 there;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) there[e] = ch < rot ? (uint32_t)__shfl((int)raw[i][e], partner, 64) : 0u;
-                const kv_h8 z = __builtin_bit_cast(kv_h8, there);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) y[e] = __builtin_fmaf((float)z[e], pair[e], (float)x[e] * own[e]);
-            } else if (ch < rot) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) y[e] = __builtin_fmaf((float)x[e ^ 1], pair[e], (float)x[e] * own[e]);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) y[e] = (float)x[e] * own[e];
-            }
+            for (int e = 0; e < 8; ++e) y[e] = (float)x[e];
             if (weight != nullptr) {
-                float sum = 0.0f;
+                float sum;
+                if constexpr (D == 64)
+                    sum = ((y[0] * y[0] + y[1] * y[1]) + (y[2] * y[2] + y[3] * y[3])) +
+                          ((y[4] * y[4] + y[5] * y[5]) + (y[6] * y[6] + y[7] * y[7]));
+                else
+                    sum = (((y[0] * y[0] + y[1] * y[1]) + y[2] * y[2]) + y[3] * y[3]) +
+                          (((y[4] * y[4] + y[5] * y[5]) + y[6] * y[6]) + y[7] * y[7]);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) sum = __builtin_fmaf((float)x[e], (float)x[e], sum);
+                for (int d = 1; d < LPR; d <<= 1) sum += kv_other(sum, d);
+                const float r = sqrtf(sum * (1.0f / D) + a.eps), rc = 1.0f / r, rz = r < INFINITY ? r : 0.0f;
 #pragma unroll
-                for (int d = 1; d < LPR; d <<= 1) sum += __shfl_xor(sum, d, 64);
-                const float r = __builtin_amdgcn_rsqf(__builtin_fmaf(sum, 1.0f / D, a.eps));
+                for (int e = 0; e < 8; ++e) {
+                    const float q0 = y[e] * rc;
+                    y[e] = __builtin_fmaf(__builtin_fmaf(-q0, rz, y[e]), rc, q0) * (float)w[e];
+                }
+            }
+            if (rot > 0 && !a.interleaved) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) y[e] *= r;
+                for (int e = 0; e < 8; ++e) {
+                    const float other = __shfl(y[e], partner, 64);
+                    if (turned) y[e] = y[e] * cs[e] + other * sn[e];
+                }
+            } else if (turned) {
+#pragma unroll
+                for (int e = 0; e < 8; e += 2) {
+                    const float y1 = y[e], y2 = y[e + 1];
+                    y[e] = y1 * cs[e] + y2 * sn[e];
+                    y[e + 1] = y2 * cs[e + 1] + y1 * sn[e + 1];
+                }
             }
 #pragma unroll
             for (int e = 0; e < 4; ++e)
@@ -237,10 +240,10 @@ void qk_launch_u(const QkArgs &all, hipStream_t stream) {
     }
 }
 
-// Heads of 128, many of them: two groups a wavefront (8192 tokens x 64 heads 51.8 us against 61.3, 512 x 80
-// 7.4 against 7.8, 128 x 80 5.0 against 4.5; four groups 50.1, 8.0, 5.9). Heads of 64, 8 to a group, gain nothing
-// (8192 x 40 20.5 against 20.6, with an int8 cache 28.4 against 26.2), nor do those of 256 (23.7 against 25.5, 32.1
-// against 30.9).
+// Heads of 128, many of them: two groups a wavefront (8192 tokens x 64 heads 51.8 us against 62.9, into an int8 cache
+// 86 against 104; 512 x 64 6.8 against 7.1, 512 x 80 7.5 against 7.7; 128 x 80 5.0 against 4.4). Heads of 64, 8 to
+// a group, gain nothing (8192 x 40 20.5 against 20.6, with an int8 cache 28.4 against 26.2), nor do those of 256 (23.7
+// against 25.5, 32.1 against 30.9).
 template <int D>
 void qk_launch(const QkArgs &a, hipStream_t stream) {
     if (D == 128 && (int64_t)a.n * (a.heads[0] + a.heads[1] + a.heads[2]) >= 32768)
