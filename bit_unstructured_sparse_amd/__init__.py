@@ -1068,11 +1068,10 @@ class _KVPagesDesc(ctypes.Structure):
 
 @dataclass(frozen=True)
 class KVPages:
-    """Which pages of a cache each sequence holds, in device memory and updated
-    there by kv_step (the tensors' contents change, the tensors do not): block_table int32 [B][width] (as attention_tree takes it), lens
-    int32 [B] tokens cached, held int32 [B] pages held, free int32 [2 + pool]: the number of
-    free pages, a counter of the call's own (0), the free pages (the next to be
-    taken last)."""
+    """Which pages of a cache each sequence holds, in device memory and updated there by kv_step: block_table int32
+    [B][width] (as attention_tree takes it), lens int32 [B] tokens cached, held int32 [B] pages held, free int32
+    [2 + pool]: the number of free pages, a counter of the call's own (0), the free pages (the next to be taken last).
+    Calls on the same pages must be ordered on one stream."""
     block_table: "object"
     lens: "object"
     held: "object"
@@ -1094,8 +1093,18 @@ class KVPages:
         desc = _KVPagesDesc(B, width, self.page_size, self.free.numel() - 2, _dptr(self.block_table), _dptr(self.lens),
                             _dptr(self.held), _dptr(self.free))
         for name, value in (("sequences", B), ("width", width), ("device", self.block_table.device),
-                            ("_index", index), ("_desc", desc), ("_ref", ctypes.addressof(desc))):
+                            ("_index", index), ("_desc", desc), ("_ref", ctypes.addressof(desc)),
+                            ("_at", self._addresses())):
             object.__setattr__(self, name, value)
+
+    def _addresses(self):
+        return (self.block_table.data_ptr(), self.lens.data_ptr(), self.held.data_ptr(), self.free.data_ptr())
+
+    def _pointer(self):
+        """The descriptor; a tensor given another storage is taken up, and checked, by the next call."""
+        if self._addresses() != self._at:
+            self.__post_init__()
+        return self._ref
 
 
 def new_kv_pages(sequences: int, width: int, num_pages: int, page_size: int, device="cuda") -> KVPages:
@@ -1130,8 +1139,8 @@ def kv_step(pages: KVPages, keep, new_tokens, rows: int, tree_mask=None, out: Op
     whose pages (or rows) do not fit waits: its slots are -1 and its kv_lens 0, and it keeps its kept tokens. Rows behind
     the last sequence get slot -1, position 0, sequence -1."""
     import torch
+    ref, i32 = pages._pointer(), torch.int32
     index, B = pages._index, pages.sequences
-    i32 = torch.int32
     if out is None:
         dev = pages.device
         out = KVStep(_new_output((rows,), torch.int64, dev, stream), _new_output((rows,), i32, dev, stream),
@@ -1139,7 +1148,7 @@ def kv_step(pages: KVPages, keep, new_tokens, rows: int, tree_mask=None, out: Op
                      _new_output((B,), i32, dev, stream))
     slots, positions, sequences, q_start, kv_lens = out
     rc = _launch(
-        load_library().kv_pages_step, index, stream, pages._ref,
+        load_library().kv_pages_step, index, stream, ref,
         None if keep is None else _flat(keep, "keep", i32, B, index), _flat(new_tokens, "new_tokens", i32, B, index),
         None if tree_mask is None else _flat(tree_mask, "tree_mask", torch.int64, rows, index), rows,
         _flat(slots, "slots", torch.int64, rows, index), _flat(positions, "positions", i32, rows, index),
@@ -1292,8 +1301,8 @@ def quantize_tokens(X, dtype: int, weight=None, eps: float = 1e-6, residual=None
     weight: float16 [K], the tokens are normed first (x / sqrt(mean(x^2) + eps) * weight). x16: True or a tensor for the
     float16 values that the codes quantise. Every code is the correctly rounded one."""
     import torch
-    if X.dim() != 2 or not X.is_cuda:
-        raise ValueError("X must be [n][K] on the device")
+    if X.dim() != 2 or not X.is_cuda or X.shape[1] == 0:
+        raise ValueError("X must be [n][K] on the device, K > 0")
     n, K = X.shape
     index, f16, dev = X.get_device(), torch.float16, X.device
     xs = _matrix_rows(X, "X", f16, n, K, index)
@@ -1410,14 +1419,14 @@ def encode_int8(W: np.ndarray, scale: np.ndarray) -> EncodedInt8:
 
 
 def gemm_workspace_bytes(M: int, K: int, N: int) -> int:
-    """Bytes of workspace gemm_w8a8 uses to split K over workgroups (0: none)."""
+    """Bytes of workspace gemm_w8a8 uses to split K over workgroups, for any number of tokens up to N (0: none)."""
     out = ctypes.c_int64(0)
     _check(load_library().gemm_w8a8_workspace_bytes(M, K, N, ctypes.byref(out)), "gemm_w8a8_workspace_bytes")
     return int(out.value)
 
 
 def new_gemm_workspace(W: DenseInt8, N: int, device="cuda"):
-    """A zero-filled workspace for gemm_w8a8 with N tokens (None if none is used).
+    """A zero-filled workspace for gemm_w8a8 with up to N tokens (None if none is used).
     It is cleared on the current stream: calls on another one wait for that."""
     import torch
     n = gemm_workspace_bytes(W.M, W.K, N)
@@ -1426,8 +1435,8 @@ def new_gemm_workspace(W: DenseInt8, N: int, device="cuda"):
 
 def gemm_w8a8(W: DenseInt8, X, scale_x, Y=None, workspace=None, stream=None):
     """float16 Y [N][M] = (W x_n) * W.scale[m] * scale_x[n], int32 sums, any N. X: int8 [N][K], rows of whole 16 bytes
-    in memory (as quantize_tokens leaves them); scale_x: float32 [N]. workspace: new_gemm_workspace(W, N), or None for
-    no split over K."""
+    in memory (as quantize_tokens leaves them); scale_x: float32 [N]. workspace: new_gemm_workspace of W and as
+    many tokens or more, or None for no split over K; calls that share one must be ordered."""
     import torch
     if X.dim() != 2 or X.shape[1] != W.K:
         raise ValueError("X must be [N][K]")

@@ -552,11 +552,14 @@ const W8Shape W8_SHAPES[] = {
 };
 
 #define W8_COUNTERS 16384      // arrival counters at the head of a workspace (64 KB, as everywhere in the library)
-#define W8_MOST_TILES ((INT64_C(1) << 31) - 8)
+#define W8_SPLIT_TILES 256     // more tiles fill the card without splits
+static_assert(W8_SPLIT_TILES <= W8_COUNTERS, "an arrival counter a tile");
+#define W8_MOST_TILES ((INT64_C(1) << 22) - 8)      // of a launch: fewer than 2^32 threads
+
+#define W8_MOST_ROWS (W8_MOST_TILES * 16)
 
 struct W8Plan {
     W8Run run;
-    int64_t tiles;
     int splits, per;
     int64_t part_bytes;      // of all tiles and splits
 };
@@ -568,9 +571,9 @@ struct W8Plan {
 W8Plan w8_plan(int64_t bands, int64_t ktiles, int64_t n, bool split) {
     const int k = (int)ktiles;
     if (k == 0 || (n <= 4 && bands * ktiles >= 32768))
-        return {bands > 512 && ktiles < 128 ? w8_stream<8, 4> : w8_stream<16, 2>, bands * ((n + 15) / 16), 1, k, 0};
-    if (n <= 16 && bands > 256) return {w8_ring<1, 1, 4, 4>, bands, 1, k, 0};
-    W8Plan best{nullptr, 0, 1, k, 0};
+        return {bands > 512 && ktiles < 128 ? w8_stream<8, 4> : w8_stream<16, 2>, 1, k, 0};
+    if (n <= 16 && bands > 256) return {w8_ring<1, 1, 4, 4>, 1, k, 0};
+    W8Plan best{nullptr, 1, k, 0};
     double least = 0.0;
     for (const W8Shape &p : W8_SHAPES) {
         const int64_t tiles = (bands + p.bands - 1) / p.bands * ((n + p.blocks * 16 - 1) / (p.blocks * 16));
@@ -580,11 +583,11 @@ W8Plan w8_plan(int64_t bands, int64_t ktiles, int64_t n, bool split) {
             double t = (double)((tiles * used + 255) / 256) * one * per;
             int64_t bytes = 0;
             if (splits > 1) {
-                if (!split || per < 8 || tiles > 256 || tiles > W8_COUNTERS) break;
+                if (!split || per < 8 || tiles > W8_SPLIT_TILES) break;
                 bytes = tiles * used * p.bands * p.blocks * 1024;
                 t += 2.5 + 1.3 * splits + (double)bytes * 0.25e-6;
             }
-            if (best.run == nullptr || t < least) best = W8Plan{p.run, tiles, used, per, bytes}, least = t;
+            if (best.run == nullptr || t < least) best = W8Plan{p.run, used, per, bytes}, least = t;
         }
     }
     return best;
@@ -594,11 +597,16 @@ W8Plan w8_plan(int64_t bands, int64_t ktiles, int64_t n, bool split) {
 
 extern "C" int gemm_w8a8_workspace_bytes(int64_t M, int64_t K, int64_t N, int64_t *bytes) {
     if (bytes == nullptr || M < 0 || K < 0 || N < 0) return BSP_E_ARG;
-    if (K > BSP_W8_MAX_K || M > INT32_MAX || N > INT32_MAX) return BSP_E_OVERFLOW;
+    if (K > BSP_W8_MAX_K || M > W8_MOST_ROWS || N > INT32_MAX) return BSP_E_OVERFLOW;
     *bytes = 0;
-    if (M == 0 || K == 0 || N == 0) return BSP_OK;
-    const W8Plan p = w8_plan((M + 15) / 16, (K + 63) / 64, N, true);
-    if (p.splits > 1) *bytes = W8_COUNTERS * 4 + p.part_bytes;
+    if (M == 0 || K == 0) return BSP_OK;
+    // plans change with every 16 tokens (and after 4), and more of them can take less
+    const int64_t bands = (M + 15) / 16, ktiles = (K + 63) / 64;
+    for (int64_t n = 1; n <= N; n = n == 1 ? 5 : n == 5 ? 17 : n + 16) {
+        if ((bands + 15) / 16 * ((n + 255) / 256) > W8_SPLIT_TILES) break;
+        const W8Plan p = w8_plan(bands, ktiles, n, true);
+        if (p.splits > 1) *bytes = std::max(*bytes, W8_COUNTERS * 4 + p.part_bytes);
+    }
     return BSP_OK;
 }
 
@@ -606,7 +614,7 @@ extern "C" int gemm_w8a8_dq(const uint8_t *tiles, int64_t M, int64_t K, const in
                             const float *scale_w, const float *scale_x, uint16_t *Y, int64_t y_stride,
                             void *workspace, int64_t workspace_bytes, hipStream_t stream) {
     if (M < 0 || K < 0 || N < 0 || workspace_bytes < 0) return BSP_E_ARG;
-    if (K > BSP_W8_MAX_K || M > INT32_MAX || N > INT32_MAX) return BSP_E_OVERFLOW;
+    if (K > BSP_W8_MAX_K || M > W8_MOST_ROWS || N > INT32_MAX) return BSP_E_OVERFLOW;
     if (M == 0 || N == 0) return BSP_OK;
     if (Y == nullptr || scale_w == nullptr || scale_x == nullptr || y_stride < M) return BSP_E_ARG;
     if (K > 0 && (tiles == nullptr || X == nullptr || x_stride < K || x_stride % 16 != 0)) return BSP_E_ARG;
@@ -616,16 +624,21 @@ extern "C" int gemm_w8a8_dq(const uint8_t *tiles, int64_t M, int64_t K, const in
     // the tokens of a tile (256 at most) are reached by 32-bit offsets
     if (K > 0 && x_stride >= INT64_C(1) << 23) return BSP_E_OVERFLOW;
     W8Args a{};
-    a.tiles = tiles, a.x = X, a.xs = x_stride, a.scale_w = scale_w, a.scale_x = scale_x, a.y = Y, a.ys = y_stride;
-    a.n = N, a.M = (int)M, a.bands = (int)((M + 15) / 16), a.ktiles = (int)((K + 63) / 64);
+    a.tiles = tiles, a.xs = x_stride, a.scale_w = scale_w, a.ys = y_stride;
+    a.M = (int)M, a.bands = (int)((M + 15) / 16), a.ktiles = (int)((K + 63) / 64);
     a.last = (int)std::max<int64_t>(x_stride - 16, 0);
-    const W8Plan p = w8_plan(a.bands, a.ktiles, N, workspace != nullptr);
-    if (p.tiles > W8_MOST_TILES) return BSP_E_OVERFLOW;
-    a.splits = p.splits, a.per = p.per;
-    if (p.splits > 1) {
-        if (workspace_bytes < W8_COUNTERS * 4 + p.part_bytes) return BSP_E_CAPACITY;
-        a.counters = (uint32_t *)workspace, a.parts = (uint8_t *)workspace + W8_COUNTERS * 4;
+    // so many tokens that tiles of 16 could pass a launch's: in runs
+    const int64_t most = W8_MOST_TILES / a.bands * 16;
+    for (int64_t t = 0; t < N; t += most) {
+        a.n = std::min(N - t, most);
+        a.x = X + t * x_stride, a.scale_x = scale_x + t, a.y = Y + t * y_stride;
+        const W8Plan p = w8_plan(a.bands, a.ktiles, a.n, workspace != nullptr && N <= most);
+        a.splits = p.splits, a.per = p.per;
+        if (p.splits > 1) {
+            if (workspace_bytes < W8_COUNTERS * 4 + p.part_bytes) return BSP_E_CAPACITY;
+            a.counters = (uint32_t *)workspace, a.parts = (uint8_t *)workspace + W8_COUNTERS * 4;
+        }
+        p.run(a, stream);
     }
-    p.run(a, stream);
     return hipGetLastError() == hipSuccess ? BSP_OK : BSP_E_HIP;
 }

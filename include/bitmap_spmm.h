@@ -736,8 +736,8 @@ int qk_norm_rope_append_f16(const uint16_t *Q, int64_t q_stride, const uint16_t 
  *   h = fp16(x + residual) (or x), y = h * weight (or h), m = max_k |y_k|, L = 127 or 7
  *   code_k = round-half-even(y_k * L / m), of the exact quotient (0 where m = 0)
  *   scale  = m / sqrt(mean(h^2) + eps) / L with a weight, m / L without, fp32
- *   x16    = fp16(y / sqrt(mean(h^2) + eps)), what the codes stand for unquantised
- *            (the adapters' activations)
+ *   x16    = fp16(y / sqrt(mean(h^2) + eps)) with a weight, h without: what the codes stand
+ *            for, unquantised (the adapters' activations)
  *   A token with an infinity or a NaN in y gets codes 0 and scale NaN.
  * --------------------------------------------------------------------------- */
 typedef struct bsp_tokens {
@@ -763,7 +763,8 @@ typedef struct bsp_tokens {
  *                pack_int4_activations does (an odd K leaves the last high nibble zero).
  *   codes        DEVICE; code_stride >= K (int8) or ceil(K / 2) (int4). What lies between a token's
  *                codes and the next token's is left as it is.
- * n == 0 or K == 0 launches nothing.
+ * n == 0 or K == 0 launches nothing (and writes no scales). No output may overlap an input but hidden, as above, nor
+ * another output.
  */
 int quantize_tokens_f16(const bsp_tokens *tokens, int dtype, uint8_t *codes, int64_t code_stride, hipStream_t stream);
 
@@ -792,7 +793,8 @@ int64_t int8_tiles_bytes(int64_t M, int64_t K);
  */
 int encode_int8_tiles(const int8_t *W, int64_t M, int64_t K, int64_t ldw, uint8_t *tiles);
 
-/* Bytes of workspace gemm_w8a8_dq uses to split K over workgroups (0: none). Host only. */
+/* Bytes of workspace gemm_w8a8_dq uses to split K over workgroups, for any number of tokens up to N (0: none). Host
+ * only. */
 int gemm_w8a8_workspace_bytes(int64_t M, int64_t K, int64_t N, int64_t *bytes);
 
 /*
@@ -806,7 +808,7 @@ int gemm_w8a8_workspace_bytes(int64_t M, int64_t K, int64_t N, int64_t *bytes);
  *                bytes, 256-byte aligned, zero-filled before its first use (its first 64 KiB hold
  *                arrival counters, left zero by every call: a workspace of the other entry points
  *                will do). Too small: BSP_E_CAPACITY. Calls that share one must be ordered.
- * K > BSP_W8_MAX_K, M >= 2^31, N >= 2^31, x_stride >= 2^23: BSP_E_OVERFLOW. K == 0 gives zeros. The result does not
+ * K > BSP_W8_MAX_K, M > 2^26 - 128, N >= 2^31, x_stride >= 2^23: BSP_E_OVERFLOW. K == 0 gives zeros. The result does not
  * depend on timing or on the workspace.
  */
 int gemm_w8a8_dq(const uint8_t *tiles, int64_t M, int64_t K, const int8_t *X, int64_t x_stride, int64_t N,

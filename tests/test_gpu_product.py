@@ -143,3 +143,28 @@ def test_tokens_into_the_product(dev):
         Y = bsp.gemm_w8a8(enc, t.codes, t.scale)
         codes, _, _, _ = step.quantise_tokens(X16, 127)
         _same(Y, step.product(W, codes, sw, t.scale.cpu().numpy()))
+
+
+def test_one_workspace_for_fewer_tokens(dev):
+    rng = np.random.default_rng(31)
+    M, K, most = 512, 11008, 1200
+    W, x, X, sw, sx = _problem(rng, most, M, K, dev)
+    enc = bsp.encode_int8(W, sw).to_device(dev)
+    ws = bsp.new_gemm_workspace(enc, most, device=dev)
+    s, want = torch.from_numpy(sx).to(dev), step.product(W, x, sw, sx)
+    for N in (most, 1, 600, 16, 1025, 897, 33, most):
+        _same(bsp.gemm_w8a8(enc, X[:N], s[:N], workspace=ws), want[:N])
+
+
+def test_more_tokens_than_one_launch_takes(dev):
+    # one channel: 2^22 - 8 tiles of 16 tokens a launch
+    N, K = ((1 << 22) - 8) * 16 + 33, 16
+    g = torch.Generator(device=dev).manual_seed(5)
+    X = torch.randint(-128, 128, (N, K), dtype=torch.int8, device=dev, generator=g)
+    w = np.arange(-120, 120, 15, dtype=np.int8).reshape(1, K)
+    sx = torch.rand(N, device=dev, generator=g) * 0.001
+    Y = bsp.gemm_w8a8(bsp.encode_int8(w, np.full(1, 0.5, np.float32)).to_device(dev), X, sx)
+    sums = torch.zeros(N, device=dev)      # whole numbers below 2^24: exact
+    for k in range(K):
+        sums += X[:, k].float() * float(w[0, k])
+    assert torch.equal(Y[:, 0], (sums * 0.5 * sx).half())

@@ -141,6 +141,30 @@ def test_workspace_of_the_product_is_checked():
             assert L.gemm_w8a8_dq(FAKE, M, K, FAKE, xs, N, FAKE, FAKE, FAKE, M, FAKE, need - 1, None) == bsp.E_CAPACITY
 
 
+def test_sizes_past_what_the_kernels_index():
+    L = bsp.load_library()
+
+    def product(M, K, xs, N, ys):
+        return L.gemm_w8a8_dq(FAKE, M, K, FAKE, xs, N, FAKE, FAKE, FAKE, ys, None, 0, None)
+
+    assert product(16, 64, 1 << 23, 4, 16) == bsp.E_OVERFLOW                       # rows too far apart
+    assert product((1 << 26) - 127, 64, 64, 4, 1 << 26) == bsp.E_OVERFLOW          # more rows than a launch has tiles
+    n = ctypes.c_int64(0)
+    assert L.gemm_w8a8_workspace_bytes((1 << 26) - 127, 64, 4, ctypes.byref(n)) == bsp.E_OVERFLOW
+    assert L.gemm_w8a8_workspace_bytes((1 << 26) - 128, 64, 4, ctypes.byref(n)) == bsp.OK
+
+    def heads(hq, hkv):
+        return L.qk_norm_rope_f16(FAKE, hq * 64, FAKE, hkv * 64, 1, hq, hkv, 64, _rotation(), FAKE, hq * 64, FAKE, hkv * 64, None)
+
+    assert heads((1 << 20) + 1, 1) == bsp.E_OVERFLOW and heads(1, (1 << 20) + 1) == bsp.E_OVERFLOW
+
+
+@pytest.mark.parametrize("M,K", [(4096, 11008), (1024, 11008), (64, 131071), (33, 40000), (16, 4096)])
+def test_more_tokens_need_no_less_workspace(M, K):
+    sizes = [bsp.gemm_workspace_bytes(M, K, N) for N in list(range(1, 40)) + list(range(41, 5000, 37)) + [1 << 30]]
+    assert sizes == sorted(sizes)
+
+
 @pytest.mark.parametrize("M,K", [(1, 1), (16, 64), (17, 65), (5, 200), (40, 16), (33, 1000)])
 def test_laid_out_weights(M, K):
     rng = np.random.default_rng(M + K)

@@ -147,3 +147,25 @@ def test_shapes_and_types_that_do_not_fit(world):
         with pytest.raises((TypeError, ValueError)):
             call()
         assert not world.lib.calls, i
+
+
+def test_pages_given_another_storage(world):
+    pages = bsp.KVPages(_tensor((3, 4), I32), _tensor((3,), I32), _tensor((3,), I32), _tensor((10,), I32), 16)
+    for name, shape in (("block_table", (3, 4)), ("lens", (3,)), ("held", (3,)), ("free", (10,))):
+        before = getattr(pages, name).data_ptr()
+        getattr(pages, name).data = torch.ones(shape, dtype=I32)
+        assert getattr(pages, name).data_ptr() != before
+        bsp.kv_step(pages, None, _tensor((3,), I32), 8)
+        d = bsp._KVPagesDesc.from_address(world.lib.calls[-1][1][0])
+        assert (d.block_table, d.lens, d.held, d.free_pages) == tuple(
+            getattr(pages, n).data_ptr() for n in ("block_table", "lens", "held", "free"))
+    calls = len(world.lib.calls)
+    pages.lens.data = torch.ones(2, dtype=I32)
+    with pytest.raises(ValueError):
+        bsp.kv_step(pages, None, _tensor((3,), I32), 8)
+    assert len(world.lib.calls) == calls
+
+
+def test_tokens_without_a_channel_are_refused(world):
+    with pytest.raises(ValueError):
+        bsp.quantize_tokens(_tensor((3, 0), F16), bsp.INT8)
