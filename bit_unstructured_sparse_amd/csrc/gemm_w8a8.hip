@@ -119,9 +119,9 @@ __device__ __forceinline__ bool w8_last(const W8Args &a, const W8Tile &tile) {
     return true;
 }
 
-// ---- at most 16 tokens: W streams from memory straight into registers ----
+// ---- at most 4 tokens: W streams from memory straight into registers ----
 
-// A workgroup owns a band of 16 channels; its W wavefronts take every W-th column tile of K, U of them
+// A workgroup owns a band of 16 channels and 16 tokens; its W wavefronts take every W-th column tile of K, U of them
 // on their way at once, and meet in LDS. W is read once: marked so, it costs the last-level cache nothing (one
 // token x 12288 x 4096, cold: 10.0 us, through a ring 11.5).
 template <int W, int U>

@@ -61,13 +61,15 @@ typedef enum bsp_status {
     BSP_OK = 0,
     BSP_E_ARG = 1,       /* null pointer, negative size, N > 32, ldw < K, unknown dtype/algo */
     BSP_E_RANGE = 2,     /* a weight outside its type's range: int4 [-8, 7], int2 [-2, 1] */
-    BSP_E_CAPACITY = 3,  /* payload buffer smaller than the encoded payload */
-    BSP_E_OVERFLOW = 4,  /* nnz >= 2^32, K >= 2^25 (int32 sums could overflow), or an index beyond 2^31 */
+    BSP_E_CAPACITY = 3,  /* payload buffer smaller than the encoded payload, a workspace smaller than the call needs */
+    BSP_E_OVERFLOW = 4,  /* nnz >= 2^32, K >= 2^25 (int32 sums could overflow), an index beyond 2^31, or a size past what
+                            an entry point names */
     BSP_E_HIP = 5,       /* a HIP launch error (hipGetLastError after the launch) */
-    BSP_E_UNSUPPORTED = 6 /* a kernel forced through an *_algo entry point cannot run this shape */
+    BSP_E_UNSUPPORTED = 6 /* a kernel forced through an *_algo entry point cannot run this shape, or a form that has no
+                             kernel (head_dim, rot, sequences) */
 } bsp_status;
 
-/* BSP_INT8 is a cache type only (bsp_kv_cache); BSP_INT2 a weight type only. */
+/* BSP_INT8 is a type of caches (bsp_kv_cache) and token codes (quantize_tokens_f16) only; BSP_INT2 of weights only. */
 typedef enum bsp_dtype { BSP_INT4 = 0, BSP_FP16 = 1, BSP_INT2 = 2, BSP_INT8 = 3 } bsp_dtype;
 
 /* Kernel choice for the *_algo entry points. BSP_ALGO_AUTO applies the
