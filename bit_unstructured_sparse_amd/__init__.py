@@ -1,7 +1,8 @@
 """Bitmap-tiled int4 / fp16 sparse x dense matmul on AMD MI355X (gfx950).
 
-A thin ctypes binding over ``libbitmap_spmm.so`` (C ABI in
-``include/bitmap_spmm.h``). Host arrays are numpy; device memory and streams
+A thin binding over ``libbitmap_spmm.so`` (C ABI in
+``include/bitmap_spmm.h``): ctypes, and natively the steps that every call repeats
+where ``_binding.so`` has been built. Host arrays are numpy; device memory and streams
 come from PyTorch tensors. Every step of the SpMM runs in the library's HIP
 kernels; there is no CPU fallback: if the library is missing, importing the
 SpMM functions raises.
