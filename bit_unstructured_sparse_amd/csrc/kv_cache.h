@@ -10,6 +10,12 @@
 typedef uint32_t kv_u4 __attribute__((ext_vector_type(4)));
 typedef uint32_t kv_u2 __attribute__((ext_vector_type(2)));
 typedef _Float16 kv_h8 __attribute__((ext_vector_type(8)));
+typedef _Float16 kv_h2 __attribute__((ext_vector_type(2)));
+
+__device__ __forceinline__ kv_h2 kv_pair(uint32_t v) { return __builtin_bit_cast(kv_h2, v); }
+
+// 1.5 * 2^23: added to a number below 2^22 it leaves its rounded value in the low bits
+#define KV_MAGIC 12582912.0f
 
 // A row's scale word: step as bfloat16 (high half), offset as fp16 (low half).
 __device__ __forceinline__ float kv_word_step(uint32_t w) { return __builtin_bit_cast(float, w & 0xFFFF0000u); }
@@ -64,55 +70,55 @@ __device__ __forceinline__ float kv_other(float v, int d) {
 // quotient (Markstein's theorem), at three operations instead of a division.
 template <int LPR>
 __device__ __forceinline__ void kv_quantise(kv_u4 raw, float levels, uint32_t (&u)[8], uint32_t &word) {
-    const kv_h8 h = __builtin_bit_cast(kv_h8, raw);
-    float x[8], lo, hi;
-    uint32_t big = 0;
+    // minimum and negated maximum in one word of two halves: two values an instruction, and one reduction over the
+    // lanes (a third of the instructions: 8192 tokens x 32 heads to int8 39.5 us, in fp32 45). (These keep a NaN, and take -0 for less than +0, as the fp32 ones do.)
+    kv_h2 least = kv_pair(raw[0]), most = least;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        x[i] = (float)h[i];
-        lo = i == 0 ? x[0] : fminf(lo, x[i]);
-        hi = i == 0 ? x[0] : fmaxf(hi, x[i]);
+    for (int i = 1; i < 4; ++i) {
+        least = __builtin_elementwise_minimum(least, kv_pair(raw[i]));
+        most = __builtin_elementwise_maximum(most, kv_pair(raw[i]));
     }
+    const uint32_t lb = __builtin_bit_cast(uint32_t, least), mb = __builtin_bit_cast(uint32_t, most) ^ 0x80008000u;
+    kv_h2 range = __builtin_elementwise_minimum(kv_pair((lb & 0xFFFFu) | (mb << 16)), kv_pair((lb >> 16) | (mb & 0xFFFF0000u)));
 #pragma unroll
-    for (int i = 0; i < 4; ++i) big = max(big, max(raw[i] & 0x7FFFu, (raw[i] >> 16) & 0x7FFFu));
-#pragma unroll
-    for (int d = 1; d < LPR; d <<= 1) {
-        lo = fminf(lo, kv_other(lo, d));
-        hi = fmaxf(hi, kv_other(hi, d));
-        big = max(big, __builtin_bit_cast(uint32_t, kv_other(__builtin_bit_cast(float, big), d)));
-    }
-    if (big >= 0x7C00u) {      // an infinity or a NaN in the row
+    for (int d = 1; d < LPR; d <<= 1)
+        range = __builtin_elementwise_minimum(
+            range, kv_pair(__builtin_bit_cast(uint32_t, kv_other(__builtin_bit_cast(float, range), d))));
+    const uint32_t ends = __builtin_bit_cast(uint32_t, range);
+    if ((ends & 0x7C00u) == 0x7C00u || (ends & 0x7C000000u) == 0x7C000000u) {      // an infinity or a NaN in the row
         word = 0x7FC07E00u;
 #pragma unroll
         for (int i = 0; i < 8; ++i) u[i] = 0;
         return;
     }
+    const kv_h8 h = __builtin_bit_cast(kv_h8, raw);
+    const float lo = (float)range.x, hi = -(float)range.y;
     const uint32_t sb = (__builtin_bit_cast(uint32_t, (hi - lo) / levels) + 0xFFFFu) & 0xFFFF0000u;
     const float s = __builtin_bit_cast(float, sb);
-    word = sb | bsp_f2h(lo);
+    word = sb | (ends & 0xFFFFu);
     const float r = sb != 0 ? 1.0f / s : 0.0f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const float nmr = x[i] - lo;
+        const float nmr = (float)h[i] - lo;
         const float q0 = nmr * r;
         const float q = __builtin_fmaf(__builtin_fmaf(-q0, s, nmr), r, q0);
-        u[i] = (uint32_t)fminf(rintf(q), levels);
+        u[i] = __builtin_bit_cast(uint32_t, fminf(q + KV_MAGIC, levels + KV_MAGIC));
     }
 }
 
-// The codes of channels ch .. ch + 7 of a row, `at` = row * D + ch.
+// The codes (the low bits of u) of channels ch .. ch + 7 of a row, `at` = row * D + ch.
 template <int KIND>
 __device__ __forceinline__ void kv_store_codes(uint8_t *codes, int64_t at, const uint32_t (&u)[8]) {
-    if constexpr (KIND == BSP_INT8) {
-        kv_u2 c;
-        c.x = u[0] | (u[1] << 8) | (u[2] << 16) | (u[3] << 24);
-        c.y = u[4] | (u[5] << 8) | (u[6] << 16) | (u[7] << 24);
-        *reinterpret_cast<kv_u2 *>(codes + at) = c;
-    } else {
-        uint32_t c = 0;
+    kv_u2 c;      // a code a byte
 #pragma unroll
-        for (int e = 0; e < 8; ++e) c |= u[e] << (4 * e);
-        *reinterpret_cast<uint32_t *>(codes + at / 2) = c;
+    for (int i = 0; i < 2; ++i)
+        c[i] = __builtin_amdgcn_perm(u[4 * i + 1], u[4 * i], 0x0C0C0400u) |
+               __builtin_amdgcn_perm(u[4 * i + 3], u[4 * i + 2], 0x04000C0Cu);
+    if constexpr (KIND == BSP_INT8) {
+        *reinterpret_cast<kv_u2 *>(codes + at) = c;
+    } else {      // a byte's code beside its neighbour's, then every other byte
+        c.x |= c.x >> 4, c.y |= c.y >> 4;
+        *reinterpret_cast<uint32_t *>(codes + at / 2) = __builtin_amdgcn_perm(c.y, c.x, 0x06040200u);
     }
 }
 

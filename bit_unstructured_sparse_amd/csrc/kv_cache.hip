@@ -9,10 +9,11 @@
 // whenever the slots are.
 //
 // Bound by HBM for long calls: 8192 tokens x 32 heads of 128, int8, written
-// and read back, 407 MB in 85.4 us (4.77 TB/s, the codes read back among them, which
+// and read back, 407 MB in 74.5 us (5.46 TB/s, the codes read back among them, which
 // the last-level cache may serve); 65537 tokens x 8 heads, int4, read back, 340 MB
 // in 75.2 us (4.52 TB/s). Four rows in flight per lane made that: with
-// one (three dependent loads of 4 to 16 bytes per lane) 92 and 106 us. Short calls
+// one (three dependent loads of 4 to 16 bytes per lane) 92 and 106 us; a row's minimum and maximum two values an
+// instruction took the first from 85.4 (writing alone 45 to 39.5). Short calls
 // are launch latency (32 tokens, write and read: 4.8 us for the two kernels).
 #include <hip/hip_runtime.h>
 

@@ -23,10 +23,10 @@
 // first), then the lanes' sums neighbours first.
 //
 // Bound by memory where tokens are many: 8192 tokens, 32 query and 32 key heads of 128, 268 MB in 51.8 us
-// (5.2 TB/s); with values into an fp16 cache 403 MB in 76 us (5.3 TB/s). Into an int8 cache 336 MB take 86 us: a row's
-// minimum, maximum and codes cost as many vector instructions as the rotation, and no longer hide. (With each lane its
-// own 8 angles a group: 84 and 127 us. With 64-bit sines throughout 55 and 91.) Few tokens are launch latency: 3.8 us,
-// 4.2 with an int8 cache.
+// (5.2 TB/s); with values into an fp16 cache 403 MB in 76 us (5.3 TB/s). Into an int8 cache 336 MB take 79 us: a row's
+// codes cost about as many vector instructions as the rotation, and no longer all hide (86 with its minimum and
+// maximum in fp32). (With each lane its own 8 angles a group: 84 and 127 us. With 64-bit sines throughout 55 and 91.) Few
+// tokens are launch latency: 3.8 us, 4.1 with an int8 cache.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -240,8 +240,8 @@ void qk_launch_u(const QkArgs &all, hipStream_t stream) {
     }
 }
 
-// Heads of 128, many of them: two groups a wavefront (8192 tokens x 64 heads 51.8 us against 62.9, into an int8 cache
-// 86 against 104; 512 x 64 6.8 against 7.1, 512 x 80 7.5 against 7.7; 128 x 80 5.0 against 4.4). Heads of 64, 8 to
+// Heads of 128, many of them: two groups a wavefront (8192 tokens x 64 heads 51.8 us against 61.3, into an int8 cache
+// 79 against 94; 512 x 64 6.8 against 7.1, 512 x 80 7.5 against 7.7; 128 x 80 5.0 against 4.4). Heads of 64, 8 to
 // a group, gain nothing (8192 x 40 20.5 against 20.6, with an int8 cache 28.4 against 26.2), nor do those of 256 (23.7
 // against 25.5, 32.1 against 30.9).
 template <int D>
