@@ -1414,7 +1414,7 @@ def encode_int8(W: np.ndarray, scale: np.ndarray) -> EncodedInt8:
     scale = np.ascontiguousarray(scale, np.float32)
     if scale.shape != (M,):
         raise ValueError("scale must be [M]")
-    tiles = np.empty(L.int8_tiles_bytes(M, K), np.uint8)
+    tiles = np.empty(max(L.int8_tiles_bytes(M, K), 0), np.uint8)
     _check(L.encode_int8_tiles(_np_ptr(W), M, K, K, _np_ptr(tiles)), "encode_int8_tiles")
     return EncodedInt8(M, K, tiles, scale)
 

@@ -4,7 +4,6 @@
 
 #include <algorithm>
 #include <atomic>
-#include <system_error>
 #include <thread>
 
 #include "bitmap_spmm.h"
@@ -29,7 +28,7 @@ void lay_out(const int8_t *W, int64_t M, int64_t K, int64_t ldw, int64_t band, u
 }  // namespace
 
 extern "C" int64_t int8_tiles_bytes(int64_t M, int64_t K) {
-    if (M < 0 || K < 0) return -1;
+    if (M < 0 || K < 0 || M > INT32_MAX || K > BSP_W8_MAX_K) return -1;
     return (M + 15) / 16 * ((K + 63) / 64) * 1024;
 }
 
@@ -49,7 +48,7 @@ extern "C" int encode_int8_tiles(const int8_t *W, int64_t M, int64_t K, int64_t 
     for (int64_t i = 0; i + 1 < want; ++i) {
         try {
             others[i] = std::thread(work);
-        } catch (const std::system_error &) {      // no thread to be had: this one does the work
+        } catch (...) {      // no thread to be had: this one does the work
             break;
         }
     }

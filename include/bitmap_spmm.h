@@ -787,11 +787,12 @@ int dequantize_tokens_f16(const uint8_t *codes, int64_t code_stride, int dtype, 
  * --------------------------------------------------------------------------- */
 #define BSP_W8_MAX_K 131071
 
-/* Bytes of the laid-out form: ceil(M/16) * ceil(K/64) * 1024; -1 for negative sizes. */
+/* Bytes of the laid-out form: ceil(M/16) * ceil(K/64) * 1024; -1 for sizes that encode_int8_tiles refuses. */
 int64_t int8_tiles_bytes(int64_t M, int64_t K);
 
 /*
- * encode_int8_tiles -- W HOST int8 [M][ldw] -> tiles HOST (int8_tiles_bytes bytes).
+ * encode_int8_tiles -- W HOST int8 [M][ldw] -> tiles HOST (int8_tiles_bytes bytes). K > BSP_W8_MAX_K, M >= 2^31:
+ * BSP_E_OVERFLOW.
  */
 int encode_int8_tiles(const int8_t *W, int64_t M, int64_t K, int64_t ldw, uint8_t *tiles);
 

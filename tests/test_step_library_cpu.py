@@ -192,6 +192,9 @@ def test_laying_out_refuses():
         assert L.encode_int8_tiles(*bad) == bsp.E_ARG, bad
     assert L.encode_int8_tiles(p, 1, 131072, 131072, p) == bsp.E_OVERFLOW
     assert L.encode_int8_tiles(None, 0, 5, 5, None) == bsp.OK
+    assert L.int8_tiles_bytes(1, 131072) == -1 and L.int8_tiles_bytes(1 << 62, 64) == -1
+    with pytest.raises(bsp.BspError):
+        bsp.encode_int8(np.zeros((1, 131072), np.int8), np.ones(1))
     with pytest.raises(TypeError):
         bsp.encode_int8(np.zeros((2, 2), np.float32), np.ones(2))
     with pytest.raises(ValueError):
