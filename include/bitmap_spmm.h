@@ -486,8 +486,8 @@ int spmspv_cbc_f16(const uint32_t *tile_offsets, const uint32_t *colinfo, const 
  *   Quantising a row x (fp16, as given):
  *                o = min x;  s = fp32((max x - o) / L) rounded up to bfloat16,
  *                L = 255 or 15;  u = round-half-even((x - o) / s), at most L
- *                (u = 0 where s = 0). A row holding an infinity or a NaN gets
- *                s = o = NaN and codes 0: it reads back as NaN.
+ *                (u = 0 where s = 0; x - o and the quotient as fp32). A row holding
+ *                an infinity or a NaN gets s = o = NaN and codes 0: it reads back as NaN.
  *   s is rounded up so that L steps reach the maximum; the error of a value is
  *   at most s / 2, plus its rounding to fp16 where it is read back.
  * --------------------------------------------------------------------------- */

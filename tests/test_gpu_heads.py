@@ -4,7 +4,7 @@ import numpy as np
 import pytest
 
 import bit_unstructured_sparse_amd as bsp
-from oracle import step
+from oracle import serving, step
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
@@ -177,3 +177,75 @@ def test_many_tokens(dev):
     k2, v2 = bsp.kv_gather(two, pos.long()[:30])
     assert torch.equal(k[2900:2930], k2) and torch.equal(v[2900:2930], v2)
     _close(q[:40], Q[:40].cpu().numpy(), w.cpu().numpy(), 1e-5, np.arange(40), 128, False)
+
+
+def _in_order(x, w, eps, positions, freq, rot, inter):
+    """The definition in fp32, each operation rounded, the squares added in fours, then neighbours first (heads of 64:
+    neighbours first throughout); sines are the nearest floats."""
+    y = x.astype(np.float32)
+    s = y * y
+    if x.shape[-1] > 64:
+        s = ((s[..., 0::4] + s[..., 1::4]) + s[..., 2::4]) + s[..., 3::4]
+    while s.shape[-1] > 1:
+        s = s[..., 0::2] + s[..., 1::2]
+    y = y / np.sqrt(s * np.float32(1.0 / x.shape[-1]) + np.float32(eps)) * w.astype(np.float32)
+    turns = (positions.astype(np.int64).astype(np.uint64)[:, None] * freq[None, :]).astype(np.int64)
+    angle = turns.astype(np.float64) * (2.0 * np.pi / 2.0 ** 64)
+    c, z = np.cos(angle).astype(np.float32)[:, None], np.sin(angle).astype(np.float32)[:, None]
+    a, b = (slice(0, rot, 2), slice(1, rot, 2)) if inter else (slice(0, rot // 2), slice(rot // 2, rot))
+    out = y.copy()
+    out[..., a], out[..., b] = y[..., a] * c - y[..., b] * z, y[..., b] * c + y[..., a] * z
+    return out.astype(np.float16)
+
+
+@pytest.mark.parametrize("D,rot,inter", [(64, 64, False), (128, 128, False), (128, 64, True), (256, 256, True)])
+def test_rounded_in_the_definitions_order(D, rot, inter, dev):
+    # A sine is the nearest float but where it lies within 2^-11 of a step from the middle of two (one in 2^10), and a
+    # step of one moves a result past an fp16 border once in 2^12: one in 2^21 of the rotated ones. Allowed: 2^-16.
+    rng = np.random.default_rng(D + rot)
+    n = 1500
+    _, Q, K, _ = _fused(rng, n, 9, 2, D, 0, dev)
+    positions = rng.integers(-(1 << 17), 1 << 17, n).astype(np.int32)
+    w = (1 + 0.3 * rng.normal(0, 1, D)).astype(np.float16)
+    freq = bsp.rope_frequencies(rot, device=dev)
+    wd = torch.from_numpy(w).to(dev)
+    q, k = bsp.qk_norm_rope(Q, K, torch.from_numpy(positions).to(dev), freq, wd, wd, eps=1e-6, interleaved=inter)
+    for got, x in ((q, Q), (k, K)):
+        want = _in_order(x.cpu().numpy(), w, 1e-6, positions, freq.cpu().numpy().view(np.uint64), rot, inter)
+        other = got.cpu().numpy() != want
+        assert not other[..., rot:].any() and other.mean() <= 2.0 ** -16, int(other.sum())
+
+
+@pytest.mark.parametrize("kind", ["int8", "int4"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_cache_rows_of_any_bits(kind, D, dev):
+    # every exponent and the subnormals, rows of one exponent, and rows with an infinity or a NaN in one place. x - o and
+    # its quotient are rounded to fp32, by 2^-24 each: a code is the neighbour of the exact quotient's where that lies
+    # within 2^-23 of itself of the middle of two (-7.8e-5 + 35040 over 4672, 7.4999999833, is 8).
+    rng = np.random.default_rng(D)
+    bits = rng.integers(0, 1 << 16, (400, 3, D)).astype(np.uint16)
+    bits[bits & 0x7C00 == 0x7C00] ^= 0x4000
+    rows = bits.reshape(-1, D)
+    rows[::5] = (rows[::5] & 0x83FF) | (rng.integers(0, 31, (rows[::5].shape[0], 1)) << 10)
+    x = bits.view(np.float16)
+    bad = np.array([[7, 1], [7, 2], [90, 0], [399, 2]])
+    for (t, h), v, at in zip(bad, (np.inf, -np.inf, np.nan, np.nan), (0, D - 1, 8, D // 2 + 3)):
+        x[t, h, at] = v
+    cache = bsp.new_kv_cache(KINDS[kind], 25, 3, 16, D, device=dev)
+    X = torch.from_numpy(x).to(dev)
+    bsp.kv_append(cache, X, X, torch.arange(400, device=dev))
+    flat = lambda t: t.transpose(1, 2).reshape(400, 3, -1).cpu().numpy()
+    good = np.ones((400, 3), bool)
+    good[bad[:, 0], bad[:, 1]] = False
+    codes, words = serving.quantise(np.where(good[..., None], x, 0), kind)
+    for c, w in ((cache.k, cache.k_scale), (cache.v, cache.v_scale)):
+        c, w = flat(c), flat(w).view(np.uint32)[..., 0]
+        assert np.array_equal(w[good], words[good])
+        got, want = (np.stack((u & 15, u >> 4), -1).reshape(400, 3, D) if kind == "int4" else u for u in (c, codes))
+        off = (got != want) & good[..., None]
+        exact = x.astype(np.float64) - np.where(good[..., None], x, 0).min(-1, keepdims=True).astype(np.float64)
+        with np.errstate(divide="ignore", invalid="ignore"):
+            exact /= (w & 0xFFFF0000).view(np.float32).astype(np.float64)[..., None]
+        assert (np.abs(got.astype(int) - want)[off] == 1).all()
+        assert (np.abs(exact[off] % 1.0 - 0.5) <= exact[off] * 2.0 ** -23).all()
+        assert not c[~good].any() and (w[~good] == 0x7FC07E00).all()
