@@ -186,10 +186,13 @@ __device__ __forceinline__ void w8_dma(const void *base, uint32_t bytes, uint32_
 }
 
 // Few tokens, through LDS: as k_w8_stream, each wavefront with a ring of P stages of its own (MB bands and NB
-// blocks of tokens, 64 columns), which it alone fills and reads.
+// blocks of tokens, 128 columns), which it alone fills and reads. A token's 128 columns come in one piece, whole lines
+// of memory: with stages of 64 columns 32 tokens x 4096 x 11008 took 11.3 us in place of 10.4 (cold 17.2, 15.7). Two
+// stages do as well as three (10.4, 10.6): the other wavefronts' loads are on their way beside a wavefront's own.
 template <int NB, int MB, int W, int P>
 __global__ __launch_bounds__(64 * W) void k_w8_ring(const W8Args a) {
-    constexpr uint32_t STAGE = (MB + NB) * 1024u;
+    constexpr int PIECES = 2 * (MB + NB);
+    constexpr uint32_t STAGE = PIECES * 1024u;
     extern __shared__ __attribute__((aligned(128))) uint8_t w8_lds[];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const W8Tile tile = w8_tile(a, 1);
@@ -197,30 +200,34 @@ __global__ __launch_bounds__(64 * W) void k_w8_ring(const W8Args a) {
     const int band = (int)tile.m * MB, nb = min(MB, a.bands - band);
     const int64_t n0 = (int64_t)tile.n * (NB * 16);
     const int ntok = (int)min((int64_t)(NB * 16), a.n - n0);
-    const int k0 = (int)tile.split * a.per, kn = min(a.per, a.ktiles - k0);
+    const int k0 = (int)tile.split * a.per, kn = min(a.per, a.ktiles - k0), pairs = (kn + 1) / 2;
     const uint8_t *wbase = a.tiles + (((int64_t)band * a.ktiles + k0) << 10);
     const int8_t *xbase = a.x + n0 * a.xs + k0 * 64;
     const uint32_t wbytes = ((uint32_t)nb * (uint32_t)a.ktiles - k0) << 10, xbytes = (uint32_t)ntok * (uint32_t)a.xs - k0 * 64;
     const uint32_t lds = (uint32_t)(uintptr_t)(w8_lds_void *)w8_lds + wave * (P * STAGE);
-    uint32_t off[MB + NB];
+    // a stage: MB bands of the first 64 columns, of the second, then 8 tokens a piece. Lane l brings piece
+    // (l % 8) ^ (row / 2) of token l / 8, row its place among the block's 16: 16 lanes that read 16 tokens' pieces
+    // from LDS together find them on different banks
+    uint32_t woff[MB], xoff[2 * NB];
 #pragma unroll
-    for (int c = 0; c < MB + NB; ++c)
-        off[c] = c < MB ? ((uint32_t)min(c, nb - 1) * (uint32_t)a.ktiles << 10) + lane * 16
-                        : (uint32_t)min((c - MB) * 16 + (lane >> 2), ntok - 1) * (uint32_t)a.xs +
-                              (((lane & 3) ^ (-(lane >> 4) & 3)) << 4);
+    for (int c = 0; c < MB; ++c) woff[c] = ((uint32_t)min(c, nb - 1) * (uint32_t)a.ktiles << 10) + lane * 16;
+#pragma unroll
+    for (int c = 0; c < 2 * NB; ++c) {
+        const int row = (c & 1) * 8 + (lane >> 3);
+        xoff[c] = (uint32_t)min((c >> 1) * 16 + row, ntok - 1) * (uint32_t)a.xs + (((lane & 7) ^ (row >> 1)) << 4);
+    }
     auto fetch = [&](int t, uint32_t slot) {
-        const uint32_t k = (uint32_t)min(t, kn - 1);
+        const uint32_t dst = lds + slot * STAGE;
 #pragma unroll
-        for (int c = 0; c < MB + NB; ++c) {
-            const uint32_t dst = lds + slot * STAGE + c * 1024u;
-            if (c < MB)
-                w8_dma(wbase, wbytes, dst, off[c], k << 10);
-            else
-                w8_dma(xbase, xbytes, dst, off[c], k << 6);
-        }
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+            for (int c = 0; c < MB; ++c)
+                w8_dma(wbase, wbytes, dst + (q * MB + c) * 1024u, woff[c], (uint32_t)min(2 * t + q, kn - 1) << 10);
+#pragma unroll
+        for (int c = 0; c < 2 * NB; ++c) w8_dma(xbase, xbytes, dst + (2 * MB + c) * 1024u, xoff[c], (uint32_t)t << 7);
     };
-    const uint32_t abase = lds + lane * 16, brow = lane & 15,
-                   bbase = lds + MB * 1024u + (brow * 4 + ((lane >> 4) ^ (-(brow >> 2) & 3))) * 16;
+    const uint32_t abase = lds + lane * 16, brow = lane & 15, bpiece = lane >> 4,
+                   bbase = lds + 2 * MB * 1024u + brow * 128u;
     w8_i4 acc[MB][NB];
 #pragma unroll
     for (int i = 0; i < MB; ++i)
@@ -228,25 +235,38 @@ __global__ __launch_bounds__(64 * W) void k_w8_ring(const W8Args a) {
         for (int j = 0; j < NB; ++j) acc[i][j] = w8_i4{0, 0, 0, 0};
     uint32_t fill = 0, use = 0;
 #pragma unroll
-    for (int s = 0; s < P - 1; ++s) {
-        fetch(wave + s * W, fill);
-        fill = fill + 1 == P ? 0 : fill + 1;
-    }
-    for (int t = wave; t < kn; t += W) {
-        w8_wait_vm<(P - 2) * (MB + NB)>();
-        w8_i4 A[MB], B[NB];
+    for (int s = 0; s < P - 1; ++s)
+        if (wave + s * W < pairs) fetch(wave + s * W, fill++);
+    for (int t = wave; t < pairs; t += W) {
+        const bool more = t + (P - 1) * W < pairs;
+        if (more)
+            w8_wait_vm<(P - 2) * PIECES>();
+        else
+            w8_wait_vm<0>();
+        w8_i4 A[2][MB], B[2][NB];
 #pragma unroll
-        for (int i = 0; i < MB; ++i) A[i] = *(w8_lds_i4 *)(uintptr_t)(abase + use * STAGE + i * 1024u);
+        for (int q = 0; q < 2; ++q) {
 #pragma unroll
-        for (int j = 0; j < NB; ++j) B[j] = *(w8_lds_i4 *)(uintptr_t)(bbase + use * STAGE + j * 1024u);
-        use = use + 1 == P ? 0 : use + 1;
-        fetch(t + (P - 1) * W, fill);
-        fill = fill + 1 == P ? 0 : fill + 1;
-#pragma unroll
-        for (int i = 0; i < MB; ++i)
+            for (int i = 0; i < MB; ++i) A[q][i] = *(w8_lds_i4 *)(uintptr_t)(abase + use * STAGE + (q * MB + i) * 1024u);
 #pragma unroll
             for (int j = 0; j < NB; ++j)
-                acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(A[i], B[j], acc[i][j], 0, 0, 0);
+                B[q][j] = *(w8_lds_i4 *)(uintptr_t)(bbase + use * STAGE + j * 2048u + (((4 * q + bpiece) ^ (brow >> 1)) << 4));
+        }
+        use = use + 1 == P ? 0 : use + 1;
+        if (more) {
+            fetch(t + (P - 1) * W, fill);
+            fill = fill + 1 == P ? 0 : fill + 1;
+        }
+        // past the last column tile W's second half is its first again, and not added
+        const bool both = 2 * t + 1 < kn;
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+            if (q == 0 || both)
+#pragma unroll
+                for (int i = 0; i < MB; ++i)
+#pragma unroll
+                    for (int j = 0; j < NB; ++j)
+                        acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(A[q][i], B[q][j], acc[i][j], 0, 0, 0);
     }
     w8_wait_vm<0>();
     __syncthreads();
@@ -496,6 +516,8 @@ __global__ __launch_bounds__(64 * WM * WN) void k_w8_tiles(const W8Args a) {
     }
 }
 
+#define W8_MOST_LDS (160u * 1024u - 256u)      // beside the kernels' own words
+
 // Allows a kernel its LDS, once for each device.
 template <class Kernel>
 void w8_allow(Kernel *kernel, unsigned lds, std::atomic<uint64_t> &done) {
@@ -521,7 +543,8 @@ void w8_stream(W8Args &a, hipStream_t stream) {
 
 template <int NB, int MB, int W, int P>
 void w8_ring(W8Args &a, hipStream_t stream) {
-    constexpr unsigned LDS = (MB + NB) * 1024u * P * W;
+    constexpr unsigned LDS = 2 * (MB + NB) * 1024u * P * W;
+    static_assert(LDS <= W8_MOST_LDS, "a workgroup's LDS");
     static std::atomic<uint64_t> done{0};
     w8_allow(k_w8_ring<NB, MB, W, P>, LDS, done);
     const unsigned grid = w8_grid(a, MB, NB);
@@ -531,6 +554,7 @@ void w8_ring(W8Args &a, hipStream_t stream) {
 template <int WM, int WN, int TM, int TN, int KS, int R>
 void w8_tiles(W8Args &a, hipStream_t stream) {
     constexpr unsigned LDS = (WM * TM + WN * TN) * 1024u * KS * R;
+    static_assert(LDS <= W8_MOST_LDS, "a workgroup's LDS");
     static std::atomic<uint64_t> done{0};
     w8_allow(k_w8_tiles<WM, WN, TM, TN, KS, R>, LDS, done);
     const unsigned grid = w8_grid(a, WM * TM, WN * TN);
@@ -546,8 +570,8 @@ struct W8Shape {
 
 // The first six split K over their wavefronts, the others the tile.
 const W8Shape W8_SHAPES[] = {
-    {1, 1, w8_ring<1, 1, 8, 4>}, {1, 2, w8_ring<2, 1, 8, 3>}, {2, 2, w8_ring<2, 2, 8, 4>}, {1, 4, w8_ring<4, 1, 4, 4>},
-    {4, 2, w8_ring<2, 4, 8, 3>}, {2, 4, w8_ring<4, 2, 8, 3>}, {4, 4, w8_tiles<2, 2, 2, 2, 4, 3>}, {8, 4, w8_tiles<2, 2, 4, 2, 2, 3>},
+    {1, 1, w8_ring<1, 1, 16, 2>}, {1, 2, w8_ring<2, 1, 8, 2>}, {2, 2, w8_ring<2, 2, 8, 2>}, {1, 4, w8_ring<4, 1, 4, 3>},
+    {4, 2, w8_ring<2, 4, 6, 2>}, {2, 4, w8_ring<4, 2, 6, 2>}, {4, 4, w8_tiles<2, 2, 2, 2, 4, 3>}, {8, 4, w8_tiles<2, 2, 4, 2, 2, 3>},
     {8, 8, w8_tiles<2, 4, 4, 2, 1, 4>}, {16, 8, w8_tiles<2, 4, 8, 2, 1, 4>}, {16, 16, w8_tiles<2, 4, 8, 4, 1, 3>},
 };
 
@@ -572,14 +596,14 @@ W8Plan w8_plan(int64_t bands, int64_t ktiles, int64_t n, bool split) {
     const int k = (int)ktiles;
     if (k == 0 || (n <= 4 && bands * ktiles >= 32768))
         return {bands > 512 && ktiles < 128 ? w8_stream<8, 4> : w8_stream<16, 2>, 1, k, 0};
-    if (n <= 16 && bands > 256) return {w8_ring<1, 1, 4, 4>, 1, k, 0};
+    if (n <= 16 && bands > 256) return {w8_ring<1, 1, 4, 2>, 1, k, 0};
     W8Plan best{nullptr, 1, k, 0};
     double least = 0.0;
     for (const W8Shape &p : W8_SHAPES) {
         const int64_t tiles = (bands + p.bands - 1) / p.bands * ((n + p.blocks * 16 - 1) / (p.blocks * 16));
         const double one = std::max((p.bands + p.blocks) / 57.0, p.bands * p.blocks / 330.0);
         for (int splits = 1; splits <= 16; splits *= 2) {
-            const int per = (k + splits - 1) / splits, used = (k + per - 1) / per;
+            const int per = ((k + splits - 1) / splits + 1) & ~1, used = (k + per - 1) / per;
             double t = (double)((tiles * used + 255) / 256) * one * per;
             int64_t bytes = 0;
             if (splits > 1) {
