@@ -13,14 +13,17 @@
 //
 // What bounds them. A CU takes in about 57 KB/us (24 bytes a cycle) of operands, from any level past its
 // L1 and however many are on their way: the time of all but the largest tiles is (bands + blocks) KB per 64
-// columns at that rate (N = 128, 4096 x 4096, 64 x 64 tiles: 8 KB a step, 0.14 us; rings 4 to 16 stages deep
-// within 3 % of each other). It is why tiles are chosen by their bytes, and why four bands and two blocks beat one and
-// four. The 256 x 256 tiles are bound by the matrix cores and the power they draw: 8192 tokens x 12288 x 4096, 332
-// us (2,480 TOP/s), 62 % of the cycles in matrix instructions at 1.92 GHz, LDS reads and the DMA's writes taking as many
-// cycles as those. What brought them there from 600 us: operands read one step ahead into a second set of registers
+// columns at that rate (N = 128, 4096 x 4096, 64 x 64 tiles: 8 KB a step, 0.14 us; deeper rings gain
+// under 3 %). It is why tiles are chosen by their bytes, and why four bands and two blocks beat one and
+// four. The 256 x 256 tiles: 8192 tokens x 12288 x 4096 in 332 to 347 us (2,480 TOP/s at best, from box to box and with the
+// power drawn), 62 % of the cycles in matrix instructions at 1.92 GHz, LDS reads and the DMA's writes taking as many
+// cycles as those. Of that time the matrix instructions alone would take 256 us, with the reads from LDS 285, the loads and
+// reads without them 235: it is their meeting. What brought them there from 600 us: operands read one step ahead into a second set of registers
 // (with the scheduler told to spread the reads: left alone it sinks them behind all matrix instructions),
 // a swizzle that leaves no bank conflict (440 to 385 us), three stages rather than four (less power), the result
-// through LDS in whole rows (366 to 332). 4 wavefronts of 128 x 128 need 512 registers and hide no latency: 490 us.
+// through LDS in whole rows (366 to 332). 4 wavefronts of 128 x 128 read a
+// third less LDS, but need all 512 registers and hide no latency: 490 us, 368 with the accumulators held in place. A
+// workgroup that stays and loads its next tile under the results' stores took 354.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
