@@ -55,6 +55,7 @@ struct W8Args {
     uint8_t *parts;          // and their sums
     int last;                // last 16-byte piece of a token's row, as a byte offset
     uint32_t mtiles, ntiles; // tiles of the result
+    bool once;               // W is read once, and too large to be there for the next call
 };
 
 // 4 neighbouring channels m .. m + 3 of token n.
@@ -188,6 +189,11 @@ __device__ __forceinline__ void w8_dma(const void *base, uint32_t bytes, uint32_
     __builtin_amdgcn_raw_ptr_buffer_load_lds(bsp_rsrc(base, bytes), (w8_lds_void *)(uintptr_t)dst, 16, off, more, 0, 0);
 }
 
+// The same of what is read once, past the last-level cache (aux 2: nt).
+__device__ __forceinline__ void w8_dma_once(const void *base, uint32_t bytes, uint32_t dst, uint32_t off, uint32_t more) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(bsp_rsrc(base, bytes), (w8_lds_void *)(uintptr_t)dst, 16, off, more, 0, 2);
+}
+
 // Few tokens, through LDS: as k_w8_stream, each wavefront with a ring of P stages of its own (MB bands and NB
 // blocks of tokens, 128 columns), which it alone fills and reads. A token's 128 columns come in one piece, whole lines
 // of memory: with stages of 64 columns 32 tokens x 4096 x 11008 took 11.3 us in place of 10.4 (cold 17.2, 15.7). Two
@@ -222,10 +228,16 @@ __global__ __launch_bounds__(64 * W) void k_w8_ring(const W8Args a) {
     auto fetch = [&](int t, uint32_t slot) {
         const uint32_t dst = lds + slot * STAGE;
 #pragma unroll
-        for (int q = 0; q < 2; ++q)
+        for (int q = 0; q < 2; ++q) {
+            const uint32_t k = (uint32_t)min(2 * t + q, kn - 1) << 10;
 #pragma unroll
-            for (int c = 0; c < MB; ++c)
-                w8_dma(wbase, wbytes, dst + (q * MB + c) * 1024u, woff[c], (uint32_t)min(2 * t + q, kn - 1) << 10);
+            for (int c = 0; c < MB; ++c) {
+                if (a.once)
+                    w8_dma_once(wbase, wbytes, dst + (q * MB + c) * 1024u, woff[c], k);
+                else
+                    w8_dma(wbase, wbytes, dst + (q * MB + c) * 1024u, woff[c], k);
+            }
+        }
 #pragma unroll
         for (int c = 0; c < 2 * NB; ++c) w8_dma(xbase, xbytes, dst + (2 * MB + c) * 1024u, xoff[c], (uint32_t)t << 7);
     };
@@ -544,6 +556,11 @@ void w8_stream(W8Args &a, hipStream_t stream) {
     hipLaunchKernelGGL((k_w8_stream<W, U>), dim3(grid), dim3(64 * W), 0, stream, a);
 }
 
+// Weights of 96 MB and more, read once a call, are mostly gone from the last-level cache (256 MB, shared with all else)
+// by the next one: marked so. 8 tokens x 128256 x 4096 87 us (unmarked 98), 32000 x 4096 cold 23.1 (27.2), on nothing but
+// itself 22.2 (21.7). Smaller ones may still be there: 12288 x 4096 cold 10.5 (11.9), on itself 10.0 (8.3).
+#define W8_ONCE (INT64_C(96) << 10)      // in tiles of 1 KB
+
 template <int NB, int MB, int W, int P>
 void w8_ring(W8Args &a, hipStream_t stream) {
     constexpr unsigned LDS = 2 * (MB + NB) * 1024u * P * W;
@@ -551,6 +568,7 @@ void w8_ring(W8Args &a, hipStream_t stream) {
     static std::atomic<uint64_t> done{0};
     w8_allow(k_w8_ring<NB, MB, W, P>, LDS, done);
     const unsigned grid = w8_grid(a, MB, NB);
+    a.once = a.ntiles == 1 && (int64_t)a.bands * a.ktiles >= W8_ONCE;
     hipLaunchKernelGGL((k_w8_ring<NB, MB, W, P>), dim3(grid), dim3(64 * W), LDS, stream, a);
 }
 

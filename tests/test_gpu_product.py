@@ -168,3 +168,14 @@ def test_more_tokens_than_one_launch_takes(dev):
     for k in range(K):
         sums += X[:, k].float() * float(w[0, k])
     assert torch.equal(Y[:, 0], (sums * 0.5 * sx).half())
+
+
+@pytest.mark.parametrize("N", [3, 8, 16])
+def test_weights_larger_than_half_the_cache(N, dev):
+    rng = np.random.default_rng(N)
+    M, K = 25700, 4100      # over 96 MB
+    W, x, X, sw, sx = _problem(rng, N, M, K, dev)
+    Y = _run(W, X, sw, sx, dev)
+    rows = rng.permutation(M)[:300]
+    rows[:2] = 0, M - 1
+    assert np.array_equal(Y.cpu().numpy()[:, rows].view(np.uint16), step.product(W[rows], x, sw[rows], sx).view(np.uint16))
