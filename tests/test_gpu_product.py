@@ -171,7 +171,7 @@ def test_more_tokens_than_one_launch_takes(dev):
 
 
 @pytest.mark.parametrize("N", [3, 8, 16])
-def test_weights_larger_than_half_the_cache(N, dev):
+def test_weights_past_the_last_level_cache(N, dev):
     rng = np.random.default_rng(N)
     M, K = 25700, 4100      # over 96 MB
     W, x, X, sw, sx = _problem(rng, N, M, K, dev)
