@@ -19,6 +19,8 @@ import os
 import subprocess
 import sys
 import sysconfig
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -56,17 +58,11 @@ def binding_command(out: str):
             "-ltorch_hip", "-lc10", "-lc10_hip"]
 
 
-def command(out: str, sources=SOURCES):
-    return [HIPCC, f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC", "-shared",
-            "-I", os.path.join(ROOT, "include"), "-I", CSRC,
-            "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
-            "-Wall", "-Wno-unused-function",
-            *sources, "-o", out, "-lpthread"]
+FLAGS = [f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC", "-I", os.path.join(ROOT, "include"), "-I", CSRC,
+         "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops", "-Wall", "-Wno-unused-function"]
 
 
-def _compile(out: str, make, verbose: bool) -> str:
-    tmp = out + f".tmp{os.getpid()}"
-    cmd = make(tmp)
+def _run(cmd, verbose: bool) -> None:
     if verbose:
         print(" ".join(cmd), flush=True)
     r = subprocess.run(cmd, capture_output=True, text=True)
@@ -75,16 +71,35 @@ def _compile(out: str, make, verbose: bool) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"{os.path.basename(cmd[0])} failed:\n" + "\n".join(msgs))
     if verbose and msgs:
-        print("\n".join(msgs))
+        print("\n".join(msgs), flush=True)
+
+
+def _library(out: str, sources, pool, verbose: bool) -> str:
+    """The sources compiled side by side and linked; `out` is replaced at the end."""
+    tmp = out + f".tmp{os.getpid()}"
+    with tempfile.TemporaryDirectory() as folder:
+        objects = [os.path.join(folder, os.path.basename(s) + ".o") for s in sources]
+        list(pool.map(lambda so: _run([HIPCC, *FLAGS, "-c", so[0], "-o", so[1]], verbose), zip(sources, objects)))
+        _run([HIPCC, f"--offload-arch={ARCH}", "-fPIC", "-shared", *objects, "-o", tmp, "-lpthread"], verbose)
     os.replace(tmp, out)
     return out
 
 
+def _binding(verbose: bool) -> None:
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = binding_command(tmp)
+    if cmd is not None:
+        _run(cmd, verbose)
+        os.replace(tmp, BINDING)
+
+
 def build(verbose: bool = False) -> str:
-    _compile(PROBE_LIB, lambda out: command(out, PROBE_SOURCES), verbose)
-    if binding_command(BINDING) is not None:
-        _compile(BINDING, binding_command, verbose)
-    return _compile(LIB, command, verbose)
+    with ThreadPoolExecutor(min(8, int(os.environ.get("MAX_JOBS", 8)))) as pool, ThreadPoolExecutor(1) as other:
+        binding = other.submit(_binding, verbose)
+        _library(PROBE_LIB, PROBE_SOURCES, pool, verbose)
+        _library(LIB, SOURCES, pool, verbose)
+        binding.result()
+    return LIB
 
 
 if __name__ == "__main__":
