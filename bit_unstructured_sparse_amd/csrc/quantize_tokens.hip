@@ -279,11 +279,19 @@ void qt_run(const QtArgs &all, hipStream_t stream) {
 // wavefronts on the card. Many tokens keep it full anyway; two pieces a thread then halve the barriers
 // and turns of workgroups: 16384 x 4096 46 us with 256 threads a token, 65 with 512; 16384 x 1024 16 us
 // with a wavefront each, 27 with 256 threads (at 1024 tokens 5.1 against 4.6: the border lies at 2048).
+// Short tokens share a wavefront, as many as leave its lanes work: 117258 x 164 43 us with 16 lanes a token, 50 with 32, 83
+// with 64 (2048 x 256 5.2, 4.2, 4.4); 32768 x 300 24 with 32 and 28 with 64, 16384 x 512 14.4 and 15.2 (2048 5.6 and 4.9).
 template <int DTYPE>
 void qt_launch(const QtArgs &a, hipStream_t stream) {
-    const bool many = a.n >= 2048;
+    const bool many = a.n >= 2048, lots = a.n >= 16384;
     if (a.K <= 128)
         qt_run<DTYPE, 16, 1>(a, stream);
+    else if (a.K <= 256 && lots)
+        qt_run<DTYPE, 16, 2>(a, stream);
+    else if (a.K <= 256)
+        qt_run<DTYPE, 32, 1>(a, stream);
+    else if (a.K <= 512 && lots)
+        qt_run<DTYPE, 32, 2>(a, stream);
     else if (a.K <= 512)
         qt_run<DTYPE, 64, 1>(a, stream);
     else if (a.K <= 1024 && many)

@@ -181,3 +181,20 @@ def test_empty_calls(dev):
     t = bsp.quantize_tokens(none, bsp.INT4)
     assert t.codes.shape == (0, 32) and t.scale.shape == (0,)
     assert bsp.dequantize_tokens(t.codes, t.scale, bsp.INT4, 64).shape == (0, 64)
+
+
+@pytest.mark.parametrize("dtype", [bsp.INT8, bsp.INT4])
+@pytest.mark.parametrize("K", [100, 129, 164, 256, 257, 300, 511, 513])
+def test_many_short_tokens(dtype, K, dev):
+    # as many as change how a token is spread over lanes: the same codes as in short calls, and the oracle's
+    rng = np.random.default_rng(K)
+    n = 16390
+    X = np.tile(_rows(rng, 1639, K), (10, 1))
+    weight = (1 + 0.2 * rng.normal(0, 1, K)).astype(np.float16)
+    x, w = torch.from_numpy(X).to(dev), torch.from_numpy(weight).to(dev)
+    t = bsp.quantize_tokens(x, dtype, weight=w, eps=1e-5, residual=x)
+    for i in range(0, n, 1490):
+        s = bsp.quantize_tokens(x[i:i + 1490], dtype, weight=w, eps=1e-5, residual=x[i:i + 1490])
+        assert torch.equal(t.codes[i:i + 1490], s.codes) and torch.equal(t.hidden[i:i + 1490].isnan(), s.hidden.isnan())
+    last = bsp.Tokens(t.codes[-60:], t.scale[-60:], None, t.hidden[-60:])
+    check(last, X[-60:], dtype, weight, 1e-5, X[-60:], dev)
