@@ -3,7 +3,7 @@
 //
 // One lane holds 8 channels of a head (a 16-byte piece), as in the cache kernels: a
 // head is 8, 16 or 32 lanes and a wavefront holds 8, 4 or 2 of them, neighbouring
-// heads of one token and one kind (query, key or value), in U such groups.
+// heads of one token and one kind (query, key or value; of several where heads are few), in U such groups.
 //
 // The angle of pair i at position p is p * freq[i] turns, freq in units of 2^-64
 // turns: the product mod 2^64 is the angle mod one turn, exactly. Split into a multiple
@@ -53,7 +53,7 @@ struct QkArgs {
     int64_t nslots;
     float eps;
     int heads[3];                 // heads of each kind; values: 0 without a cache
-    uint32_t parts[3];            // running number of a token's items: queries, keys, values
+    uint32_t parts[3];            // running number of a token's items: queries, keys, values (MIX: the last is all)
     uint32_t n;
     int kind, page_shift, rot, interleaved;
 };
@@ -93,7 +93,8 @@ __device__ __forceinline__ void qk_store(uint16_t *p, kv_u4 v) { __builtin_memcp
 
 typedef float qk_f4 __attribute__((ext_vector_type(4)));
 
-template <int D, int U>
+// MIX: queries, keys and values follow each other without a gap, and a wavefront may hold some of two kinds or all.
+template <int D, int U, bool MIX>
 __global__ __launch_bounds__(QK_BLOCK) void k_qk_heads(const QkArgs a, uint32_t items) {
     constexpr int LPR = D / 8, RPW = 64 / LPR;
     __shared__ __align__(16) float turns[QK_BLOCK / 64][2][D / 2];      // each wavefront's cosines and sines
@@ -101,25 +102,35 @@ __global__ __launch_bounds__(QK_BLOCK) void k_qk_heads(const QkArgs a, uint32_t 
     const uint32_t item = __builtin_amdgcn_readfirstlane(blockIdx.x * (QK_BLOCK / 64) + wave);
     if (item >= items) return;
     const uint32_t token = item / a.parts[2], part = item - token * a.parts[2];
-    const int kind = part < a.parts[0] ? 0 : part < a.parts[1] ? 1 : 2;
-    const int first = (int)(part - (kind == 0 ? 0 : a.parts[kind - 1])) * (RPW * U);
-    const int heads = a.heads[kind];
+    const int h1 = a.heads[0], h2 = h1 + a.heads[1];
+    const int one = part < a.parts[0] ? 0 : part < a.parts[1] ? 1 : 2;      // the kind of all rows, unless MIX
+    const int first = MIX ? (int)part * (RPW * U)
+                          : one == 0 ? (int)part * (RPW * U)
+                          : one == 1 ? h1 + (int)(part - a.parts[0]) * (RPW * U)
+                                     : h2 + (int)(part - a.parts[1]) * (RPW * U);
+    const int rows = !MIX && one == 0 ? h1 : !MIX && one == 1 ? h2 : h2 + a.heads[2];
+    auto kind_of = [&](int r) { return !MIX ? one : r < h1 ? 0 : r < h2 ? 1 : 2; };
     const int ch = (lane % LPR) * 8;
-    const uint16_t *src = a.x[kind] + (int64_t)token * a.xs[kind];
+    // where row r would lie if it were a query, a key, a value
+    const uint16_t *const qs = a.x[0] + (int64_t)token * a.xs[0], *const ks = a.x[1] + (int64_t)token * a.xs[1] - (int64_t)h1 * D,
+                   *const vs = a.x[2] + (int64_t)token * a.xs[2] - (int64_t)h2 * D;
+    int place[U];
     kv_u4 raw[U];
+    kv_h8 w[U];
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-        // heads past the last are read as head 0, so that every lane of the shuffles holds a value
-        const int h = first + i * RPW + lane / LPR;
-        raw[i] = qk_load(src + (int64_t)(h < heads ? h : 0) * D + ch);
+        // rows past the last are read as the item's first, so that every lane of the reductions holds a value
+        place[i] = first + i * RPW + lane / LPR;
+        const int r = place[i] < rows ? place[i] : first;
+        const int kind = kind_of(r);
+        raw[i] = qk_load((kind == 0 ? qs : kind == 1 ? ks : vs) + (int64_t)r * D + ch);
+        const uint16_t *weight = kind == 0 ? a.weight[0] : kind == 1 ? a.weight[1] : nullptr;
+        if (weight != nullptr) w[i] = __builtin_bit_cast(kv_h8, *reinterpret_cast<const kv_u4 *>(weight + ch));
     }
-    const int rot = kind == 2 ? 0 : a.rot, half = rot / 2;
-    const uint16_t *weight = kind == 2 ? nullptr : a.weight[kind];
+    const int rot = first < h2 ? a.rot : 0, half = rot / 2;
     float cs[8], sn[8];
-    kv_h8 w;
     int partner = lane;
     const bool turned = ch < rot;
-    if (weight != nullptr) w = __builtin_bit_cast(kv_h8, *reinterpret_cast<const kv_u4 *>(weight + ch));
     if (rot > 0) {
         // each pair's angle once for the wavefront, by way of its own LDS
         const int32_t p = a.positions[token];
@@ -147,21 +158,21 @@ __global__ __launch_bounds__(QK_BLOCK) void k_qk_heads(const QkArgs a, uint32_t 
             }
         }
     }
-    const int64_t slot = a.o[1] == nullptr && kind > 0 ? a.slots[token] : -1;
+    const int64_t slot = a.o[1] == nullptr && first + RPW * U > h1 ? a.slots[token] : -1;
     const bool stored = slot >= 0 && slot < a.nslots;
     const int64_t page = (stored ? slot : 0) >> a.page_shift;
     const int64_t off = (stored ? slot : 0) & (((int64_t)1 << a.page_shift) - 1);
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-        const int h = first + i * RPW + lane / LPR;
-        const bool live = h < heads;
-        if (kind != 2) {
+        const bool live = place[i] < rows;
+        const int r = live ? place[i] : first, kind = kind_of(r);
+        if (kind < 2) {
 #pragma clang fp contract(off)
             const kv_h8 x = __builtin_bit_cast(kv_h8, raw[i]);
             float y[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) y[e] = (float)x[e];
-            if (weight != nullptr) {
+            if ((kind == 0 ? a.weight[0] : a.weight[1]) != nullptr) {
                 float sum;
                 if constexpr (D == 64)
                     sum = ((y[0] * y[0] + y[1] * y[1]) + (y[2] * y[2] + y[3] * y[3])) +
@@ -171,11 +182,11 @@ __global__ __launch_bounds__(QK_BLOCK) void k_qk_heads(const QkArgs a, uint32_t 
                           (((y[4] * y[4] + y[5] * y[5]) + y[6] * y[6]) + y[7] * y[7]);
 #pragma unroll
                 for (int d = 1; d < LPR; d <<= 1) sum += kv_other(sum, d);
-                const float r = sqrtf(sum * (1.0f / D) + a.eps), rc = 1.0f / r, rz = r < INFINITY ? r : 0.0f;
+                const float root = sqrtf(sum * (1.0f / D) + a.eps), rc = 1.0f / root, rz = root < INFINITY ? root : 0.0f;
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     const float q0 = y[e] * rc;
-                    y[e] = __builtin_fmaf(__builtin_fmaf(-q0, rz, y[e]), rc, q0) * (float)w[e];
+                    y[e] = __builtin_fmaf(__builtin_fmaf(-q0, rz, y[e]), rc, q0) * (float)w[i][e];
                 }
             }
             if (rot > 0 && !a.interleaved) {
@@ -197,11 +208,13 @@ __global__ __launch_bounds__(QK_BLOCK) void k_qk_heads(const QkArgs a, uint32_t 
                 raw[i][e] = bsp_f2h(bsp_rounded(y[2 * e])) | ((uint32_t)bsp_f2h(bsp_rounded(y[2 * e + 1])) << 16);
         }
         if (kind == 0 || a.o[1] != nullptr) {
-            if (live) qk_store(a.o[kind] + (int64_t)token * a.os[kind] + (int64_t)h * D + ch, raw[i]);
+            uint16_t *o = kind == 0 ? a.o[0] + (int64_t)token * a.os[0] : a.o[1] + (int64_t)token * a.os[1] - (int64_t)h1 * D;
+            if (live) qk_store(o + (int64_t)r * D + ch, raw[i]);
             continue;
         }
-        const int64_t row = ((page * heads + (live ? h : 0)) << a.page_shift) + off;
-        uint8_t *codes = a.codes[kind - 1];
+        const bool value = kind == 2;
+        const int64_t row = ((page * a.heads[1] + (r - (value ? h2 : h1))) << a.page_shift) + off;
+        uint8_t *codes = value ? a.codes[1] : a.codes[0];
         if (a.kind == BSP_FP16) {
             if (live && stored) *reinterpret_cast<kv_u4 *>(codes + row * (2 * D) + 2 * ch) = raw[i];
         } else {
@@ -212,17 +225,18 @@ __global__ __launch_bounds__(QK_BLOCK) void k_qk_heads(const QkArgs a, uint32_t 
                 kv_store_codes<BSP_INT8>(codes, row * D + ch, u);
             else
                 kv_store_codes<BSP_INT4>(codes, row * D + ch, u);
-            if (ch == 0) a.words[kind - 1][row] = word;
+            if (ch == 0) (value ? a.words[1] : a.words[0])[row] = word;
         }
     }
 }
 
 // A launch holds fewer than 2^32 threads: more tokens go in several.
-template <int D, int U>
+template <int D, int U, bool MIX>
 void qk_launch_u(const QkArgs &all, hipStream_t stream) {
     constexpr int RUN = 64 / (D / 8) * U;
     uint32_t parts[3], total = 0;
     for (int k = 0; k < 3; ++k) parts[k] = total += (uint32_t)((all.heads[k] + RUN - 1) / RUN);
+    if (MIX) parts[2] = total = (uint32_t)((all.heads[0] + all.heads[1] + all.heads[2] + RUN - 1) / RUN);
     const uint32_t most = std::max<uint32_t>((UINT32_C(1) << 25) / total, 1);
     for (uint32_t t = 0; t < all.n; t += std::min(most, all.n - t)) {
         QkArgs a = all;
@@ -236,7 +250,7 @@ void qk_launch_u(const QkArgs &all, hipStream_t stream) {
         if (a.slots != nullptr) a.slots += t;
         const uint32_t items = a.n * total;
         const unsigned grid = (items + QK_BLOCK / 64 - 1) / (QK_BLOCK / 64);
-        hipLaunchKernelGGL((k_qk_heads<D, U>), dim3(grid), dim3(QK_BLOCK), 0, stream, a, items);
+        hipLaunchKernelGGL((k_qk_heads<D, U, MIX>), dim3(grid), dim3(QK_BLOCK), 0, stream, a, items);
     }
 }
 
@@ -244,12 +258,27 @@ void qk_launch_u(const QkArgs &all, hipStream_t stream) {
 // 79 against 94; 512 x 64 6.8 against 7.1, 512 x 80 7.5 against 7.7; 128 x 80 5.0 against 4.4). Heads of 64, 8 to
 // a group, gain nothing (8192 x 40 20.5 against 20.6, with an int8 cache 28.4 against 26.2), nor do those of 256 (23.7
 // against 25.5, 32.1 against 30.9).
+//
+// Kinds mixed in a wavefront where that takes over a twelfth fewer of them: 8192 tokens x (5 + 1) heads of 128 10.3 us against 14.2,
+// (28 + 4, with values, into an int8 cache) 33.5 against 37.8, (8 + 2 + 2) heads of 64 x 6120 9.2 against 10.3. Where it
+// takes as many, what is then found out lane by lane costs more: (32 + 32) 56.3 against 51.8.
+template <int D, int U>
+void qk_launch_mix(const QkArgs &a, hipStream_t stream) {
+    constexpr int RUN = 64 / (D / 8) * U;
+    int apart = 0, all = 0;
+    for (int k = 0; k < 3; ++k) apart += (a.heads[k] + RUN - 1) / RUN, all += a.heads[k];
+    if (12 * ((all + RUN - 1) / RUN) < 11 * apart)
+        qk_launch_u<D, U, true>(a, stream);
+    else
+        qk_launch_u<D, U, false>(a, stream);
+}
+
 template <int D>
 void qk_launch(const QkArgs &a, hipStream_t stream) {
     if (D == 128 && (int64_t)a.n * (a.heads[0] + a.heads[1] + a.heads[2]) >= 32768)
-        qk_launch_u<128, 2>(a, stream);
+        qk_launch_mix<128, 2>(a, stream);
     else
-        qk_launch_u<D, 1>(a, stream);
+        qk_launch_mix<D, 1>(a, stream);
 }
 
 int qk_common(QkArgs &a, int64_t n, int64_t hq, int64_t hkv, int64_t D, const bsp_rotation *r, bool values,

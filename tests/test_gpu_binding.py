@@ -133,3 +133,38 @@ def test_calls_from_several_threads(dev):
     torch.cuda.synchronize()
     for a, b in zip(got, want):
         assert torch.equal(a.codes, b.codes) and torch.equal(a.scale, b.scale)
+
+
+def test_calls_from_several_threads(dev):
+    # each on a stream and a workspace of its own; the launch gives up the interpreter's lock
+    rng = np.random.default_rng(12)
+    W = rng.integers(-128, 128, (512, 11008)).astype(np.int8)
+    enc = bsp.encode_int8(W, np.full(512, 1e-4, np.float32)).to_device(dev)
+    X = torch.from_numpy(rng.normal(0, 1, (600, 11008)).astype(np.float16)).to(dev)
+    t = bsp.quantize_tokens(X, bsp.INT8)
+    want = bsp.gemm_w8a8(enc, t.codes, t.scale)
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work():
+        try:
+            stream = torch.cuda.Stream()
+            with torch.cuda.stream(stream):
+                ws = bsp.new_gemm_workspace(enc, 600, device=dev)
+                for n in (600, 1, 33, 600, 257, 16):
+                    q = bsp.quantize_tokens(X[:n], bsp.INT8)
+                    Y = bsp.gemm_w8a8(enc, q.codes, q.scale, workspace=ws)
+                    back = bsp.dequantize_tokens(q.codes, q.scale, bsp.INT8, 11008)
+                    stream.synchronize()
+                    if not (torch.equal(Y, want[:n]) and torch.equal(q.codes, t.codes[:n]) and torch.isfinite(back).all()):
+                        wrong.append(n)
+        except Exception as e:
+            wrong.append(e)
+
+    threads = [threading.Thread(target=work) for _ in range(4)]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    torch.cuda.synchronize()
+    assert not wrong
