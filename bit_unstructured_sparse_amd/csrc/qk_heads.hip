@@ -42,7 +42,7 @@ namespace {
 
 struct QkArgs {
     const uint16_t *x[3];         // query, key, value heads
-    uint16_t *o[2];               // their results (o[1] null: keys go to the cache)
+    uint16_t *o[2];               // their results (cached: o[0] alone)
     int64_t xs[3], os[2];         // token strides in elements
     const uint16_t *weight[2];
     const uint64_t *freq;
@@ -56,6 +56,7 @@ struct QkArgs {
     uint32_t parts[3];            // running number of a token's items: queries, keys, values (MIX: the last is all)
     uint32_t n;
     int kind, page_shift, rot, interleaved;
+    bool cached;                  // keys and values go to the cache
 };
 
 // sin and cos of t * 2^-64 turns, rounded to 32 bits.
@@ -158,7 +159,8 @@ __global__ __launch_bounds__(QK_BLOCK) void k_qk_heads(const QkArgs a, uint32_t 
             }
         }
     }
-    const int64_t slot = a.o[1] == nullptr && first + RPW * U > h1 ? a.slots[token] : -1;
+    // (an item of queries alone has no slot to read: without kv heads there need be none)
+    const int64_t slot = a.cached && min(first + RPW * U, rows) > h1 ? a.slots[token] : -1;
     const bool stored = slot >= 0 && slot < a.nslots;
     const int64_t page = (stored ? slot : 0) >> a.page_shift;
     const int64_t off = (stored ? slot : 0) & (((int64_t)1 << a.page_shift) - 1);
@@ -207,7 +209,7 @@ __global__ __launch_bounds__(QK_BLOCK) void k_qk_heads(const QkArgs a, uint32_t 
             for (int e = 0; e < 4; ++e)
                 raw[i][e] = bsp_f2h(bsp_rounded(y[2 * e])) | ((uint32_t)bsp_f2h(bsp_rounded(y[2 * e + 1])) << 16);
         }
-        if (kind == 0 || a.o[1] != nullptr) {
+        if (kind == 0 || !a.cached) {
             uint16_t *o = kind == 0 ? a.o[0] + (int64_t)token * a.os[0] : a.o[1] + (int64_t)token * a.os[1] - (int64_t)h1 * D;
             if (live) qk_store(o + (int64_t)r * D + ch, raw[i]);
             continue;
@@ -291,6 +293,7 @@ int qk_common(QkArgs &a, int64_t n, int64_t hq, int64_t hkv, int64_t D, const bs
     if ((((uintptr_t)r->q_weight | (uintptr_t)r->k_weight) & 15u) != 0) return BSP_E_ARG;
     if (n == 0 || hq + hkv == 0) return BSP_OK;
     const int64_t heads[3] = {hq, hkv, values ? hkv : 0};
+    a.cached = values;
     uintptr_t bits = 0;
     for (int k = 0; k < 3; ++k) {
         a.heads[k] = (int)heads[k];
