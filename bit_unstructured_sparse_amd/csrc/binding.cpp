@@ -58,9 +58,22 @@ constexpr int arity(int (*)(A...)) {
 
 #define MOST_ARGS 20
 
+enum Kind : char { WHOLE, REAL, ADDRESS };
+
+template <class T>
+constexpr Kind kind_of = std::is_pointer_v<T> ? ADDRESS : std::is_floating_point_v<T> ? REAL : WHOLE;
+
+template <class Fn>
+struct Kinds;
+template <class... A>
+struct Kinds<int (*)(A...)> {
+    static constexpr Kind of[] = {kind_of<A>...};
+};
+
 struct Entry {
     const char *name;
     int args;
+    const Kind *kinds;      // of its arguments
     int (*invoke)(void *, const Arg *);
     PyObject *object;      // the library's function object, as the binding passes it
     void *address;
@@ -72,7 +85,7 @@ int invoke(void *address, const Arg *v) {
 }
 
 // (declarations only: the addresses come from the library that the binding has loaded)
-#define ENTRY(name) {#name, arity(decltype(&name){}), invoke<decltype(&name)>, nullptr, nullptr}
+#define ENTRY(name) {#name, arity(decltype(&name){}), Kinds<decltype(&name)>::of, invoke<decltype(&name)>, nullptr, nullptr}
 
 Entry entries[] = {
     ENTRY(kv_cache_append),     ENTRY(kv_cache_gather),         ENTRY(attention_tree_f16),
@@ -80,8 +93,9 @@ Entry entries[] = {
     ENTRY(quantize_tokens_f16), ENTRY(dequantize_tokens_f16),   ENTRY(gemm_w8a8_dq),
 };
 
-// A plain integer, None, bytes or float as an argument; false for anything else.
-bool argument(PyObject *o, Arg &a) {
+// What ctypes takes for an argument of its kind, as a plain integer, None or bytes (addresses) or float; false for
+// anything else.
+bool argument(PyObject *o, Kind kind, Arg &a) {
     a.d = 0.0;
     if (PyLong_CheckExact(o)) {
         a.i = (int64_t)PyLong_AsUnsignedLongLongMask(o);
@@ -90,9 +104,9 @@ bool argument(PyObject *o, Arg &a) {
         a.d = (double)a.i;
         return overflow == 0;
     }
-    if (o == Py_None) return a.i = 0, true;
-    if (PyBytes_CheckExact(o)) return a.i = (int64_t)(uintptr_t)PyBytes_AS_STRING(o), true;
-    if (PyFloat_CheckExact(o)) return a.i = 0, a.d = PyFloat_AS_DOUBLE(o), true;
+    if (kind == ADDRESS && o == Py_None) return a.i = 0, true;
+    if (kind == ADDRESS && PyBytes_CheckExact(o)) return a.i = (int64_t)(uintptr_t)PyBytes_AS_STRING(o), true;
+    if (kind == REAL && PyFloat_CheckExact(o)) return a.i = 0, a.d = PyFloat_AS_DOUBLE(o), true;
     return false;
 }
 
@@ -191,7 +205,7 @@ PyObject *launch(PyObject *, PyObject *const *a, Py_ssize_t n) {
             if (e.object != a[0] || e.address == nullptr) continue;
             Arg v[MOST_ARGS];
             bool good = e.args == (int)n - 2 && e.args <= MOST_ARGS;
-            for (Py_ssize_t i = 3; good && i < n; ++i) good = argument(a[i], v[i - 3]);
+            for (Py_ssize_t i = 3; good && i < n; ++i) good = argument(a[i], e.kinds[i - 3], v[i - 3]);
             if (!good || c10::hip::current_device() != index) break;
             v[e.args - 1].i = (int64_t)(uintptr_t)c10::hip::getCurrentHIPStream((c10::DeviceIndex)index).stream();
             int status;
