@@ -86,11 +86,20 @@ def _library(out: str, sources, pool, verbose: bool) -> str:
 
 
 def _binding(verbose: bool) -> None:
+    """The native module, where it can be built. Where it cannot (no host compiler, no headers or GPU libraries of
+    PyTorch) that is reported, and the binding's Python functions do its work: one of other sources must not stay."""
     tmp = BINDING + f".tmp{os.getpid()}"
     cmd = binding_command(tmp)
-    if cmd is not None:
+    if cmd is None:
+        return
+    try:
         _run(cmd, verbose)
         os.replace(tmp, BINDING)
+    except (RuntimeError, OSError) as e:
+        for left in (tmp, BINDING):
+            if os.path.exists(left):
+                os.remove(left)
+        print(f"{os.path.basename(BINDING)} not built, calls go through ctypes: {e}", file=sys.stderr, flush=True)
 
 
 def build(verbose: bool = False) -> str:
