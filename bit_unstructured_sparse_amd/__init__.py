@@ -1138,7 +1138,8 @@ def kv_step(pages: KVPages, keep, new_tokens, rows: int, tree_mask=None, out: Op
     rows. Pages that are no longer needed go back, those needed are taken; block_table, lens, held and free are
     updated in place. tree_mask: int64 [rows], attention_tree's: positions follow the depth in the tree. A sequence
     whose pages (or rows) do not fit waits: its slots are -1 and its kv_lens 0, and it keeps its kept tokens. Rows behind
-    the last sequence get slot -1, position 0, sequence -1."""
+    the last sequence get slot -1, position 0, sequence -1. out: tensors for the
+    results, over none of the call's inputs or pages (refused otherwise)."""
     import torch
     ref, i32 = pages._pointer(), torch.int32
     index, B = pages._index, pages.sequences

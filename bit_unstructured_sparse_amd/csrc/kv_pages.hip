@@ -181,6 +181,28 @@ __global__ __launch_bounds__(PG_BLOCK) void k_pages_step(const PgArgs a) {
     }
 }
 
+// Whether a result lies over an input, the state or another result: workgroups read the inputs while others write.
+bool pg_overlap(const bsp_kv_pages *p, const int32_t *keep, const int32_t *more, const uint64_t *mask, int64_t rows,
+                const int64_t *slots, const int32_t *positions, const int32_t *sequences, const int32_t *q_start,
+                const int32_t *kv_lens) {
+    struct {
+        const void *at;
+        int64_t bytes;
+    } r[] = {{slots, rows * 8}, {positions, rows * 4}, {sequences, rows * 4}, {q_start, (p->sequences + 1) * 4},
+             {kv_lens, p->sequences * 4},      // the results, then what must not be under them
+             {keep, p->sequences * 4}, {more, p->sequences * 4}, {mask, rows * 8}, {p->lens, p->sequences * 4},
+             {p->held, p->sequences * 4}, {p->block_table, p->sequences * p->table_width * 4},
+             {p->free_pages, (p->pool + 2) * 4}};
+    constexpr int ALL = sizeof r / sizeof r[0];
+    for (int i = 0; i < 5; ++i)
+        for (int j = i + 1; j < ALL; ++j) {
+            if (r[i].at == nullptr || r[j].at == nullptr || r[i].bytes == 0 || r[j].bytes == 0) continue;
+            const uintptr_t a = (uintptr_t)r[i].at, b = (uintptr_t)r[j].at;
+            if (a < b + (uintptr_t)r[j].bytes && b < a + (uintptr_t)r[i].bytes) return true;
+        }
+    return false;
+}
+
 }  // namespace
 
 extern "C" int kv_pages_step(const bsp_kv_pages *pages, const int32_t *keep, const int32_t *new_tokens,
@@ -205,6 +227,7 @@ extern "C" int kv_pages_step(const bsp_kv_pages *pages, const int32_t *keep, con
           (uintptr_t)q_start | (uintptr_t)kv_lens) & 3u) != 0)
         return BSP_E_ARG;
     if ((((uintptr_t)slots | (uintptr_t)tree_mask) & 7u) != 0) return BSP_E_ARG;
+    if (pg_overlap(p, keep, new_tokens, tree_mask, rows, slots, positions, sequences, q_start, kv_lens)) return BSP_E_ARG;
     PgArgs a{};
     a.table = p->block_table, a.lens = p->lens, a.held = p->held, a.free_pages = p->free_pages;
     a.keep = keep, a.more = new_tokens, a.mask = tree_mask;

@@ -681,8 +681,8 @@ typedef struct bsp_kv_pages {
  * takes pages and the pages taken up to it are more than there are (then so do the
  * later ones that take pages): it keeps its pages and its kept tokens, appends none,
  * gets slots -1 and kv_lens 0 (attention then gives zeros for its rows).
- * Calls on the same pages must be ordered on one stream. The outputs must not overlap
- * the inputs.
+ * Calls on the same pages must be ordered on one stream. An output that overlaps an
+ * input, the pages' arrays or another output is refused (BSP_E_ARG); keep may be lens.
  */
 int kv_pages_step(const bsp_kv_pages *pages, const int32_t *keep, const int32_t *new_tokens,
                   const uint64_t *tree_mask, int64_t rows, int64_t *slots, int32_t *positions, int32_t *sequences,
