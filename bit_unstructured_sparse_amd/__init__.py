@@ -31,7 +31,7 @@ __all__ = ["load_library", "encode", "pack_int4", "Encoded", "DeviceMatrix", "sp
            "spmm_f16_lora", "spmm_w4a4_dq_lora", "lora_workspace_bytes", "new_lora_workspace", "KVPages", "new_kv_pages",
            "KVStep", "kv_step", "rope_frequencies", "qk_norm_rope", "qk_norm_rope_append", "Tokens", "quantize_tokens",
            "dequantize_tokens", "EncodedInt8", "DenseInt8", "encode_int8", "gemm_workspace_bytes",
-           "new_gemm_workspace", "gemm_w8a8"]
+           "new_gemm_workspace", "describe_gemm", "gemm_w8a8"]
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 library_path = os.path.join(HERE, "libbitmap_spmm.so")
@@ -54,7 +54,7 @@ EXPORTS = ["encode_bitmap_tiles", "pack_int4_activations", "spmm_bitmap_w4a4", "
            "lora_workspace_bytes", "spmm_bitmap_f16_lora", "spmm_bitmap_w4a4_dq_lora",
            "kv_pages_step", "qk_norm_rope_f16", "qk_norm_rope_append_f16", "quantize_tokens_f16",
            "dequantize_tokens_f16", "int8_tiles_bytes", "encode_int8_tiles", "gemm_w8a8_workspace_bytes",
-           "gemm_w8a8_dq"]
+           "gemm_w8a8_describe", "gemm_w8a8_dq"]
 
 
 class BspError(RuntimeError):
@@ -145,6 +145,8 @@ def load_library():
         L.int8_tiles_bytes.argtypes, L.int8_tiles_bytes.restype = [I64, I64], I64
         L.encode_int8_tiles.argtypes, L.encode_int8_tiles.restype = [P, I64, I64, I64, P], I32
         L.gemm_w8a8_workspace_bytes.argtypes, L.gemm_w8a8_workspace_bytes.restype = [I64, I64, I64, P], I32
+        L.gemm_w8a8_describe.argtypes = [I64, I64, I64, I32, ctypes.c_char_p, ctypes.c_size_t]
+        L.gemm_w8a8_describe.restype = I32
         L.gemm_w8a8_dq.argtypes = [P, I64, I64, P, I64, I64, P, P, P, I64, P, I64, P]
         L.gemm_w8a8_dq.restype = I32
         _lib = L
@@ -1433,6 +1435,13 @@ def new_gemm_workspace(W: DenseInt8, N: int, device="cuda"):
     import torch
     n = gemm_workspace_bytes(W.M, W.K, N)
     return torch.zeros(n, dtype=torch.uint8, device=device) if n else None
+
+
+def describe_gemm(M: int, K: int, N: int, workspace: bool = False) -> str:
+    """The kernel, tile (channels x tokens) and split of K that gemm_w8a8 takes."""
+    buf = ctypes.create_string_buffer(256)
+    _check(load_library().gemm_w8a8_describe(M, K, N, int(workspace), buf, 256), "gemm_w8a8_describe")
+    return buf.value.decode()
 
 
 def gemm_w8a8(W: DenseInt8, X, scale_x, Y=None, workspace=None, stream=None):

@@ -26,6 +26,8 @@
 // workgroup that stays and loads its next tile under the results' stores took 354.
 #include <hip/hip_runtime.h>
 
+#include <stdio.h>
+
 #include <algorithm>
 #include <atomic>
 #include <type_traits>
@@ -587,14 +589,22 @@ typedef void (*W8Run)(W8Args &, hipStream_t);
 struct W8Shape {
     int bands, blocks;       // a workgroup's tile, in 16s
     W8Run run;
+    const char *name;
 };
+
+#define W8_STREAM(W, U) {1, 1, w8_stream<W, U>, "k_w8_stream<" #W ", " #U ">"}
+#define W8_RING(NB, MB, W, P) {MB, NB, w8_ring<NB, MB, W, P>, "k_w8_ring<" #NB ", " #MB ", " #W ", " #P ">"}
+#define W8_TILES(WM, WN, TM, TN, KS, R) \
+    {WM * TM, WN * TN, w8_tiles<WM, WN, TM, TN, KS, R>, "k_w8_tiles<" #WM ", " #WN ", " #TM ", " #TN ", " #KS ", " #R ">"}
 
 // The first six split K over their wavefronts, the others the tile.
 const W8Shape W8_SHAPES[] = {
-    {1, 1, w8_ring<1, 1, 16, 2>}, {1, 2, w8_ring<2, 1, 8, 2>}, {2, 2, w8_ring<2, 2, 8, 2>}, {1, 4, w8_ring<4, 1, 4, 3>},
-    {4, 2, w8_ring<2, 4, 6, 2>}, {2, 4, w8_ring<4, 2, 6, 2>}, {4, 4, w8_tiles<2, 2, 2, 2, 4, 3>}, {8, 4, w8_tiles<2, 2, 4, 2, 2, 3>},
-    {8, 8, w8_tiles<2, 4, 4, 2, 1, 4>}, {16, 8, w8_tiles<2, 4, 8, 2, 1, 4>}, {16, 16, w8_tiles<2, 4, 8, 4, 1, 3>},
+    W8_RING(1, 1, 16, 2), W8_RING(2, 1, 8, 2), W8_RING(2, 2, 8, 2), W8_RING(4, 1, 4, 3), W8_RING(2, 4, 6, 2),
+    W8_RING(4, 2, 6, 2), W8_TILES(2, 2, 2, 2, 4, 3), W8_TILES(2, 2, 4, 2, 2, 3), W8_TILES(2, 4, 4, 2, 1, 4),
+    W8_TILES(2, 4, 8, 2, 1, 4), W8_TILES(2, 4, 8, 4, 1, 3),
 };
+// For few tokens alone (w8_plan).
+const W8Shape W8_STREAM_16 = W8_STREAM(16, 2), W8_STREAM_8 = W8_STREAM(8, 4), W8_RING_4 = W8_RING(1, 1, 4, 2);
 
 #define W8_COUNTERS 16384      // arrival counters at the head of a workspace (64 KB, as everywhere in the library)
 #define W8_SPLIT_TILES 256     // more tiles fill the card without splits
@@ -604,7 +614,7 @@ static_assert(W8_SPLIT_TILES <= W8_COUNTERS, "an arrival counter a tile");
 #define W8_MOST_ROWS (W8_MOST_TILES * 16)
 
 struct W8Plan {
-    W8Run run;
+    const W8Shape *shape;
     int splits, per;
     int64_t part_bytes;      // of all tiles and splits
 };
@@ -616,8 +626,8 @@ struct W8Plan {
 W8Plan w8_plan(int64_t bands, int64_t ktiles, int64_t n, bool split) {
     const int k = (int)ktiles;
     if (k == 0 || (n <= 4 && bands * ktiles >= 32768))
-        return {bands > 512 && ktiles < 128 ? w8_stream<8, 4> : w8_stream<16, 2>, 1, k, 0};
-    if (n <= 16 && bands > 256) return {w8_ring<1, 1, 4, 2>, 1, k, 0};
+        return {bands > 512 && ktiles < 128 ? &W8_STREAM_8 : &W8_STREAM_16, 1, k, 0};
+    if (n <= 16 && bands > 256) return {&W8_RING_4, 1, k, 0};
     W8Plan best{nullptr, 1, k, 0};
     double least = 0.0;
     for (const W8Shape &p : W8_SHAPES) {
@@ -632,13 +642,28 @@ W8Plan w8_plan(int64_t bands, int64_t ktiles, int64_t n, bool split) {
                 bytes = tiles * used * p.bands * p.blocks * 1024;
                 t += 2.5 + 1.3 * splits + (double)bytes * 0.25e-6;
             }
-            if (best.run == nullptr || t < least) best = W8Plan{p.run, used, per, bytes}, least = t;
+            if (best.shape == nullptr || t < least) best = W8Plan{&p, used, per, bytes}, least = t;
         }
     }
     return best;
 }
 
+// The tokens of one launch: so many that tiles of 16 could pass a launch's go in runs.
+int64_t w8_most_tokens(int64_t bands) { return W8_MOST_TILES / bands * 16; }
+
 }  // namespace
+
+extern "C" int gemm_w8a8_describe(int64_t M, int64_t K, int64_t N, int with_workspace, char *buf, size_t n) {
+    if (M < 0 || K < 0 || N < 0 || buf == nullptr || n == 0) return BSP_E_ARG;
+    if (K > BSP_W8_MAX_K || M > W8_MOST_ROWS || N > INT32_MAX) return BSP_E_OVERFLOW;
+    const int at = snprintf(buf, n, "dtype=int8 M=%lld K=%lld N=%lld", (long long)M, (long long)K, (long long)N);
+    if (M == 0 || N == 0 || at < 0 || (size_t)at >= n) return BSP_OK;
+    const int64_t bands = (M + 15) / 16, most = w8_most_tokens(bands);
+    const W8Plan p = w8_plan(bands, (K + 63) / 64, std::min(N, most), with_workspace != 0 && N <= most);
+    snprintf(buf + at, n - at, " -> kernel=%s tile=%dx%d splits=%d", p.shape->name, p.shape->bands * 16, p.shape->blocks * 16,
+             p.splits);
+    return BSP_OK;
+}
 
 extern "C" int gemm_w8a8_workspace_bytes(int64_t M, int64_t K, int64_t N, int64_t *bytes) {
     if (bytes == nullptr || M < 0 || K < 0 || N < 0) return BSP_E_ARG;
@@ -672,8 +697,7 @@ extern "C" int gemm_w8a8_dq(const uint8_t *tiles, int64_t M, int64_t K, const in
     a.tiles = tiles, a.xs = x_stride, a.scale_w = scale_w, a.ys = y_stride;
     a.M = (int)M, a.bands = (int)((M + 15) / 16), a.ktiles = (int)((K + 63) / 64);
     a.last = (int)std::max<int64_t>(x_stride - 16, 0);
-    // so many tokens that tiles of 16 could pass a launch's: in runs
-    const int64_t most = W8_MOST_TILES / a.bands * 16;
+    const int64_t most = w8_most_tokens(a.bands);
     for (int64_t t = 0; t < N; t += most) {
         a.n = std::min(N - t, most);
         a.x = X + t * x_stride, a.scale_x = scale_x + t, a.y = Y + t * y_stride;
@@ -683,7 +707,7 @@ extern "C" int gemm_w8a8_dq(const uint8_t *tiles, int64_t M, int64_t K, const in
             if (workspace_bytes < W8_COUNTERS * 4 + p.part_bytes) return BSP_E_CAPACITY;
             a.counters = (uint32_t *)workspace, a.parts = (uint8_t *)workspace + W8_COUNTERS * 4;
         }
-        p.run(a, stream);
+        p.shape->run(a, stream);
     }
     return hipGetLastError() == hipSuccess ? BSP_OK : BSP_E_HIP;
 }

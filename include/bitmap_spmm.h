@@ -800,6 +800,11 @@ int encode_int8_tiles(const int8_t *W, int64_t M, int64_t K, int64_t ldw, uint8_
  * only. */
 int gemm_w8a8_workspace_bytes(int64_t M, int64_t K, int64_t N, int64_t *bytes);
 
+/* The kernel, its tile (channels x tokens) and over how many workgroups K is split, as gemm_w8a8_dq chooses them
+ * without a workspace (0) or with one of gemm_w8a8_workspace_bytes() (1), written NUL-terminated into buf (at most n bytes).
+ * Host only. */
+int gemm_w8a8_describe(int64_t M, int64_t K, int64_t N, int with_workspace, char *buf, size_t n);
+
 /*
  * gemm_w8a8_dq -- asynchronous on `stream`.
  *   tiles        DEVICE, 16-byte aligned, as encode_int8_tiles wrote them.
