@@ -1,6 +1,9 @@
-"""Calls through the native launch: numbers of another kind are refused as ctypes refuses them."""
+"""Calls through the native launch: numbers of another kind are refused as ctypes refuses them; several threads call on
+the stream they share, and with a workspace of their own."""
 import ctypes
+import threading
 
+import numpy as np
 import pytest
 
 import bit_unstructured_sparse_amd as bsp
@@ -31,3 +34,56 @@ def test_a_number_of_another_kind_is_refused(bad, dev):
         bsp.kv_step(pages, None, lens.view(1), bad, out=out)
     torch.cuda.synchronize()
     assert (O == 5).all() and pages.lens.tolist() == [2]
+
+
+def _threads(work, count=4):
+    wrong = []
+
+    def guarded(i):
+        try:
+            work(i)
+        except Exception as e:
+            wrong.append(e)
+
+    threads = [threading.Thread(target=guarded, args=(i,)) for i in range(count)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not wrong, wrong
+
+
+def test_several_threads_quantise_on_one_stream(dev):
+    # outputs of one thread's calls are freed, and taken by another's, between the calls
+    x = [torch.randn(100, 512, device=dev).half() for _ in range(4)]
+    want = [bsp.quantize_tokens(a, bsp.INT8) for a in x]
+    got = [None] * 4
+    torch.cuda.synchronize()
+
+    def work(i):
+        for _ in range(50):
+            got[i] = bsp.quantize_tokens(x[i], bsp.INT8)
+
+    _threads(work)
+    for a, b in zip(got, want):
+        assert torch.equal(a.codes, b.codes) and torch.equal(a.scale, b.scale)
+
+
+def test_several_threads_multiply_on_one_stream(dev):
+    # K split: parts and counters in a workspace of each thread's own
+    rng = np.random.default_rng(4)
+    enc = bsp.encode_int8(rng.integers(-128, 128, (512, 11008)).astype(np.int8), np.full(512, 1e-4, np.float32)).to_device(dev)
+    X = torch.from_numpy(rng.integers(-128, 128, (400, 11008)).astype(np.int8)).to(dev)
+    s = torch.full((400,), 0.01, device=dev)
+    want = bsp.gemm_w8a8(enc, X, s)
+    ws = [bsp.new_gemm_workspace(enc, 400, device=dev) for _ in range(4)]
+    torch.cuda.synchronize()
+
+    def work(i):
+        for n in (400, 3, 65, 300, 33, 400):
+            Y = bsp.gemm_w8a8(enc, X[:n], s[:n], workspace=ws[i])
+            torch.cuda.current_stream().synchronize()
+            assert torch.equal(Y, want[:n])
+
+    _threads(work)
