@@ -11,17 +11,22 @@
 // ring of its own in LDS by DMA, so that no barrier stands between memory and the matrix instructions
 // (k_w8_ring). Past that a workgroup's wavefronts share the tile and a ring (k_w8_tiles).
 //
-// What bounds them. A CU takes in about 57 KB/us (24 bytes a cycle) of operands, from any level past its
-// L1 and however many are on their way: the time of all but the largest tiles is (bands + blocks) KB per 64
-// columns at that rate (N = 128, 4096 x 4096, 64 x 64 tiles: 8 KB a step, 0.14 us; deeper rings gain
-// under 3 %). It is why tiles are chosen by their bytes, and why four bands and two blocks beat one and
-// four. The 256 x 256 tiles: 8192 tokens x 12288 x 4096 in 332 to 347 us (2,480 TOP/s at best, from box to box and with the
-// power drawn), 62 % of the cycles in matrix instructions at 1.92 GHz, LDS reads and the DMA's writes taking as many
-// cycles as those. Of that time the matrix instructions alone would take 256 us, with the reads from LDS 285, the loads and
-// reads without them 235: it is their meeting. What brought them there from 600 us: operands read one step ahead into a second set of registers
+// What bounds them. The time of all but the largest tiles is (bands + blocks) KB per 64 columns at about 57 KB/us a CU
+// (N = 128, 4096 x 4096, 64 x 64 tiles: 8 KB a step, 0.14 us; deeper rings gain under 3 %). It is why tiles are
+// chosen by their bytes, and why four bands and two blocks beat one and four. That rate is measured on the
+// tiles, a mean over where their operands come from, and not what a CU can take: with each wavefront reading lines of its own and
+// all 256 CUs at it, one takes in 98 to 134 KB/us from its L2, 20 to 28 from the last-level cache and 19 to 23 from memory,
+// in pieces of 64 bytes, 128 or 1 KB (within a quarter of each other, neither form the fastest throughout). 32 tokens x
+// 4096 x 11008: the 45 MB of W alone are 7 of the 10 us at the last-level cache's 6.5 TB/s.
+//
+// The 256 x 256 tiles: 8192 tokens x 12288 x 4096 in 332 to 349 us back to back, 366 in the middle of 50 traced launches
+// (from box to box and with the power drawn; 2,250 to 2,480 TOP/s), 66 % of the cycles in matrix instructions, LDS reads and
+// the DMA's writes taking as many cycles as those. Of that time the matrix instructions alone would take 256 us, with the
+// reads from LDS 285, the loads and reads without them 235: it is their meeting. What brought them there from 600 us:
+// operands read one step ahead into a second set of registers
 // (with the scheduler told to spread the reads: left alone it sinks them behind all matrix instructions),
-// a swizzle that leaves no bank conflict (440 to 385 us), three stages rather than four (less power), the result
-// through LDS in whole rows (366 to 332). 4 wavefronts of 128 x 128 read a
+// a swizzle that leaves the operands' reads no bank conflict (440 to 385 us), three stages rather than four (less power), the
+// result through LDS in whole rows (366 to 332). 4 wavefronts of 128 x 128 read a
 // third less LDS, but need all 512 registers and hide no latency: 490 us, 368 with the accumulators held in place. A
 // workgroup that stays and loads its next tile under the results' stores took 354.
 #include <hip/hip_runtime.h>
@@ -619,10 +624,23 @@ struct W8Plan {
     int64_t part_bytes;      // of all tiles and splits
 };
 
-// A tile's time is that of its operands' way into the CU (a KB of them every 1 / 57 us, whatever the
-// tile) or of its matrix instructions (a 16 x 16 x 64 block every 1 / 330 us), whichever is longer; the tiles of
+// A tile's time is that of its operands' way into the CU (a KB of them every 1 / 57 us, the rate that tiles reach) or of its
+// matrix instructions (a 16 x 16 x 64 block every 1 / 330 us), whichever is longer; the tiles of
 // a CU come one after the other. Splitting K shares a tile among workgroups, which then store and one of which
 // adds the parts: 2.5 us, 1.3 for each, and their bytes at 4 TB/s.
+//
+// Few tokens are tiles of one band, and how many wavefronts share its columns is a matter of how many bands there are
+// (us on the same W again and again / past the last-level cache):
+// - up to 4 tokens and 32 MB of weights W streams past LDS: 1 x 4096 x 8192 4.8 / 7.1, through the ring of 16 wavefronts
+//   5.2 / 9.0; 1 x 12288 x 4096 7.7 / 9.8, through that of 4 7.7 / 11.5; with less the rings do as well (1 x 4096 x 4096 4.0).
+//   Two workgroups of 16 wavefronts are on a CU at once, four of 8: past 512 bands those have no second round (12288 x 4096
+//   7.7, of 16 8.8; 32768 x 1024 5.9 and 7.5; at 512 bands alike, 4.7). Long rows want the wavefronts (12288 x 8192 of 8 14.2,
+//   of 16 13.9; 4096 x 11008 8.5 and 6.6): the border is 128 column tiles (just below it, at 513 bands, 16 would be better:
+//   8208 x 8128 11.9 and 10.6).
+// - up to 16 tokens past 256 bands: the ring of 16 wavefronts fills a CU's LDS, so band 257 waits for a second
+//   round; five of 4 wavefronts fit (8 x 12288 x 4096 7.8 / 11.6, of 16 11.2 / 14.4; 8 x 4112 x 1024 2.7 and 3.8; at 256
+//   bands 8 x 4096 x 4096 5.6, of 16 4.1). Few bands past 256 and long rows lose by it (8 x 4112 x 11008 12.8, of 16 11.3), and
+//   16 x 128256 x 4096 takes 97 for the 88 of the tiles below.
 W8Plan w8_plan(int64_t bands, int64_t ktiles, int64_t n, bool split) {
     const int k = (int)ktiles;
     if (k == 0 || (n <= 4 && bands * ktiles >= 32768))

@@ -22,11 +22,13 @@
 // The mean's squares are added as a 16-byte piece holds them, its halves of four in turn (heads of 64: neighbours
 // first), then the lanes' sums neighbours first.
 //
-// Bound by memory where tokens are many: 8192 tokens, 32 query and 32 key heads of 128, 268 MB in 51.8 us
-// (5.2 TB/s); with values into an fp16 cache 403 MB in 76 us (5.3 TB/s). Into an int8 cache 336 MB take 79 us: a row's
-// codes cost about as many vector instructions as the rotation, and no longer all hide (86 with its minimum and
-// maximum in fp32). (With each lane its own 8 angles a group: 84 and 127 us. With 64-bit sines throughout 55 and 91.) Few
-// tokens are launch latency: 3.8 us, 4.1 with an int8 cache.
+// Bound by memory where tokens and heads are many: 8192 tokens, 32 query and 32 key heads of 128, 268 MB in 48 to 53 us
+// (5.1 to 5.6 TB/s); with values into an fp16 cache 403 MB in 76 us (5.3 TB/s). Into an int8 cache 338 MB take 79 to 83 us,
+// into an int4 one 304 MB 80: a row's codes cost about as many vector instructions as the rotation, and no longer all hide
+// (86 with its minimum and maximum in fp32). (With each lane its own 8 angles a group: 84 and 127 us. With 64-bit sines
+// throughout 55 and 91.) Few heads a token fill a part of a wavefront, which evaluates all of the token's angles all the same:
+// 60000 tokens x (1 + 1) heads of 64 25 us, of 128 38, 8192 x (8 + 1, with values) of 256 into an int8 cache 26, where the bytes
+// take 6.4, 12.9 and 16.7 us at the rate of a copy (4.77 TB/s). Few tokens are launch latency: 3.8 us, 3.9 with an int8 cache.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>

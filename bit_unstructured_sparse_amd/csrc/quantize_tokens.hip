@@ -12,10 +12,13 @@
 // 16384 channels; longer tokens are read twice). Rounding is by adding 1.5 * 2^23, which leaves a code in
 // the low bits; the exact comparison is one branch for 8 channels.
 //
-// Bound by memory where tokens are many: 8191 x 8192 with residual and norm to int8, and back, 671 MB in 111 us
+// Bound by memory where tokens are many and long: 8191 x 8192 with residual and norm to int8, and back, 671 MB in 111 to 116 us
 // (6.0 TB/s, part of it the last-level cache's; the sums' inputs are read past it, which leaves the codes there: 133 us
-// otherwise). Odd rows cost little more, their pieces are read and written whole at any address: 4096 x 11007 51 us,
-// 4096 x 11008 42 (146 with single values). Few tokens are launch latency: one token of 4096 3.5 us, back 2.9.
+// otherwise), to int4 77 of them and back 26. Odd rows cost more, their pieces are read and written whole at any address: 4096 x
+// 11007, normed, 50 us, 4096 x 11008 39 (146 with single values). Many short tokens have one or two pieces a lane on their way,
+// and read the weight again for each: 16384 x 164 with residual and norm 7.5 us, 32768 x 300 23, where the bytes take 3.9
+// and 14.4 at the rate of a copy (4.77 TB/s). Few tokens are launch latency: one token of 4096 2.9 us, back 2.0 (3.3 and
+// 2.5 in a graph).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>

@@ -725,7 +725,8 @@ int qk_norm_rope_f16(const uint16_t *Q, int64_t q_stride, const uint16_t *K, int
 /*
  * qk_norm_rope_append_f16 -- the same, with the keys (rounded to fp16) and the
  * values V written to the cache's slots: bit for bit what qk_norm_rope_f16 and
- * kv_cache_append leave there, in one pass. slots as for kv_cache_append.
+ * kv_cache_append leave there, in one pass. slots as for kv_cache_append. Without kv heads (here and above) the queries
+ * alone are worked on, and what belongs to keys and values may be NULL, slots among it.
  */
 int qk_norm_rope_append_f16(const uint16_t *Q, int64_t q_stride, const uint16_t *K, int64_t k_stride,
                             const uint16_t *V, int64_t v_stride, int64_t n, int64_t q_heads,
