@@ -15,10 +15,11 @@
 // workgroup to finish, which an arrival counter beside the count names.
 //
 // Short calls are bound by latency: dependent trips to memory (lengths; a row's page; the state) beside an empty launch's
-// 1.8 us. 32 sequences of one token 3.3 us (3.7 in a graph), in one workgroup. Several workgroups have the arrivals at one counter besides, and
-// each computes the sums for itself: 256 with trees (7,700 rows) 5.1 us, 512 with prompts (62,000 rows) 9.6, of which the
-// rows' bytes are 0.3 (at most 256 workgroups: with 64 12.5, with 1024 11.2; with a fence before the arrival 16). Sequences
-// are summed 256 at a time, 1.5 us a time: one token each for 512 of them 6.3 us, for 1,024 9.3, for 4,096 26.6.
+// 1.8 us. 32 sequences of one token 3.3 us (3.7 in a graph), in one workgroup. Several workgroups have the arrivals at
+// one counter besides, and each computes the sums for itself: 256 with trees (7,700 rows) 5.1 us, 512 with prompts (62,000
+// rows) 9.6, of which the rows' bytes are 0.3 (at most 256 workgroups: with 64 12.5, with 1024 11.2; with a fence before
+// the arrival 16). Sequences are summed 256 at a time, about 1.5 us a time: one token each for 512 of them 6.3 us, for
+// 1,024 9.3, for 4,096 26.6.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
