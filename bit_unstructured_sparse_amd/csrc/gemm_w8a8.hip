@@ -19,8 +19,8 @@
 // in pieces of 64 bytes, 128 or 1 KB (within a quarter of each other, neither form the fastest throughout). 32 tokens x
 // 4096 x 11008: the 45 MB of W alone are 7 of the 10 us at the last-level cache's 6.5 TB/s.
 //
-// The 256 x 256 tiles: 8192 tokens x 12288 x 4096 in 332 to 349 us back to back, 366 in the middle of 50 traced launches
-// (from box to box and with the power drawn; 2,250 to 2,480 TOP/s), 66 % of the cycles in matrix instructions, LDS reads and
+// The 256 x 256 tiles: 8192 tokens x 12288 x 4096 in 328 to 349 us back to back, 369 in the middle of 50 traced launches
+// (from box to box and with the power drawn; 2,230 to 2,510 TOP/s), 66 % of the cycles in matrix instructions, LDS reads and
 // the DMA's writes taking as many cycles as those. Of that time the matrix instructions alone would take 256 us, with the
 // reads from LDS 285, the loads and reads without them 235: it is their meeting. What brought them there from 600 us:
 // operands read one step ahead into a second set of registers
