@@ -20,9 +20,9 @@
 // 4096 x 11008: the 45 MB of W alone are 7 of the 10 us at the last-level cache's 6.5 TB/s.
 //
 // The 256 x 256 tiles: 8192 tokens x 12288 x 4096 in 328 to 349 us back to back, 369 in the middle of 50 traced launches
-// (from box to box and with the power drawn; 2,230 to 2,510 TOP/s), 66 % of the cycles in matrix instructions, LDS reads and
-// the DMA's writes taking as many cycles as those. Of that time the matrix instructions alone would take 256 us, with the
-// reads from LDS 285, the loads and reads without them 235: it is their meeting. What brought them there from 600 us:
+// (from machine to machine and with the power drawn; 2,230 to 2,510 TOP/s), 66 % of the cycles in matrix instructions, LDS
+// reads and the DMA's writes taking as many cycles as those. Of that time the matrix instructions alone would take 256 us,
+// with the reads from LDS 285, the loads and reads without them 235: it is their meeting. What brought them there from 600:
 // operands read one step ahead into a second set of registers
 // (with the scheduler told to spread the reads: left alone it sinks them behind all matrix instructions),
 // a swizzle that leaves the operands' reads no bank conflict (440 to 385 us), three stages rather than four (less power), the

@@ -4,7 +4,7 @@
 // This is measurement infrastructure, not part of the SpMM: the benchmark
 // reads the SpMM's roofline fraction against the vendor HBM peak, and reports
 // beside it what a plain read of the same byte count achieves per launch on
-// the same box (and what a read of >= 1 GiB achieves), so that launch ramp-up
+// the same machine (and what a read of >= 1 GiB achieves), so that launch ramp-up
 // and first-byte latency are visible as a ceiling of their own.
 //
 // Each thread reads 16-byte granules (64 lanes x 16 B = 1 KB per wavefront
